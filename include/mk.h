@@ -60,7 +60,8 @@ enum {
   MK_ERR_UNSUPPORTED = 8,   /* dims this build does not support (see mk_create) */
   MK_ERR_NO_DEVICE = 9,     /* no usable sm_103 device */
   MK_ERR_SCRATCH_LIMIT = 10,/* mk_decode_step_static: workspace larger than its static scratch */
-  MK_ERR_BAD_TOKEN = 11     /* a token id outside [0, vocab) reached the kernel (sticky) */
+  MK_ERR_BAD_TOKEN = 11,    /* a token id outside [0, vocab) reached the kernel (sticky) */
+  MK_ERR_NO_PAGES = 12      /* too few free pages (mk_cache.h) */
 };
 
 /* Model dimensions.  page_size tokens per KV page; num_pages pages in each

@@ -25,18 +25,19 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(BUILD, "libmk.so")
 
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
-SOURCES = ["mk_kernel.cu", "mk_api.cpp", "mk_schedule.cpp", "mk_noalloc.cu"]
+SOURCES = ["mk_kernel.cu", "mk_api.cpp", "mk_schedule.cpp", "mk_noalloc.cu", "mk_kv.cu"]
 
 MK_OK = 0
 STATUS_NAMES = {0: "MK_OK", 1: "MK_ERR_INVALID_ARG", 2: "MK_ERR_BATCH", 3: "MK_ERR_PAGE_OOB",
                 4: "MK_ERR_NO_SCHEDULE", 5: "MK_ERR_CUDA", 6: "MK_ERR_DEVICE_TIMEOUT",
                 7: "MK_ERR_BAD_TASK", 8: "MK_ERR_UNSUPPORTED", 9: "MK_ERR_NO_DEVICE",
-                10: "MK_ERR_SCRATCH_LIMIT", 11: "MK_ERR_BAD_TOKEN"}
+                10: "MK_ERR_SCRATCH_LIMIT", 11: "MK_ERR_BAD_TOKEN", 12: "MK_ERR_NO_PAGES"}
 MK_ERR_INVALID_ARG, MK_ERR_BATCH, MK_ERR_PAGE_OOB, MK_ERR_NO_SCHEDULE = 1, 2, 3, 4
 MK_ERR_CUDA, MK_ERR_DEVICE_TIMEOUT, MK_ERR_BAD_TASK, MK_ERR_UNSUPPORTED = 5, 6, 7, 8
 MK_ERR_NO_DEVICE = 9
 MK_ERR_SCRATCH_LIMIT = 10
 MK_ERR_BAD_TOKEN = 11
+MK_ERR_NO_PAGES = 12
 
 
 def build_commands() -> List[List[str]]:
@@ -103,10 +104,21 @@ class mk_plan_info(ctypes.Structure):
                  "n_up", "n_out", "n_lm", "n_attn_slots", "n_down")]
 
 
+class mk_kv_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_pools", "num_pages", "page_size", "n_seqs", "max_pages_per_seq")] + [
+                    ("page_bytes", ctypes.c_int64), ("pools", ctypes.POINTER(ctypes.c_void_p)),
+                    ("page_tables", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+                    ("page_refs", ctypes.c_void_p)]
+
+
 EXPORTS = ["mk_create", "mk_build_schedule", "mk_decode_step", "mk_sync", "mk_destroy",
            "mk_status_string", "mk_set_wait_limit_ns", "mk_debug_routing", "mk_debug_dump",
            "mk_get_stats", "mk_debug_poison_wait", "mk_plan", "mk_decode_step_static",
-           "mk_set_trace", "mk_get_trace", "mk_set_stage_trace_cta"]
+           "mk_set_trace", "mk_get_trace", "mk_set_stage_trace_cta",
+           "mk_kv_create", "mk_kv_destroy", "mk_kv_copy_pages", "mk_kv_fork", "mk_kv_resize",
+           "mk_kv_compact", "mk_kv_sync"]
+_NO_STATUS = ("mk_destroy", "mk_status_string", "mk_kv_destroy")
 
 _lib = None
 
@@ -141,8 +153,15 @@ def lib():
         L.mk_set_trace.argtypes = [vp, i32]
         L.mk_get_trace.argtypes = [vp, vp, u64, vp, vp]
         L.mk_set_stage_trace_cta.argtypes = [vp, i32]
+        L.mk_kv_create.argtypes = [ctypes.POINTER(mk_kv_desc), vp, ctypes.POINTER(vp)]
+        L.mk_kv_destroy.argtypes = [vp]
+        L.mk_kv_destroy.restype = None
+        for n in ("mk_kv_copy_pages", "mk_kv_fork", "mk_kv_resize"):
+            getattr(L, n).argtypes = [vp, i32, vp, vp]
+        L.mk_kv_compact.argtypes = [vp, vp]
+        L.mk_kv_sync.argtypes = [vp]
         for n in EXPORTS:
-            if n not in ("mk_destroy", "mk_status_string"):
+            if n not in _NO_STATUS:
                 getattr(L, n).restype = i32
         _lib = L
     return _lib
@@ -330,6 +349,16 @@ class Decoder:
         self.batch = len(seq_lens)
         mk_build_schedule(self.ctx, self.batch, seq_lens, page_tables)
 
+    def schedule_cache(self, cache, seqs, seq_lens=None):
+        """Schedules the sequences `seqs` (row numbers) of a KvCache over this
+        decoder's pools.  Reads their table rows back (synchronises).  seq_lens:
+        their cached tokens; None: one less than the cache's lengths, that is,
+        the cache was grown by the token of the next step."""
+        if cache.max_pages_per_seq != self.cdims.max_pages_per_seq:
+            raise ValueError("the cache's table rows have another width than this decoder's")
+        lens, tables = cache.read(seqs)
+        self.build_schedule(lens - 1 if seq_lens is None else seq_lens, tables)
+
     def decode_step(self, token_ids, out_logits, out_next_tokens):
         mk_decode_step(self.ctx, token_ids, out_logits, out_next_tokens)
 
@@ -376,3 +405,6 @@ class Decoder:
             self.close()
         except Exception:
             pass
+
+
+from .cache import KvCache  # noqa: E402  (needs the functions above)

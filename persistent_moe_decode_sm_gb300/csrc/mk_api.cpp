@@ -237,6 +237,7 @@ const char *mk_status_string(mk_status s) {
     case MK_ERR_NO_DEVICE: return "no usable sm_103 device";
     case MK_ERR_SCRATCH_LIMIT: return "workspace larger than the static scratch of mk_decode_step_static";
     case MK_ERR_BAD_TOKEN: return "token id outside the vocabulary";
+    case MK_ERR_NO_PAGES: return "too few free pages";
     default: return "unknown status";
   }
 }
