@@ -95,6 +95,74 @@ mk_status mk_kv_compact(mk_kv *kv, int32_t *page_map);
  * MK_ERR_INVALID_ARG while the stream is being captured. */
 mk_status mk_kv_sync(mk_kv *kv);
 
+/* ---- attention over shared pages -------------------------------------------
+ *
+ * A batch of sequences, each with one or more query tokens, attends to its paged
+ * K and V.  Consecutive sequences form groups; the first prefix_lens[g] tokens
+ * of a group's sequences lie in the same pages, and those pages are read once
+ * for all of the group's query tokens and heads (single tokens of 64 samples of
+ * one prompt read the prompt once instead of 64 times). */
+
+typedef struct {
+  int32_t n_q_heads, n_kv_heads, head_dim;   /* as mk_create; n_q_heads / n_kv_heads <= 64 */
+  int32_t page_size, num_pages;              /* page_size a multiple of 16, at most 256 */
+  int32_t max_tokens;                        /* query tokens of a call, at most 2^20 */
+  int32_t max_seqs, max_groups;              /* of a call, at most 1024 each */
+  int32_t n_layers;
+  const void *const *k_caches;               /* HOST arrays [n_layers] of DEVICE pools */
+  const void *const *v_caches;
+  float scale;                               /* of the scores; 0: 1 / sqrt(head_dim) */
+} mk_attn_desc;
+
+/* A call's batch.  The arrays are DEVICE memory and are read by the call on the
+ * GPU, so they can be updated between replays of a captured call. */
+typedef struct {
+  int32_t n_seqs, n_tokens;
+  int32_t n_groups;                 /* 0: no sequence shares pages */
+  int32_t max_pages_per_seq;        /* entries of a table row */
+  const int32_t *page_tables;       /* [n_seqs][max_pages_per_seq] */
+  const int32_t *seq_lens;          /* [n_seqs] cached tokens, the query tokens among them */
+  const int32_t *q_offsets;         /* [n_seqs + 1] from 0, not decreasing, the last one <=
+                                     * n_tokens: sequence b's query tokens; or NULL: one
+                                     * token each, n_tokens == n_seqs */
+  const int32_t *group_starts;      /* [n_groups + 1] from 0 to n_seqs, not decreasing */
+  const int32_t *prefix_lens;       /* [n_groups] */
+} mk_attn_batch;
+
+typedef struct mk_attn mk_attn;
+
+/* MK_ERR_INVALID_ARG / MK_ERR_UNSUPPORTED / MK_ERR_NO_DEVICE / MK_ERR_CUDA. */
+mk_status mk_attn_create(const mk_attn_desc *desc, void *stream, mk_attn **out);
+void mk_attn_destroy(mk_attn *attn);
+
+/* Attention of the batch's query tokens over layer `layer`'s pools.  With T
+ * query tokens and length L, query t of a sequence sits at position L - T + t
+ * and sees the keys at positions <= its own (K and V of the query tokens are in
+ * the cache already).  q: bf16 [n_tokens][n_q_heads][head_dim], q_token_stride
+ * elements from a token to the next (a multiple of 8; heads are contiguous);
+ * out: bf16 [n_tokens][n_q_heads][head_dim], contiguous; lse: fp32
+ * [n_tokens][n_q_heads] or NULL, the natural logarithm of the softmax sum.  Both
+ * q and out 16-byte aligned.  A token that sees no key (T > L) gets zeros and
+ * lse -inf; rows behind the last sequence's tokens are not written.
+ *
+ * Only positions below a sequence's length are read, and their K and V have to
+ * be finite; page entries and contents behind it do not matter.  Of a group's
+ * prefix the whole pages are shared, by the first sequence's table row; a
+ * shorter sequence in the group is cut off at its own length.  Softmax in fp32;
+ * the probabilities are rounded to bf16 for the product with V, and so is the
+ * result.  The same call gives the same bits.
+ *
+ * A wrong DEVICE argument (offsets, lengths or starts that are out of order or
+ * out of range: nothing is written; a page id out of range: that page's keys
+ * are undefined) is reported by mk_attn_sync, once. */
+mk_status mk_prefix_attention(mk_attn *attn, int32_t layer, const mk_attn_batch *batch,
+                              const void *q, int64_t q_token_stride, void *out, float *lse);
+
+/* Waits for the stream and returns the first device error since the last
+ * mk_attn_sync (MK_OK if none); clears it.  MK_ERR_INVALID_ARG while the stream
+ * is being captured. */
+mk_status mk_attn_sync(mk_attn *attn);
+
 #ifdef __cplusplus
 }
 #endif

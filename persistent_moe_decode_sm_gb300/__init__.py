@@ -25,7 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(BUILD, "libmk.so")
 
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
-SOURCES = ["mk_kernel.cu", "mk_api.cpp", "mk_schedule.cpp", "mk_noalloc.cu", "mk_kv.cu"]
+SOURCES = ["mk_kernel.cu", "mk_api.cpp", "mk_schedule.cpp", "mk_noalloc.cu", "mk_kv.cu",
+           "mk_attn.cu"]
 
 MK_OK = 0
 STATUS_NAMES = {0: "MK_OK", 1: "MK_ERR_INVALID_ARG", 2: "MK_ERR_BATCH", 3: "MK_ERR_PAGE_OOB",
@@ -112,13 +113,29 @@ class mk_kv_desc(ctypes.Structure):
                     ("page_refs", ctypes.c_void_p)]
 
 
+class mk_attn_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_q_heads", "n_kv_heads", "head_dim", "page_size", "num_pages",
+                 "max_tokens", "max_seqs", "max_groups", "n_layers")] + [
+                    ("k_caches", ctypes.POINTER(ctypes.c_void_p)),
+                    ("v_caches", ctypes.POINTER(ctypes.c_void_p)), ("scale", ctypes.c_float)]
+
+
+class mk_attn_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_tokens", "n_groups",
+                                              "max_pages_per_seq")] + [
+        (n, ctypes.c_void_p) for n in
+        ("page_tables", "seq_lens", "q_offsets", "group_starts", "prefix_lens")]
+
+
 EXPORTS = ["mk_create", "mk_build_schedule", "mk_decode_step", "mk_sync", "mk_destroy",
            "mk_status_string", "mk_set_wait_limit_ns", "mk_debug_routing", "mk_debug_dump",
            "mk_get_stats", "mk_debug_poison_wait", "mk_plan", "mk_decode_step_static",
            "mk_set_trace", "mk_get_trace", "mk_set_stage_trace_cta",
            "mk_kv_create", "mk_kv_destroy", "mk_kv_copy_pages", "mk_kv_fork", "mk_kv_resize",
-           "mk_kv_compact", "mk_kv_sync"]
-_NO_STATUS = ("mk_destroy", "mk_status_string", "mk_kv_destroy")
+           "mk_kv_compact", "mk_kv_sync",
+           "mk_attn_create", "mk_attn_destroy", "mk_prefix_attention", "mk_attn_sync"]
+_NO_STATUS = ("mk_destroy", "mk_status_string", "mk_kv_destroy", "mk_attn_destroy")
 
 _lib = None
 
@@ -160,6 +177,11 @@ def lib():
             getattr(L, n).argtypes = [vp, i32, vp, vp]
         L.mk_kv_compact.argtypes = [vp, vp]
         L.mk_kv_sync.argtypes = [vp]
+        L.mk_attn_create.argtypes = [ctypes.POINTER(mk_attn_desc), vp, ctypes.POINTER(vp)]
+        L.mk_attn_destroy.argtypes = [vp]
+        L.mk_attn_destroy.restype = None
+        L.mk_prefix_attention.argtypes = [vp, i32, ctypes.POINTER(mk_attn_batch), vp, i64, vp, vp]
+        L.mk_attn_sync.argtypes = [vp]
         for n in EXPORTS:
             if n not in _NO_STATUS:
                 getattr(L, n).restype = i32
@@ -407,4 +429,4 @@ class Decoder:
             pass
 
 
-from .cache import KvCache  # noqa: E402  (needs the functions above)
+from .cache import KvCache, PrefixAttention  # noqa: E402  (needs the functions above)

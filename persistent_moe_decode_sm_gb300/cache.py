@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _addr, _check, lib, mk_kv_desc
+from . import _addr, _check, lib, mk_attn_batch, mk_attn_desc, mk_kv_desc
 
 
 def _stream(stream, device):
@@ -124,6 +124,114 @@ class KvCache:
     def close(self):
         if self.handle:
             self._lib.mk_kv_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class PrefixAttention:
+    """Attention of a batch's query tokens over paged K and V, reading the pages
+    that a group of sequences shares once for all of them.
+
+    layers: (k_cache, v_cache) of each layer, contiguous bf16 [num_pages]
+    [n_kv_heads][page_size][head_dim].  max_tokens bounds a call's query tokens
+    (it sizes the workspace).  scale: of the scores, None for 1 / sqrt(head_dim)."""
+
+    def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, layers,
+                 max_tokens: int, max_seqs: int = 1024, max_groups: int = 1024,
+                 scale: float = None, stream=None):
+        import torch
+
+        layers = [tuple(kv) for kv in layers]
+        if not layers:
+            raise ValueError("no layers")
+        dev, pages = layers[0][0].device, layers[0][0].shape[0]
+        for k, v in layers:
+            for t, what in ((k, "k_cache"), (v, "v_cache")):
+                _want(t, what, "bfloat16", dev)
+                if t.numel() != pages * n_kv_heads * page_size * head_dim:
+                    raise ValueError(f"{what} is not [{pages}][{n_kv_heads}][{page_size}]"
+                                     f"[{head_dim}]")
+        if dev.type != "cuda":
+            raise ValueError("the caches have to be CUDA tensors")
+        if scale is not None and not scale > 0.0:
+            raise ValueError("scale has to be positive")
+        self.handle = None
+        self.device, self.layers, self.max_tokens = dev, layers, max_tokens
+        self.heads, self.head_dim = n_q_heads, head_dim
+        self._lib = lib()
+        n = len(layers)
+        ks = (ctypes.c_void_p * n)(*[k.data_ptr() for k, _ in layers])
+        vs = (ctypes.c_void_p * n)(*[v.data_ptr() for _, v in layers])
+        desc = mk_attn_desc(n_q_heads, n_kv_heads, head_dim, page_size, pages, max_tokens,
+                            max_seqs, max_groups, n, ks, vs, scale or 0.0)
+        h = ctypes.c_void_p()
+        with torch.cuda.device(dev):
+            _check(self._lib.mk_attn_create(ctypes.byref(desc), _stream(stream, dev),
+                                            ctypes.byref(h)), "mk_attn_create")
+        self.handle = h.value
+
+    def batch(self, page_tables, seq_lens, q_offsets=None, group_starts=None, prefix_lens=None,
+              n_tokens: int = None):
+        """The batch of a call, to be kept as long as its tensors stay in place (their
+        contents may change between calls).  q_offsets None: one query token each.
+        n_tokens: rows of q and out; None: with q_offsets max_tokens, else one each."""
+        _want(page_tables, "page_tables", "int32", self.device, 2)
+        _want(seq_lens, "seq_lens", "int32", self.device, 1)
+        n = seq_lens.numel()
+        if page_tables.shape[0] != n:
+            raise ValueError("seq_lens has an entry for each table row")
+        if (group_starts is None) != (prefix_lens is None):
+            raise ValueError("group_starts and prefix_lens come together")
+        groups = 0
+        if group_starts is not None:
+            _want(group_starts, "group_starts", "int32", self.device, 1)
+            _want(prefix_lens, "prefix_lens", "int32", self.device, 1)
+            groups = prefix_lens.numel()
+            if group_starts.numel() != groups + 1:
+                raise ValueError("group_starts has one entry more than prefix_lens")
+        if q_offsets is not None:
+            _want(q_offsets, "q_offsets", "int32", self.device, 1)
+            if q_offsets.numel() != n + 1:
+                raise ValueError("q_offsets has one entry more than there are sequences")
+        if n_tokens is None:
+            n_tokens = n if q_offsets is None else self.max_tokens
+        b = mk_attn_batch(n, n_tokens, groups, page_tables.shape[1], page_tables.data_ptr(), seq_lens.data_ptr(),
+                          _addr(q_offsets), _addr(group_starts), _addr(prefix_lens))
+        b.keep = (page_tables, seq_lens, q_offsets, group_starts, prefix_lens)
+        return b
+
+    def run(self, layer: int, batch, q, out, lse=None):
+        """out [n_tokens][n_q_heads][head_dim] = attention of q over the layer's pools;
+        lse (fp32 [n_tokens][n_q_heads]) receives the logarithm of the softmax sums.  q may
+        have a token stride of its own (the q part of a fused projection)."""
+        rows = (batch.n_tokens, self.heads, self.head_dim)
+        if (q.shape != rows or q.dtype != self.layers[0][0].dtype or q.device != self.device
+                or q.stride(2) != 1 or q.stride(1) != self.head_dim):
+            raise ValueError(f"q has to be bfloat16 {rows} with contiguous heads on {self.device}")
+        _want(out, "out", "bfloat16", self.device)
+        if out.shape != rows:
+            raise ValueError(f"out has to be {rows}")
+        if lse is not None:
+            _want(lse, "lse", "float32", self.device)
+            if lse.shape != rows[:2]:
+                raise ValueError(f"lse has to be {rows[:2]}")
+        _check(self._lib.mk_prefix_attention(
+            self.handle, layer, ctypes.byref(batch), q.data_ptr(),
+            q.stride(0) if rows[0] > 1 else self.heads * self.head_dim, out.data_ptr(),
+            None if lse is None else lse.data_ptr()), "mk_prefix_attention")
+
+    def sync(self):
+        """Waits for the stream; raises the MkError of the first device error."""
+        _check(self._lib.mk_attn_sync(self.handle), "mk_attn_sync")
+
+    def close(self):
+        if self.handle:
+            self._lib.mk_attn_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
