@@ -146,9 +146,11 @@ void mk_attn_destroy(mk_attn *attn);
  * lse -inf; rows behind the last sequence's tokens are not written.
  *
  * Only positions below a sequence's length are read, and their K and V have to
- * be finite; page entries and contents behind it do not matter.  Of a group's
- * prefix the whole pages are shared, by the first sequence's table row; a
- * shorter sequence in the group is cut off at its own length.  Softmax in fp32;
+ * be finite; page entries and contents behind it do not matter.  A sequence of
+ * length 0 or without query tokens reads nothing.  What the others of a group
+ * share is read through the first one's table row: the whole pages of the
+ * prefix, as far as the shortest of them fills them.  Their rows have to name
+ * the same pages there.  Softmax in fp32;
  * the probabilities are rounded to bf16 for the product with V, and so is the
  * result.  The same call gives the same bits.
  *

@@ -221,6 +221,24 @@ mk_status mk_encode_wd_maps(const mk_model_dims *dm, const void *const *w_down, 
   return MK_OK;
 }
 
+mk_status mk_encode_rows_map(const mk_attn_desc *d, const void *pool, int box_rows,
+                             void *host_out) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return MK_ERR_CUDA;
+  const int cols = mk_box_inner(d->head_dim);
+  const cuuint64_t dims[2] = {(cuuint64_t)d->head_dim,
+                              (cuuint64_t)d->num_pages * d->n_kv_heads * d->page_size};
+  const cuuint64_t strides[1] = {(cuuint64_t)d->head_dim * 2};
+  const cuuint32_t box[2] = {(cuuint32_t)cols, (cuuint32_t)box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  if (enc((CUtensorMap *)host_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(pool),
+          dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          cols < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return MK_ERR_INVALID_ARG;
+  return MK_OK;
+}
+
 extern "C" {
 
 const char *mk_status_string(mk_status s) {

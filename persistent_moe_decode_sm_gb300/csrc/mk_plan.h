@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "mk.h"
+#include "mk_cache.h"
 
 struct MkPlan {
   int n_cta = 0, tasks_per_cta = 0, n_layer_tasks_max = 0, batch = 0;
@@ -47,6 +48,11 @@ mk_status mk_encode_wd_maps(const mk_model_dims *d, const void *const *w_down, i
 /* Rows of d per down box for the batch-1 ring stages (a multiple of 8, at
  * most 256). */
 int mk_fold_rows(const mk_model_dims *d);
+
+/* Encodes a 2-D TMA tensor map (128 bytes) over a K or V pool viewed as
+ * [num_pages * n_kv_heads * page_size rows][head_dim]: box {min(head_dim, 64)
+ * columns, box_rows rows}, swizzled over the box's row (64 or 128 bytes). */
+mk_status mk_encode_rows_map(const mk_attn_desc *d, const void *pool, int box_rows, void *host_out);
 
 mk_status mk_validate_dims(const mk_model_dims *d);
 /* u_seen > 0: the distinct experts per layer observed at this batch size,

@@ -213,6 +213,19 @@ def test_shorter_sequences_than_the_prefix_says():
 
 
 @gpu
+def test_finished_sequences_inside_a_group():
+    """Rows of length 0 with no pages, first in the group and within it."""
+    c = Case([(64, [(10, 1), (7, 1), (33, 1), (9, 1)])], (4, 2, 64))
+    for b in (0, 2):
+        c.lens[b] = 0
+        c.tables[b] = -1
+    c.check()
+    c = Case([(64, [(10, 0), (7, 3), (33, 0), (9, 2)])], (4, 2, 64))
+    c.tables[0] = -1                       # no query tokens: not read
+    c.check()
+
+
+@gpu
 def test_groups_change_nothing_but_the_order_of_sums():
     c = Case([(333, [(9, 1), (100, 1), (17, 1)]), (64, [(1, 1)]), (0, [(5, 1), (6, 1)])], (16, 2, 64))
     want = c.exact()
