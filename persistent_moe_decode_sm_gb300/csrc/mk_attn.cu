@@ -171,32 +171,43 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       : "memory");
 }
 #define R8(x, i) x(i), x(i + 1), x(i + 2), x(i + 3), x(i + 4), x(i + 5), x(i + 6), x(i + 7)
-#define R32(x) R8(x, 0), R8(x, 8), R8(x, 16), R8(x, 24)
-/* 32 columns of this thread's TMEM lane; values may be used behind tmem_landed. */
+#define R32(x, i) R8(x, i), R8(x, i + 8), R8(x, i + 16), R8(x, i + 24)
+/* 32 or 128 columns of this thread's TMEM lane.  The load and its wait are one
+ * statement: between two, the compiler could move registers that have not landed. */
 __device__ __forceinline__ void tmem_ld32(uint32_t at, float *v) {
 #define OUT(i) "=f"(v[i])
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31}, [%32];"
-      : R32(OUT)
-      : "r"(at));
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R32(OUT, 0)
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld128(uint32_t at, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x128.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63, "
+      "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+      "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95, "
+      "%96, %97, %98, %99, %100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, %111, "
+      "%112, %113, %114, %115, %116, %117, %118, %119, %120, %121, %122, %123, %124, %125, %126, %127}, [%128];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R32(OUT, 0), R32(OUT, 32), R32(OUT, 64), R32(OUT, 96)
+      : "r"(at)
+      : "memory");
 #undef OUT
-}
-__device__ __forceinline__ void tmem_wait_ld() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_landed(float *v) {
-#define IO(i) "+f"(v[i])
-  asm volatile("" : R32(IO));
-#undef IO
 }
 __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *v) {
 #define IN(i) "r"(v[i])
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
       "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-      "%29, %30, %31};" ::R32(IN),
+      "%29, %30, %31};" ::R32(IN, 0),
       "r"(at)
       : "memory");
 #undef IN
@@ -639,11 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (busy) {
             float x[kTile];
-#pragma unroll
-            for (int i = 0; i < kTile; i += 32) tmem_ld32(at_s + i, x + i);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < kTile; i += 32) tmem_landed(x + i);
+            tmem_ld128(at_s, x);
             if (!__all_sync(0xffffffffu, limit >= k0 + kTile)) {
 #pragma unroll
               for (int i = 0; i < kTile; ++i) x[i] = k0 + i < limit ? x[i] : -INFINITY;
@@ -664,8 +671,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < D; i += 32) {
                   float o[32];
                   tmem_ld32(at_o + i, o);
-                  tmem_wait_ld();
-                  tmem_landed(o);
                   uint32_t w[32];
 #pragma unroll
                   for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(o[k] * f);
@@ -724,8 +729,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < D; i += 32) {
               float o[32];
               tmem_ld32(at_o + i, o);
-              tmem_wait_ld();
-              tmem_landed(o);
 #pragma unroll
               for (int k = 0; k < 32; ++k) xo[(i + k) * kTile + r] = o[k];
             }
@@ -761,8 +764,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < D; i += 32) {
               float o[32];
               tmem_ld32(at_o + i, o);
-              tmem_wait_ld();
-              tmem_landed(o);
               if (joins) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k) o[k] = o[k] * f0 + xo[(i + k) * kTile + r] * f1;
@@ -790,8 +791,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (joins) {
+            /* no warp of either stream writes Q again before all have read */
             __syncwarp();
             if (lane == 0) bar_arrive(&sm->xfree);
+            ok = warp_wait(&sm->xfree, (nx - 1) & 1, abort);
+            if (!ok) break;
           }
         }
         tc_fence_before();
