@@ -3,22 +3,23 @@
  * sequences share (include/mk_cache.h).
  *
  * The work is cut into tiles of 128 keys.  An item is a range of keys that a
- * set of query rows reads: a group's shared pages with all rows (query tokens x
- * heads of one kv head) of the group's sequences, 256 rows at a time, or one
- * sequence's own pages with that sequence's rows.  All items' tiles lie end to
- * end on one line, cut evenly over the SMs, so a CTA's share may begin and end
- * inside an item; every piece leaves a partial (maximum, sum, weighted sum) per
- * row, and attn_merge joins them.  The cut follows from the lengths on the
- * device: each CTA takes it itself, so that a captured call follows its batch.
+ * set of query rows reads: a group's shared pages with the rows (query tokens x
+ * heads of one kv head) of the group's sequences, or one sequence's own pages
+ * with that sequence's rows.  Items of more than 128 rows (up to 256: pairs) and
+ * items of at most 128 rows (singles) lie end to end on a line each, and each
+ * line is cut evenly, the pairs over the SMs and the singles over twice as many
+ * streams.  A share may begin and end inside an item; every piece leaves a
+ * partial (maximum, sum, weighted sum) per row, and attn_merge joins them.  The
+ * cut follows from the lengths on the device: each CTA takes it itself, so that
+ * a captured call follows its batch.
  *
- * attn_tiles, one CTA per SM: a producer warp moves K and V tiles with TMA, one
- * box per page and 64 dims, into swizzled shared memory; one thread issues
- * S = Q K^T and O += P V on the tensor cores (tcgen05, 128 rows, accumulators in
- * TMEM); two warpgroups turn S into P, one row a thread, P going back to TMEM
- * as the A operand.  The two work on their own S, P and O, so that one's
- * softmax runs under the other's products: on two tiles of rows over the same
- * keys where an item has more than 128 rows, else on the even and odd key tiles
- * of the same rows, joined at the piece's end.
+ * attn_tiles, one CTA per SM: producer warps move K and V tiles with TMA, one box
+ * per page and 64 dims, into swizzled shared memory; one thread issues S = Q K^T
+ * and O += P V on the tensor cores (tcgen05, 128 rows, accumulators in TMEM); two
+ * warpgroups, the streams, turn S into P, one row a thread, P going back to TMEM
+ * as the A operand.  A pair's two row tiles run on the two streams over the same
+ * K and V; of the singles each stream has its own share.  Either way one stream's
+ * softmax, and its piece's beginning and end, run under the other's products.
  */
 #include <cuda.h> /* tensor-map types; the encoder is reached through the runtime */
 #include <cuda_bf16.h>
@@ -35,14 +36,17 @@
 
 namespace {
 
-constexpr int kThreads = 320;      /* 8 softmax warps, the producer, the issuer */
+constexpr int kThreads = 384;      /* two softmax warpgroups; two producers, the issuer */
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88; /* 256 * 208 + 128 * 88 = 384 * 168 */
 constexpr int kTile = 128;         /* keys per tile; rows per row tile */
+constexpr int kItemCost = 2;       /* what an item's beginning and end cost, in tiles */
 constexpr int kMaxSeqs = 1024;     /* of a call: the cut's tables are in shared memory */
 constexpr uint64_t kWaitLimit = 2000000000ull; /* ns */
 /* The running maximum moves only when a score exceeds it by this much (in powers
  * of two): P then stays below 2^8, exact in its relative precision, and the
  * accumulator is rescaled a few times per row rather than in most tiles. */
 constexpr float kSlack = 8.0f;
+constexpr int kSchedStride = kMaxSeqs + 1;
 
 struct Args {
   int32_t Hq, Hkv, G, P, num_pages, max_pages, n_seqs, n_tokens, n_groups, box_rows;
@@ -54,10 +58,10 @@ struct Args {
   float scale_log2; /* scale * log2(e) */
   int32_t *err_host;
   /* workspace */
-  int32_t *sched;    /* the cut, for attn_merge: [0] bad, [1] groups' units, [2] all units, then
-                      * [kMaxSeqs + 1] each: cumulated units of the groups, of the sequences,
-                      * the groups' shared keys */
-  float *part;       /* [2 * n_tokens * Hq + grid * 256][D] weighted sums */
+  int32_t *sched;    /* the cut, for attn_merge: [0] bad, [1] [2] the lines' lengths, then
+                      * kSchedStride each: the groups' and the sequences' beginnings on the
+                      * pairs' line, on the singles' line, the groups' shared keys */
+  float *part;       /* [2 * n_tokens * Hq + 4 * SMs * 128][D] weighted sums */
   float2 *part_ml;   /* the same rows: maximum (in powers of two), sum */
 };
 
@@ -75,14 +79,16 @@ struct Cfg {
 
 struct Smem { /* behind the tiles */
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
-  uint64_t sfull[2], pready[2], qready[2], oready[2], xfull, xfree, drain;
+  uint64_t sfull[2], pready[2], qready[2], oready[2], drain;
   uint32_t tmem;
   int abort;
-  int sums[kThreads / 32];
-  int total_g, total;
-  float xm[kTile], xl[kTile];
-  int32_t off[kMaxSeqs + 1], len[kMaxSeqs], start[kMaxSeqs], cum_s[kMaxSeqs + 1];
-  int32_t gs[kMaxSeqs + 1], plen[kMaxSeqs], lead[kMaxSeqs], cum_g[kMaxSeqs + 1];
+  int piece_tiles[2]; /* from a stream to the issuer with Q: tiles of a single piece, 0: no more */
+  unsigned long long sums[kThreads / 32];
+  int total[2];       /* length of the pairs' line, of the singles' */
+  int32_t off[kMaxSeqs + 1], len[kMaxSeqs];
+  int32_t cum_g[2][kMaxSeqs + 1], cum_s[2][kMaxSeqs + 1]; /* beginnings on the two lines */
+  int32_t plen[kMaxSeqs];
+  uint16_t gs[kMaxSeqs + 1], lead[kMaxSeqs]; /* a group's first sequence, its first that reads */
 };
 
 /* ---- PTX -------------------------------------------------------------------- */
@@ -130,6 +136,16 @@ __device__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
     }
   }
 }
+__device__ __forceinline__ bool bar_test(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(saddr(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
   return __all_sync(0xffffffffu, bar_wait(b, parity, abort));
 }
@@ -172,7 +188,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 #define R8(x, i) x(i), x(i + 1), x(i + 2), x(i + 3), x(i + 4), x(i + 5), x(i + 6), x(i + 7)
 #define R32(x, i) R8(x, i), R8(x, i + 8), R8(x, i + 16), R8(x, i + 24)
-/* 32 or 128 columns of this thread's TMEM lane.  The load and its wait are one
+/* 16, 32 or 128 columns of this thread's TMEM lane.  The load and its wait are one
  * statement: between two, the compiler could move registers that have not landed. */
 __device__ __forceinline__ void tmem_ld32(uint32_t at, float *v) {
 #define OUT(i) "=f"(v[i])
@@ -182,6 +198,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float *v) {
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
       "tcgen05.wait::ld.sync.aligned;"
       : R32(OUT, 0)
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t at, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R8(OUT, 0), R8(OUT, 8)
       : "r"(at)
       : "memory");
 }
@@ -241,21 +266,35 @@ __host__ __device__ constexpr uint32_t inst_desc(int n, bool b_n_major) {
 
 __host__ __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
 
-/* Tiles of block j (BT query tokens) of a sequence's own keys. */
-__device__ __forceinline__ int own_tiles(int len, int T, int start, int BT, int j) {
-  const int seen = min(len, len - T + min(T, (j + 1) * BT)); /* keys the block's last token sees */
-  return seen > start ? div_up(seen - start, kTile) : 0;
+/* Query tokens come in blocks of two row tiles.  T tokens: this many blocks have
+ * more than one row tile (pairs); a last one may have one (a single). */
+__device__ __forceinline__ int pair_blocks(int T, int TB) {
+  return T / (2 * TB) + (T % (2 * TB) > TB);
 }
-/* The CTA that owns unit u of `total` cut over n CTAs: CTA c owns [c total / n, (c + 1) total / n). */
-__device__ __forceinline__ int cta_of(int u, int total, int n) {
-  return (int)((((long long)u + 1) * n - 1) / total);
+__device__ __forceinline__ bool has_single(int T, int TB) {
+  const int r = T % (2 * TB);
+  return r > 0 && r <= TB;
+}
+/* Keys that the last token of block j of a sequence sees. */
+__device__ __forceinline__ int block_end(int len, int T, int TB, int j) {
+  return min(len, len - T + min(T, (j + 1) * 2 * TB));
+}
+__device__ __forceinline__ int key_tiles(int begin, int end) {
+  return end > begin ? div_up(end - begin, kTile) : 0;
+}
+__device__ __forceinline__ int item_cost(int tiles) { return tiles ? tiles + kItemCost : 0; }
+/* The worker that owns place x of a line cut over n: worker w owns
+ * [w total / n, (w + 1) total / n). */
+__device__ __forceinline__ int worker_of(int x, int total, int n) {
+  return (int)((((long long)x + 1) * n - 1) / total);
 }
 /* Last i in [0, n) with a[i] <= x (a not decreasing, a[0] <= x). */
-__device__ __forceinline__ int find(const int32_t *a, int n, int x) {
+template <class T>
+__device__ __forceinline__ int find(const T *a, int n, int x) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int m = (lo + hi + 1) >> 1;
-    if (a[m] <= x)
+    if ((int)a[m] <= x)
       lo = m;
     else
       hi = m - 1;
@@ -263,17 +302,18 @@ __device__ __forceinline__ int find(const int32_t *a, int n, int x) {
   return lo;
 }
 
-__device__ int cta_scan(int v, Smem *sm, int *total) { /* exclusive */
+/* Exclusive prefix sums over the CTA, two 32-bit counts in one word. */
+__device__ unsigned long long cta_scan(unsigned long long v, Smem *sm, unsigned long long *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  unsigned long long x = v;
 #pragma unroll
   for (int o = 1; o < 32; o *= 2) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
   if (lane == 31) sm->sums[warp] = x;
   __syncthreads();
-  int before = 0, all = 0;
+  unsigned long long before = 0, all = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w < warp) before += sm->sums[w];
@@ -283,147 +323,226 @@ __device__ int cta_scan(int v, Smem *sm, int *total) { /* exclusive */
   __syncthreads();
   return before + x - v;
 }
+__device__ __forceinline__ unsigned long long two(int pairs, int singles) {
+  return (unsigned long long)(unsigned)pairs << 32 | (unsigned)singles;
+}
 
 /* Loads and checks the batch and cuts it.  False (for the whole CTA, and every
  * CTA alike) if it is not sound. */
 __device__ bool take_cut(const Args &a, Smem *sm) {
-  const int tid = threadIdx.x;
-  const int BT = 2 * (kTile / a.G);
+  constexpr int N = (kMaxSeqs + kThreads) / kThreads; /* entries a thread: all loads at once */
+  const int tid = threadIdx.x, TB = kTile / a.G;
+  const int ns = a.n_seqs, ng = a.n_groups;
   const long long cap = (long long)a.max_pages * a.P;
   bool bad = false;
-  for (int i = tid; i <= a.n_seqs; i += kThreads) sm->off[i] = a.off ? a.off[i] : i;
-  for (int i = tid; i < a.n_seqs; i += kThreads) {
-    const int l = a.lens[i];
-    bad |= l < 0 || l > cap;
-    sm->len[i] = l;
-  }
-  for (int i = tid; i <= a.n_groups; i += kThreads) {
-    sm->gs[i] = a.n_groups ? a.starts[i] : 0;
-    if (i < a.n_groups) {
-      const int l = a.prefix[i];
-      bad |= l < 0;
-      sm->plen[i] = l;
-      sm->lead[i] = a.n_seqs;
+  {
+    int l[N], o[N], g[N], p[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = tid + k * kThreads;
+      l[k] = i < ns ? a.lens[i] : 0;
+      o[k] = !a.off ? i : i <= ns ? a.off[i] : 0;
+      g[k] = i <= ng && ng ? a.starts[i] : 0;
+      p[k] = i < ng ? a.prefix[i] : 0;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = tid + k * kThreads;
+      bad |= l[k] < 0 || l[k] > cap || p[k] < 0 || g[k] < 0 || g[k] > ns;
+      if (i < ns) sm->len[i] = l[k];
+      if (i <= ns) sm->off[i] = o[k];
+      if (i <= ng) sm->gs[i] = (uint16_t)g[k];
+      if (i < ng) {
+        sm->plen[i] = p[k];
+        sm->lead[i] = (uint16_t)ns;
+      }
     }
   }
   __syncthreads();
-  for (int i = tid; i < a.n_seqs; i += kThreads) bad |= sm->off[i + 1] < sm->off[i];
-  if (tid == 0) bad |= sm->off[0] != 0 || sm->off[a.n_seqs] > a.n_tokens;
-  for (int i = tid; i < a.n_groups; i += kThreads) bad |= sm->gs[i + 1] < sm->gs[i];
-  if (tid == 0 && a.n_groups) bad |= sm->gs[0] != 0 || sm->gs[a.n_groups] != a.n_seqs;
+  for (int i = tid; i < ns; i += kThreads) bad |= sm->off[i + 1] < sm->off[i];
+  for (int i = tid; i < ng; i += kThreads) bad |= sm->gs[i + 1] < sm->gs[i];
+  if (tid == 0)
+    bad |= sm->off[0] != 0 || sm->off[ns] > a.n_tokens || (ng && (sm->gs[0] != 0 || sm->gs[ng] != ns));
   if (__syncthreads_or(bad)) return false;
   /* shared keys: whole pages that every sequence with something to read has; a
    * group of one reads them with its own */
-  if (a.n_groups) {
-    for (int i = tid; i < a.n_seqs; i += kThreads)
+  if (ng) {
+    for (int i = tid; i < ns; i += kThreads)
       if (sm->len[i] > 0 && sm->off[i + 1] > sm->off[i]) {
-        const int g = find(sm->gs, a.n_groups + 1, i);
+        const int g = find(sm->gs, ng + 1, i);
         atomicMin(&sm->plen[g], sm->len[i]);
-        atomicMin(&sm->lead[g], i);
+        /* the first that reads: the lowest index behind which none of the group reads */
+        bool first = true;
+        for (int j = sm->gs[g]; first && j < i; ++j)
+          first = !(sm->len[j] > 0 && sm->off[j + 1] > sm->off[j]);
+        if (first) sm->lead[g] = (uint16_t)i;
       }
     __syncthreads();
-    for (int i = tid; i < a.n_groups; i += kThreads)
-      sm->plen[i] = sm->gs[i + 1] - sm->lead[i] < 2 ? 0 : sm->plen[i] / a.P * a.P;
+    for (int i = tid; i < ng; i += kThreads)
+      sm->plen[i] = (int)sm->gs[i + 1] - sm->lead[i] < 2 ? 0 : sm->plen[i] / a.P * a.P;
+    __syncthreads();
   }
-  __syncthreads();
-  int base = 0;
-  for (int i0 = 0; i0 < a.n_groups; i0 += kThreads) {
+  unsigned long long base = 0;
+  for (int i0 = 0; i0 < ng; i0 += kThreads) {
     const int i = i0 + tid;
-    int units = 0;
-    if (i < a.n_groups) {
-      const int tokens = sm->off[sm->gs[i + 1]] - sm->off[sm->gs[i]];
-      units = a.Hkv * div_up(tokens, BT) * div_up(sm->plen[i], kTile);
+    unsigned long long cost = 0;
+    if (i < ng) {
+      const int T = sm->off[sm->gs[i + 1]] - sm->off[sm->gs[i]];
+      const int c = a.Hkv * item_cost(key_tiles(0, sm->plen[i]));
+      cost = two(pair_blocks(T, TB) * c, has_single(T, TB) ? c : 0);
     }
-    int total;
-    const int at = cta_scan(units, sm, &total);
-    if (i < a.n_groups) sm->cum_g[i] = base + at;
-    base += total;
-  }
-  const int total_g = base;
-  for (int i0 = 0; i0 < a.n_seqs; i0 += kThreads) {
-    const int i = i0 + tid;
-    int units = 0;
-    if (i < a.n_seqs) {
-      const int T = sm->off[i + 1] - sm->off[i];
-      const int start = a.n_groups ? sm->plen[find(sm->gs, a.n_groups + 1, i)] : 0;
-      sm->start[i] = start;
-      for (int j = 0; j * BT < T; ++j) units += own_tiles(sm->len[i], T, start, BT, j);
-      units *= a.Hkv;
+    unsigned long long total;
+    const unsigned long long at = base + cta_scan(cost, sm, &total);
+    if (i < ng) {
+      sm->cum_g[0][i] = (int)(at >> 32);
+      sm->cum_g[1][i] = (int)at;
     }
-    int total;
-    const int at = cta_scan(units, sm, &total);
-    if (i < a.n_seqs) sm->cum_s[i] = base + at;
     base += total;
   }
   if (tid == 0) {
-    sm->cum_g[a.n_groups] = total_g;
-    sm->cum_s[a.n_seqs] = base;
-    sm->total_g = total_g;
-    sm->total = base;
+    sm->cum_g[0][ng] = (int)(base >> 32);
+    sm->cum_g[1][ng] = (int)base;
+  }
+  for (int i0 = 0; i0 < ns; i0 += kThreads) {
+    const int i = i0 + tid;
+    unsigned long long cost = 0;
+    if (i < ns) {
+      const int T = sm->off[i + 1] - sm->off[i], len = sm->len[i];
+      const int start = ng ? sm->plen[find(sm->gs, ng + 1, i)] : 0, nb = pair_blocks(T, TB);
+      int pairs = 0, singles = 0;
+      for (int j = 0; j < nb; ++j) pairs += item_cost(key_tiles(start, block_end(len, T, TB, j)));
+      if (has_single(T, TB)) singles = item_cost(key_tiles(start, block_end(len, T, TB, nb)));
+      cost = two(pairs * a.Hkv, singles * a.Hkv);
+    }
+    unsigned long long total;
+    const unsigned long long at = base + cta_scan(cost, sm, &total);
+    if (i < ns) {
+      sm->cum_s[0][i] = (int)(at >> 32);
+      sm->cum_s[1][i] = (int)at;
+    }
+    base += total;
+  }
+  if (tid == 0) {
+    sm->cum_s[0][ns] = sm->total[0] = (int)(base >> 32);
+    sm->cum_s[1][ns] = sm->total[1] = (int)base;
   }
   __syncthreads();
   return true;
 }
 
-/* One CTA's part of an item. */
+/* One worker's part of an item. */
 struct Piece {
   int own;             /* 1: a sequence's own keys, 0: a group's shared ones */
   int seq;             /* whose table row names the pages */
   int kvh, tok0, ntok; /* query tokens of the item */
   int key0, kend;      /* the item's keys */
-  int t0, t1, nt;      /* tiles of this piece, of the item */
+  int t0, n, nt;       /* first tile and tiles of this piece, tiles of the item */
 };
 
-__device__ Piece piece_at(const Args &a, const Smem *sm, int u, int u1) {
-  const int BT = 2 * (kTile / a.G);
+/* The piece at place x of a line, x < end; x moves behind it.  A share that ends
+ * within an item's fixed cost has no tile of it: n is 0. */
+__device__ Piece next_piece(const Args &a, const Smem *sm, int line, int &x, int end) {
+  const int TB = kTile / a.G;
   Piece p;
-  int j, r;
-  if (u < sm->total_g) {
-    const int g = find(sm->cum_g, a.n_groups, u);
+  int j, begin; /* the item's block, its place */
+  if (x < sm->cum_g[line][a.n_groups]) {
+    const int g = find(sm->cum_g[line], a.n_groups, x);
+    const int first = sm->off[sm->gs[g]], T = sm->off[sm->gs[g + 1]] - first;
     p.own = 0;
     p.seq = sm->lead[g];
-    const int end = sm->off[sm->gs[g + 1]], first = sm->off[sm->gs[g]], n = div_up(end - first, BT);
-    p.nt = div_up(sm->plen[g], kTile);
-    r = u - sm->cum_g[g];
-    const int item = r / p.nt;
-    r -= item * p.nt;
-    p.kvh = item / n;
-    j = item - p.kvh * n;
-    p.tok0 = first + j * BT;
-    p.ntok = min(BT, end - p.tok0);
     p.key0 = 0;
     p.kend = sm->plen[g];
+    p.nt = key_tiles(0, p.kend);
+    const int nb = pair_blocks(T, TB), per = line == 0 ? nb : 1, cost = item_cost(p.nt);
+    const int item = (x - sm->cum_g[line][g]) / cost;
+    begin = sm->cum_g[line][g] + item * cost;
+    p.kvh = item / per;
+    j = line == 0 ? item - p.kvh * per : nb;
+    p.tok0 = first + j * 2 * TB;
+    p.ntok = min(2 * TB, T - j * 2 * TB);
   } else {
-    const int b = find(sm->cum_s, a.n_seqs, u);
+    const int b = find(sm->cum_s[line], a.n_seqs, x);
+    const int T = sm->off[b + 1] - sm->off[b], len = sm->len[b];
     p.own = 1;
     p.seq = b;
-    const int T = sm->off[b + 1] - sm->off[b], len = sm->len[b], start = sm->start[b];
-    const int per = (sm->cum_s[b + 1] - sm->cum_s[b]) / a.Hkv;
-    r = u - sm->cum_s[b];
-    p.kvh = r / per;
-    r -= p.kvh * per;
-    for (j = 0;; ++j) {
-      p.nt = own_tiles(len, T, start, BT, j);
-      if (r < p.nt) break;
-      r -= p.nt;
+    p.key0 = a.n_groups ? sm->plen[find(sm->gs, a.n_groups + 1, b)] : 0;
+    const int per = (sm->cum_s[line][b + 1] - sm->cum_s[line][b]) / a.Hkv;
+    p.kvh = (x - sm->cum_s[line][b]) / per;
+    begin = sm->cum_s[line][b] + p.kvh * per;
+    for (j = line == 0 ? 0 : pair_blocks(T, TB);; ++j) {
+      p.kend = block_end(len, T, TB, j);
+      p.nt = key_tiles(p.key0, p.kend);
+      const int cost = item_cost(p.nt);
+      if (x < begin + cost) break;
+      begin += cost;
     }
-    p.tok0 = sm->off[b] + j * BT;
-    p.ntok = min(BT, T - j * BT);
-    p.key0 = start;
-    p.kend = min(len, len - T + min(T, (j + 1) * BT));
+    p.tok0 = sm->off[b] + j * 2 * TB;
+    p.ntok = min(2 * TB, T - j * 2 * TB);
   }
-  p.t0 = r;
-  p.t1 = min(p.nt, r + (u1 - u));
+  p.t0 = max(0, x - begin - kItemCost);
+  p.n = max(0, min(p.nt, end - begin - kItemCost) - p.t0);
+  x = min(end, begin + item_cost(p.nt));
+  return p;
+}
+/* The next piece with tiles; n is 0 at the share's end. */
+__device__ Piece next_tiles(const Args &a, const Smem *sm, int line, int &x, int end) {
+  Piece p;
+  p.n = 0;
+  while (x < end) {
+    p = next_piece(a, sm, line, x, end);
+    if (p.n) break;
+  }
   return p;
 }
 
 /* ---- the tiles ---------------------------------------------------------------- */
+
+/* Loads tile t of a piece (or nothing of it behind the last key): one box a lane. */
+template <int D>
+struct Loader {
+  using C = Cfg<D>;
+  const Args &a;
+  int box, half, page;
+  __device__ Loader(const Args &a_, int lane) : a(a_) {
+    const int boxes = kTile / a.box_rows;
+    box = lane % boxes;
+    half = lane / boxes;
+    page = -1;
+  }
+  __device__ __forceinline__ int key(const Piece &p, int t) const {
+    return p.key0 + (p.t0 + t) * kTile + box * a.box_rows;
+  }
+  /* the page of this lane's box of tile t; -1: no box */
+  __device__ __forceinline__ void look_up(const Piece &p, int t) {
+    const int k = key(p, t);
+    page = -1;
+    if (t < p.n && half < C::NH && k < p.kend)
+      page = __ldg(a.tables + (size_t)p.seq * a.max_pages + k / a.P);
+  }
+  __device__ __forceinline__ void load(const Piece &p, int t, int pg, const CUtensorMap *map,
+                                       uint8_t *tile, uint64_t *full, int lane) {
+    const int k = key(p, t);
+    bool mine = half < C::NH && k < p.kend;
+    if (mine && (unsigned)pg >= (unsigned)a.num_pages) {
+      mine = false;
+      *(volatile int32_t *)a.err_host = MK_ERR_PAGE_OOB;
+    }
+    const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+    const uint32_t bytes = a.box_rows * C::ROWB;
+    if (lane == 0) bar_expect(full, boxes * bytes);
+    __syncwarp();
+    if (mine)
+      tma_2d(saddr(tile + half * C::BLOCK + box * bytes), map, half * C::COLS,
+             (pg * a.Hkv + p.kvh) * a.P + k % a.P, full);
+  }
+};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                const __grid_constant__ Args a) {
   using C = Cfg<D>;
+  constexpr int R = C::STAGES / 2; /* K (and V) slots of a stream; pairs use all of both */
   extern __shared__ uint8_t raw[];
   uint8_t *base = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   uint8_t *qs = base, *ks = qs + 2 * C::TILE, *vs = ks + C::STAGES * C::TILE;
@@ -443,38 +562,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&sm->qready[s], 4);
       bar_init(&sm->oready[s], 1);
     }
-    bar_init(&sm->xfull, 4);
-    bar_init(&sm->xfree, 4);
     bar_init(&sm->drain, 1);
     sm->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const bool sound = take_cut(a, sm);
-  if (blockIdx.x == 0) {
-    if (tid == 0) {
-      a.sched[0] = !sound;
-      a.sched[1] = sound ? sm->total_g : 0;
-      a.sched[2] = sound ? sm->total : 0;
-      if (!sound) *(volatile int32_t *)a.err_host = MK_ERR_INVALID_ARG;
-    }
-    if (sound) {
-      int32_t *w = a.sched + 4;
-      for (int i = tid; i <= a.n_groups; i += kThreads) {
-        w[i] = sm->cum_g[i];
-        if (i < a.n_groups) w[2 * (kMaxSeqs + 1) + i] = sm->plen[i];
-      }
-      for (int i = tid; i <= a.n_seqs; i += kThreads) w[kMaxSeqs + 1 + i] = sm->cum_s[i];
-    }
-  }
-  if (!sound) return;
-  const int total = sm->total, n_cta = gridDim.x;
-  const int u_begin = (int)((long long)blockIdx.x * total / n_cta);
-  const int u_end = (int)(((long long)blockIdx.x + 1) * total / n_cta);
-  if (u_begin == u_end) return;
-
-  if (warp == 9) {
+  if (warp == 10) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      saddr(&sm->tmem)),
                  "r"(512)
@@ -482,115 +574,231 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
-  __syncthreads();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const bool sound = take_cut(a, sm);
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
   volatile int *abort = &sm->abort;
+  if (blockIdx.x == 0) {
+    if (tid == 0) {
+      a.sched[0] = !sound;
+      a.sched[1] = sound ? sm->total[0] : 0;
+      a.sched[2] = sound ? sm->total[1] : 0;
+      if (!sound) *(volatile int32_t *)a.err_host = MK_ERR_INVALID_ARG;
+    }
+    if (sound) {
+      int32_t *w = a.sched + 4;
+      for (int i = tid; i <= max(a.n_groups, a.n_seqs); i += kThreads)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (i <= a.n_groups) w[2 * k * kSchedStride + i] = sm->cum_g[k][i];
+          if (i <= a.n_seqs) w[(2 * k + 1) * kSchedStride + i] = sm->cum_s[k][i];
+          if (i < a.n_groups) w[4 * kSchedStride + i] = sm->plen[i];
+        }
+    }
+  }
+  /* this worker's shares: of the pairs, and of the singles for each stream */
+  const int n_cta = gridDim.x;
+  int from[3] = {0, 0, 0}, to[3] = {0, 0, 0};
+  if (sound) {
+    const long long tp = sm->total[0], ts = sm->total[1];
+    const int c = blockIdx.x;
+    from[0] = (int)(c * tp / n_cta);
+    to[0] = (int)((c + 1) * tp / n_cta);
+    from[1] = (int)(2 * c * ts / (2 * n_cta));
+    to[1] = from[2] = (int)((2 * c + 1) * ts / (2 * n_cta));
+    to[2] = (int)((2 * c + 2) * ts / (2 * n_cta));
+  }
   const int TB = kTile / a.G; /* query tokens of a row tile */
 
-  if (warp == 8) {
-    /* ---- producer: K one tile ahead of V, the order in which the products need them */
-    const int boxes = kTile / a.box_rows;
-    const int box = lane % boxes, half = lane / boxes;
-    const uint32_t box_bytes = a.box_rows * C::ROWB;
-    int ik = 0, iv = 0;
-    bool ok = true;
-    for (int u = u_begin; ok && u < u_end;) {
-      const Piece p = piece_at(a, sm, u, u_end);
-      const int n = p.t1 - p.t0;
-      u += n;
-      const int32_t *row = a.tables + (size_t)p.seq * a.max_pages;
-      for (int i = 0; ok && i <= n; ++i) {
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int t = kv == 0 ? i : i - 1;
-          if (t < 0 || t >= n) continue;
-          int &it = kv == 0 ? ik : iv;
-          const int slot = it % C::STAGES;
-          uint64_t *full = kv == 0 ? &sm->kfull[slot] : &sm->vfull[slot];
-          uint64_t *empty = kv == 0 ? &sm->kempty[slot] : &sm->vempty[slot];
-          const int key = p.key0 + (p.t0 + t) * kTile + box * a.box_rows;
-          int page = -1;
-          if (half < C::NH && key < p.kend) {
-            page = __ldg(row + key / a.P);
-            if ((unsigned)page >= (unsigned)a.num_pages) {
-              page = -1;
-              *(volatile int32_t *)a.err_host = MK_ERR_PAGE_OOB;
-            }
-          }
-          ok = warp_wait(empty, ((it / C::STAGES) & 1) ^ 1, abort);
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp < 10) {
+      /* ---- producers: of the pairs warp 8 loads K and warp 9 V; of the singles each
+       * loads both of its stream, K before V, the order in which the products need them */
+      const int s = warp - 8;
+      Loader<D> ld(a, lane);
+      uint32_t armed_k = 0, armed_v = 0; /* parities of each slot's next use */
+      bool ok = true;
+      int it = 0;
+      for (int x = from[0]; ok && x < to[0];) {
+        const Piece p = next_tiles(a, sm, 0, x, to[0]);
+        ld.look_up(p, 0);
+        for (int t = 0; ok && t < p.n; ++t) {
+          const int page = ld.page, slot = it % C::STAGES;
+          ld.look_up(p, t + 1);
+          ok = warp_wait(s == 0 ? &sm->kempty[slot] : &sm->vempty[slot],
+                         ((it / C::STAGES) & 1) ^ 1, abort);
           if (!ok) break;
-          const int loads = __popc(__ballot_sync(0xffffffffu, page >= 0));
-          if (lane == 0) bar_expect(full, loads * box_bytes);
-          __syncwarp();
-          if (page >= 0)
-            tma_2d(saddr((kv == 0 ? ks : vs) + slot * C::TILE + half * C::BLOCK +
-                         box * box_bytes),
-                   kv == 0 ? &kmap : &vmap, half * C::COLS,
-                   (page * a.Hkv + p.kvh) * a.P + key % a.P, full);
+          ld.load(p, t, page, s == 0 ? &kmap : &vmap, (s == 0 ? ks : vs) + slot * C::TILE,
+                  s == 0 ? &sm->kfull[slot] : &sm->vfull[slot], lane);
           ++it;
         }
       }
-    }
-    if (!ok) { /* gave up: let the copies in flight land */
-      for (int i = 0; i < C::STAGES; ++i) {
-        volatile int none = 0;
-        const int jk = ik - 1 - i, jv = iv - 1 - i;
-        if (jk >= 0) warp_wait(&sm->kfull[jk % C::STAGES], (jk / C::STAGES) & 1, &none);
-        if (jv >= 0) warp_wait(&sm->vfull[jv % C::STAGES], (jv / C::STAGES) & 1, &none);
-      }
-    }
-  } else if (warp == 9) {
-    /* ---- issuer: op j is tile j or j / 2 of the piece on stream j % 2 */
-    if (lane == 0) {
-      constexpr uint32_t id_qk = inst_desc(kTile, false), id_pv = inst_desc(D, true);
-      int ik = 0, iv = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-      bool ok = true;
-      for (int u = u_begin; ok && u < u_end;) {
-        const Piece p = piece_at(a, sm, u, u_end);
-        const int n = p.t1 - p.t0;
-        u += n;
-        const bool pair = p.ntok > TB;
-        const int ops = pair ? 2 * n : n;
-        for (int s = 0; ok && s < 2; ++s)
-          if (s < ops) ok = bar_wait(&sm->qready[s], nq[s]++ & 1, abort);
-        auto qk = [&](int j) {
-          const int s = j & 1, it = ik + (pair ? j >> 1 : j), slot = it % C::STAGES;
-          if (!bar_wait(&sm->kfull[slot], (it / C::STAGES) & 1, abort)) return false;
-          tc_fence_after();
-          const uint32_t q0 = saddr(qs + s * C::TILE), k0 = saddr(ks + slot * C::TILE);
-#pragma unroll
-          for (int h = 0; h < C::NH; ++h)
-#pragma unroll
-            for (int c = 0; c < C::COLS / 16; ++c)
-              mma_ss(tmem + s * kTile,
-                     mat_desc(q0 + h * C::BLOCK + c * 32, 16, 8 * C::ROWB, C::SWIZZLE),
-                     mat_desc(k0 + h * C::BLOCK + c * 32, 16, 8 * C::ROWB, C::SWIZZLE), id_qk,
-                     h + c > 0);
-          tc_commit(&sm->sfull[s]);
-          if (!pair || s == 1) tc_commit(&sm->kempty[slot]);
-          return true;
-        };
-        for (int j = 0; ok && j < 2 && j < ops; ++j) ok = qk(j);
-        for (int j = 0; ok && j < ops; ++j) {
-          const int s = j & 1, t = pair ? j >> 1 : j, it = iv + t, slot = it % C::STAGES;
-          ok = bar_wait(&sm->vfull[slot], (it / C::STAGES) & 1, abort) &&
-               bar_wait(&sm->pready[s], np[s]++ & 1, abort);
+      /* uses of each slot so far: the other producer's too */
+      int pair_tiles = 0;
+      for (int x = from[0]; ok && x < to[0];) pair_tiles += next_tiles(a, sm, 0, x, to[0]).n;
+      for (int i = 0; i < C::STAGES; ++i)
+        armed_k |= (uint32_t)(((pair_tiles + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
+      armed_v = armed_k;
+      int ring = 0;
+      for (int x = from[1 + s]; ok && x < to[1 + s];) {
+        const Piece p = next_tiles(a, sm, 1, x, to[1 + s]);
+        ld.look_up(p, 0);
+        for (int t = 0; ok && t < p.n; ++t) {
+          const int page = ld.page, slot = s * R + ring;
+          ring = ring + 1 == R ? 0 : ring + 1;
+          ld.look_up(p, t + 1);
+          ok = warp_wait(&sm->kempty[slot], ((armed_k >> slot) & 1) ^ 1, abort);
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t v0 = saddr(vs + slot * C::TILE);
-#pragma unroll
-          for (int c = 0; c < kTile / 16; ++c)
-            mma_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + c * 8,
-                   mat_desc(v0 + c * 16 * C::ROWB, C::BLOCK, 8 * C::ROWB, C::SWIZZLE), id_pv,
-                   j > 1 || c > 0);
-          if (!pair || s == 1) tc_commit(&sm->vempty[slot]);
-          if (j + 2 < ops) ok = qk(j + 2);
+          ld.load(p, t, page, &kmap, ks + slot * C::TILE, &sm->kfull[slot], lane);
+          armed_k ^= 1u << slot;
+          ok = warp_wait(&sm->vempty[slot], ((armed_v >> slot) & 1) ^ 1, abort);
+          if (!ok) break;
+          ld.load(p, t, page, &vmap, vs + slot * C::TILE, &sm->vfull[slot], lane);
+          armed_v ^= 1u << slot;
         }
-        for (int s = 0; ok && s < 2; ++s)
-          if (s < ops) tc_commit(&sm->oready[s]);
-        ik += n;
-        iv += n;
+      }
+      if (!ok) {
+        /* gave up: let the copies in flight land.  A slot that was filled and not yet
+         * consumed completes a phase; the parity before its next use names it. */
+        volatile int none = 0;
+        for (int i = 0; i < C::STAGES; ++i) {
+          if (it > 0) {
+            const int last = it - 1 - (it - 1 - i + C::STAGES) % C::STAGES;
+            if (last >= 0)
+              warp_wait(s == 0 ? &sm->kfull[i] : &sm->vfull[i], (last / C::STAGES) & 1, &none);
+          }
+          if (i / R == s) {
+            if (from[1 + s] < to[1 + s] && ring >= 0) {
+              warp_wait(&sm->kfull[i], ((armed_k >> i) & 1) ^ 1, &none);
+              warp_wait(&sm->vfull[i], ((armed_v >> i) & 1) ^ 1, &none);
+            }
+          }
+        }
+      }
+    } else if (warp == 10 && lane == 0) {
+      /* ---- issuer */
+      constexpr uint32_t id_qk = inst_desc(kTile, false), id_pv = inst_desc(D, true);
+      auto qk = [&](int s, int slot) {
+        const uint64_t q0 = mat_desc(saddr(qs + s * C::TILE), 16, 8 * C::ROWB, C::SWIZZLE);
+        const uint64_t k0 = mat_desc(saddr(ks + slot * C::TILE), 16, 8 * C::ROWB, C::SWIZZLE);
+#pragma unroll
+        for (int h = 0; h < C::NH; ++h)
+#pragma unroll
+          for (int c = 0; c < C::COLS / 16; ++c) {
+            const int o = (h * C::BLOCK + c * 32) >> 4;
+            mma_ss(tmem + s * kTile, q0 + o, k0 + o, id_qk, h + c > 0);
+          }
+      };
+      auto pv = [&](int s, int slot, bool acc) {
+        const uint64_t v0 = mat_desc(saddr(vs + slot * C::TILE), C::BLOCK, 8 * C::ROWB, C::SWIZZLE);
+#pragma unroll
+        for (int c = 0; c < kTile / 16; ++c)
+          mma_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + c * 8,
+                 v0 + ((c * 16 * C::ROWB) >> 4), id_pv, acc || c > 0);
+      };
+      bool ok = true;
+      uint32_t q_par = 0, p_par = 0, k_par = 0, v_par = 0; /* a bit per stream, slot */
+      int it = 0; /* pair tiles */
+      for (int x = from[0]; ok && x < to[0];) { /* pairs: both streams over the same K and V */
+        const int n = next_tiles(a, sm, 0, x, to[0]).n;
+        if (n == 0) break;
+        ok = bar_wait(&sm->qready[0], q_par & 1, abort) &&
+             bar_wait(&sm->qready[1], q_par & 1, abort);
+        if (!ok) break;
+        q_par ^= 3;
+        for (int t = 0; ok && t <= n; ++t) {
+          const int kslot = (it + t) % C::STAGES, vslot = (it + t - 1) % C::STAGES;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (ok && t > 0) {
+              if (s == 0) ok = bar_wait(&sm->vfull[vslot], (v_par >> vslot) & 1, abort);
+              ok = ok && bar_wait(&sm->pready[s], (p_par >> s) & 1, abort);
+              if (!ok) break;
+              p_par ^= 1u << s;
+              tc_fence_after();
+              pv(s, vslot, t > 1);
+              if (s == 1) {
+                tc_commit(&sm->vempty[vslot]);
+                v_par ^= 1u << vslot;
+              }
+              if (t == n) tc_commit(&sm->oready[s]);
+            }
+            if (ok && t < n) {
+              if (s == 0) ok = bar_wait(&sm->kfull[kslot], (k_par >> kslot) & 1, abort);
+              if (!ok) break;
+              tc_fence_after();
+              qk(s, kslot);
+              tc_commit(&sm->sfull[s]);
+              if (s == 1) {
+                tc_commit(&sm->kempty[kslot]);
+                k_par ^= 1u << kslot;
+              }
+            }
+          }
+        }
+        it += n;
+      }
+      /* singles: whichever stream's next product is ready */
+      int left[2] = {0, 0}, done = 0, ring[2] = {0, 0};
+      bool want_pv[2] = {false, false}, fresh[2] = {false, false};
+      uint64_t since = 0;
+      for (int idle = 0; ok && done < 2;) {
+        bool moved = false;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const int slot = s * R + ring[s];
+          if (left[s] < 0) continue;
+          if (left[s] == 0) { /* the next piece */
+            if (!bar_test(&sm->qready[s], (q_par >> s) & 1)) continue;
+            q_par ^= 1u << s;
+            left[s] = *(volatile int *)&sm->piece_tiles[s];
+            fresh[s] = true;
+            moved = true;
+            if (left[s] == 0) {
+              left[s] = -1;
+              ++done;
+              continue;
+            }
+          }
+          if (!want_pv[s]) {
+            if (!bar_test(&sm->kfull[slot], (k_par >> slot) & 1)) continue;
+            k_par ^= 1u << slot;
+            tc_fence_after();
+            qk(s, slot);
+            tc_commit(&sm->sfull[s]);
+            tc_commit(&sm->kempty[slot]);
+            want_pv[s] = true;
+            moved = true;
+          } else {
+            if (!bar_test(&sm->vfull[slot], (v_par >> slot) & 1) ||
+                !bar_test(&sm->pready[s], (p_par >> s) & 1))
+              continue;
+            v_par ^= 1u << slot;
+            p_par ^= 1u << s;
+            tc_fence_after();
+            pv(s, slot, !fresh[s]);
+            fresh[s] = false;
+            tc_commit(&sm->vempty[slot]);
+            ring[s] = ring[s] + 1 == R ? 0 : ring[s] + 1;
+            want_pv[s] = false;
+            if (--left[s] == 0) tc_commit(&sm->oready[s]);
+            moved = true;
+          }
+        }
+        if (moved) {
+          idle = 0;
+          since = 0;
+        } else if ((++idle & 255) == 0) {
+          const uint64_t t = now_ns();
+          if (!since)
+            since = t;
+          else if (t - since > kWaitLimit)
+            *abort = 1;
+          if (*abort) ok = false;
+        }
       }
       if (!ok) { /* gave up: let the products in flight end */
         volatile int none = 0;
@@ -599,37 +807,57 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     /* ---- softmax: stream s, one row a thread */
     const int s = warp >> 2, r = tid & (kTile - 1);
     const uint32_t lanes = (uint32_t)(warp & 3) << 21; /* this warp's TMEM lanes */
     const uint32_t at_s = tmem + lanes + s * kTile, at_o = at_s + 2 * kTile;
+    uint8_t *qd = qs + s * C::TILE + (warp & 3) * 32 * C::ROWB; /* this warp's rows of Q */
     const float c2 = a.scale_log2;
-    int ns = 0, no = 0, iv = 0, nx = 0;
+    uint32_t s_par = 0, o_par = 0;
+    int it = 0, ring = 0;   /* pair tiles; this stream's slot */
+    uint32_t v_par = 0;     /* parities of this stream's slots, set behind the pairs */
     bool ok = true;
-    for (int u = u_begin; ok && u < u_end;) {
-      const Piece p = piece_at(a, sm, u, u_end);
-      const int n = p.t1 - p.t0;
-      u += n;
-      const bool pair = p.ntok > TB;
-      const int ops = pair ? 2 * n : n;
-      if (s < ops) {
+    for (int line = 0; ok && line < 2; ++line) {
+      const bool pair = line == 0;
+      int x = pair ? from[0] : from[1 + s];
+      const int end = pair ? to[0] : to[1 + s];
+      if (!pair)
+        for (int i = 0; i < C::STAGES; ++i)
+          v_par |= (uint32_t)(((it + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
+      while (ok) {
+        const Piece p = next_tiles(a, sm, line, x, end);
+        if (pair && p.n == 0) break;
+        if (tid == s * kTile) *(volatile int *)&sm->piece_tiles[s] = p.n;
+        if (p.n == 0) {
+          __syncwarp();
+          if (lane == 0) bar_arrive(&sm->qready[s]);
+          break;
+        }
         const int tok0 = p.tok0 + (pair ? s * TB : 0);
-        const int ntok = min(TB, p.tok0 + p.ntok - tok0);
-        const int rows = ntok * a.G;
-        /* Q rows into swizzled shared memory, zeros behind the last */
-        uint8_t *qd = qs + s * C::TILE;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const int k = i * kTile + r, qr = k / (D / 8), ch = k % (D / 8);
-          const int hb = ch / (C::COLS / 8), cc = ch % (C::COLS / 8);
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (qr < rows) {
-            const int t = qr / a.G;
-            x = __ldg((const uint4 *)(a.q + (tok0 + t) * a.q_stride +
-                                      (long long)(p.kvh * a.G + qr - t * a.G) * D + ch * 8));
+        const int rows = min(TB, p.tok0 + p.ntok - tok0) * a.G;
+        /* this warp's 32 rows of Q into swizzled shared memory, zeros behind the last */
+        {
+          uint4 v[D / 8];
+          constexpr int PER = D / 8; /* 16-byte chunks of a row */
+          const int ch = lane % PER, r0 = (warp & 3) * 32 + lane / PER;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int qr = r0 + i * (32 / PER);
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (qr < rows) {
+              const int t = qr / a.G;
+              v[i] = __ldg((const uint4 *)(a.q + (tok0 + t) * a.q_stride +
+                                           (long long)(p.kvh * a.G + qr - t * a.G) * D + ch * 8));
+            }
           }
-          const int sw = D < 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
-          *(uint4 *)(qd + hb * C::BLOCK + qr * C::ROWB + sw * 16) = x;
+          const int hb = ch / (C::COLS / 8), cc = ch % (C::COLS / 8);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int qr = lane / PER + i * (32 / PER);
+            const int sw = D < 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
+            *(uint4 *)(qd + hb * C::BLOCK + qr * C::ROWB + sw * 16) = v[i];
+          }
         }
         fence_async_smem();
         __syncwarp();
@@ -638,15 +866,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool valid = r < rows, busy = (warp & 3) * 32 < rows;
         const int tok = tok0 + (valid ? r / a.G : 0);
         const int head = p.kvh * a.G + (valid ? r % a.G : 0);
-        const int b = p.own ? p.seq : find(sm->off, a.n_seqs + 1, tok);
+        const int b = p.own ? p.seq : a.off ? find(sm->off, a.n_seqs + 1, tok) : tok;
         /* keys of the item that this row sees end here */
         const int limit = min(p.kend, sm->len[b] - (sm->off[b + 1] - tok) + 1);
         float m = -INFINITY, l = 0.0f; /* m in score units */
-        for (int j = s; j < ops; j += 2) {
-          const int t = pair ? j >> 1 : j;
+        for (int t = 0; t < p.n; ++t) {
           const int k0 = p.key0 + (p.t0 + t) * kTile;
-          ok = warp_wait(&sm->sfull[s], ns++ & 1, abort);
+          ok = warp_wait(&sm->sfull[s], s_par, abort);
           if (!ok) break;
+          s_par ^= 1;
           tc_fence_after();
           if (busy) {
             float x[kTile];
@@ -659,15 +887,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 4; i < kTile; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
             const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (j < 2) {
+            if (t == 0) {
               m = top;
             } else {
               const bool move = m == -INFINITY ? top > m : (top - m) * c2 > kSlack;
               if (__any_sync(0xffffffffu, move)) {
                 /* the products into O so far are complete: they were issued before this S */
-                const float to = move ? top : m;
-                const float f = move ? exp2_approx((m - to) * c2) : 1.0f; /* m -inf: 0 */
-#pragma unroll
+                const float now = move ? top : m;
+                const float f = move ? exp2_approx((m - now) * c2) : 1.0f; /* m -inf: 0 */
+#pragma unroll 1
                 for (int i = 0; i < D; i += 32) {
                   float o[32];
                   tmem_ld32(at_o + i, o);
@@ -677,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tmem_st32(at_o + i, w);
                 }
                 l *= f;
-                m = to;
+                m = now;
               }
             }
             const float off = m == -INFINITY ? 0.0f : -m * c2;
@@ -698,10 +926,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             tmem_wait_st();
           }
+          const int slot = pair ? it % C::STAGES : s * R + ring;
           if (k0 + kTile > p.kend) {
             /* zero the V rows behind the last key: what lies there may be NaN */
-            const int it = iv + t, slot = it % C::STAGES;
-            ok = warp_wait(&sm->vfull[slot], (it / C::STAGES) & 1, abort);
+            ok = warp_wait(&sm->vfull[slot],
+                           pair ? (it / C::STAGES) & 1 : (v_par >> slot) & 1, abort);
             if (!ok) break;
             if (k0 + r >= p.kend) {
               uint8_t *vr = vs + slot * C::TILE + r * C::ROWB;
@@ -712,106 +941,102 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_async_smem();
           }
+          if (pair) {
+            ++it;
+          } else {
+            v_par ^= 1u << slot;
+            ring = ring + 1 == R ? 0 : ring + 1;
+          }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) bar_arrive(&sm->pready[s]);
         }
         if (!ok) break;
-        ok = warp_wait(&sm->oready[s], no++ & 1, abort);
+        ok = warp_wait(&sm->oready[s], o_par, abort);
         if (!ok) break;
+        o_par ^= 1;
         tc_fence_after();
-        /* even and odd tiles of the same rows: the second stream hands over its part */
-        const bool joins = !pair && n > 1;
-        float *xo = (float *)qs; /* [D][128]: Q is read by now */
-        if (joins && s == 1) {
-          if (busy) {
-#pragma unroll
-            for (int i = 0; i < D; i += 32) {
-              float o[32];
-              tmem_ld32(at_o + i, o);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) xo[(i + k) * kTile + r] = o[k];
-            }
-            sm->xm[r] = m;
-            sm->xl[r] = l;
-          }
-          __syncwarp();
-          if (lane == 0) bar_arrive(&sm->xfull);
-          ok = warp_wait(&sm->xfree, nx++ & 1, abort); /* Q may be written again */
-          if (!ok) break;
-        } else {
-          float f0 = 1.0f, f1 = 0.0f;
-          if (joins) {
-            ok = warp_wait(&sm->xfull, nx++ & 1, abort);
-            if (!ok) break;
-            const float m1 = sm->xm[r], mm = fmaxf(m, m1);
-            if (mm != -INFINITY) {
-              f0 = exp2_approx((m - mm) * c2);
-              f1 = exp2_approx((m1 - mm) * c2);
-            }
-            l = l * f0 + sm->xl[r] * f1;
-            m = mm;
-          }
-          const bool whole = p.own && p.key0 == 0 && n == p.nt; /* nothing to merge */
+        if (busy) {
+          /* rows of O through this warp's part of Q (read by now), so that a row's
+           * columns are written together */
+          const bool whole = p.own && p.key0 == 0 && p.n == p.nt; /* nothing to merge */
           const long long orow = (long long)tok * a.Hq + head;
-          const long long prow =
-              p.t0 == 0 ? (long long)p.own * a.n_tokens * a.Hq + orow
-                        : 2ll * a.n_tokens * a.Hq + (long long)blockIdx.x * 2 * kTile +
-                              (pair ? s * kTile : 0) + r;
+          const long long extra = 2ll * a.n_tokens * a.Hq +
+                                  (pair ? 2ll * blockIdx.x + s
+                                        : 2ll * n_cta + 2ll * blockIdx.x + s) * kTile;
+          const long long prow = p.t0 == 0 ? (long long)p.own * a.n_tokens * a.Hq + orow : extra + r;
           const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-          if (busy) {
+          constexpr int W = D / 2;            /* columns staged at a time */
+          constexpr int RL = W / 4, RI = 32 / RL; /* lanes of a row, rows at a time */
+#pragma unroll 1
+          for (int i0 = 0; i0 < D; i0 += W) {
 #pragma unroll
-            for (int i = 0; i < D; i += 32) {
-              float o[32];
-              tmem_ld32(at_o + i, o);
-              if (joins) {
+            for (int i = 0; i < W; i += 16) {
+              float o[16];
+              tmem_ld16(at_o + i0 + i, o);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] = o[k] * f0 + xo[(i + k) * kTile + r] * f1;
-              }
-              if (valid && whole) {
-                uint4 *d = (uint4 *)(a.out + orow * D + i);
-#pragma unroll
-                for (int k = 0; k < 32; k += 8)
-                  d[k / 8] = make_uint4(pack_bf16(o[k] * inv, o[k + 1] * inv),
-                                        pack_bf16(o[k + 2] * inv, o[k + 3] * inv),
-                                        pack_bf16(o[k + 4] * inv, o[k + 5] * inv),
-                                        pack_bf16(o[k + 6] * inv, o[k + 7] * inv));
-              } else if (valid) {
-                float4 *d = (float4 *)(a.part + prow * D + i);
-#pragma unroll
-                for (int k = 0; k < 32; k += 4)
-                  d[k / 4] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+              for (int k = 0; k < 4; ++k) {
+                const int c = i / 4 + k; /* float4 of the row, 8 (4) to a swizzled row */
+                constexpr int CR = C::ROWB / 16;
+                *(float4 *)(qd + c / CR * C::BLOCK + lane * C::ROWB +
+                            ((c % CR) ^ (lane & (CR - 1))) * 16) =
+                    make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
               }
             }
-            if (valid && whole) {
-              if (a.lse)
-                a.lse[orow] = l > 0.0f ? (m * c2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
-            } else if (valid) {
-              a.part_ml[prow] = make_float2(m == -INFINITY ? m : m * c2, l);
-            }
-          }
-          if (joins) {
-            /* no warp of either stream writes Q again before all have read */
             __syncwarp();
-            if (lane == 0) bar_arrive(&sm->xfree);
-            ok = warp_wait(&sm->xfree, (nx - 1) & 1, abort);
-            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 32 / RI; ++i) {
+              const int row = i * RI + lane / RL, c = lane % RL;
+              constexpr int CR = C::ROWB / 16;
+              const float4 o = *(const float4 *)(qd + c / CR * C::BLOCK + row * C::ROWB +
+                                                 ((c % CR) ^ (row & (CR - 1))) * 16);
+              const long long pr = __shfl_sync(0xffffffffu, prow, row);
+              const long long dr = __shfl_sync(0xffffffffu, orow, row);
+              const float f = __shfl_sync(0xffffffffu, inv, row);
+              if ((warp & 3) * 32 + row < rows) {
+                if (whole)
+                  *(uint2 *)(a.out + dr * D + i0 + c * 4) =
+                      make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+                else
+                  *(float4 *)(a.part + pr * D + i0 + c * 4) = o;
+              }
+            }
+            __syncwarp();
+          }
+          if (valid && whole) {
+            if (a.lse)
+              a.lse[orow] = l > 0.0f ? (m * c2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          } else if (valid) {
+            a.part_ml[prow] = make_float2(m == -INFINITY ? m : m * c2, l);
           }
         }
         tc_fence_before();
       }
-      iv += n;
     }
   }
   __syncthreads();
   if (tid == 0 && *abort) *(volatile int32_t *)a.err_host = MK_ERR_DEVICE_TIMEOUT;
-  if (warp == 9) {
+  if (warp == 10) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
 }
 
 /* ---- the join ----------------------------------------------------------------- */
+
+/* find() by a whole warp: 32 places a round, so one or two loads deep. */
+__device__ __forceinline__ int warp_find(const int32_t *a, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n; /* the answer is in [lo, lo + len) */
+  while (len > 1) {
+    const int step = (len + 31) / 32, i = lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, i < len && a[lo + i] <= x);
+    const int k = 31 - __clz(le | 1u);
+    lo += k * step;
+    len = min(step, len - k * step);
+  }
+  return lo;
+}
 
 /* One warp per output row: M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
  * Reads L2: the partials were written just before. */
@@ -825,44 +1050,54 @@ __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a
   const int tok = (int)(orow / a.Hq), head = (int)(orow - (long long)tok * a.Hq);
   const int tokens = a.off ? a.off[a.n_seqs] : a.n_seqs;
   if (tok >= tokens) return;
-  const int TB = kTile / a.G, BT = 2 * TB, total = a.sched[2];
+  const int TB = kTile / a.G, BT = 2 * TB;
   const int kvh = head / a.G, hg = head - kvh * a.G;
-  const int32_t *cum_g = a.sched + 4, *cum_s = cum_g + kMaxSeqs + 1, *plens = cum_s + kMaxSeqs + 1;
-  const int b = a.off ? find(a.off, a.n_seqs + 1, tok) : tok;
+  const int32_t *cut = a.sched + 4;
+  const int b = a.off ? warp_find(a.off, a.n_seqs + 1, tok) : tok;
   const int first = a.off ? a.off[b] : b, T = a.off ? a.off[b + 1] - first : 1, len = a.lens[b];
-  int plen = 0, n_shared = 0, n_own = 0;          /* pieces */
-  int cs = 0, co = 0;                             /* their first CTAs */
-  int rs = 0, ro = 0;                             /* the row's place in a CTA's own slots */
+  int plen = 0, n_shared = 0, n_own = 0;      /* pieces */
+  long long xs = 0, xo = 0;                   /* where those behind the first are: one tile a worker */
+  int ss = 0, so = 0;                         /* rows from a worker's slot to the next */
+  const long long dense = (long long)a.n_tokens * a.Hq;
+  auto pieces = [&](int line, int begin, int tiles, int ti, long long &at, int &step) {
+    const int total = a.sched[1 + line], n = line == 0 ? n_cta : 2 * n_cta;
+    const int w0 = worker_of(begin + kItemCost, total, n);
+    const int w1 = worker_of(begin + kItemCost + tiles - 1, total, n);
+    const int tile = ti / TB;                 /* of a pair */
+    step = line == 0 ? 2 * kTile : kTile;
+    at = 2 * dense + (line == 0 ? 0 : 2ll * n_cta * kTile) + (long long)w0 * step + tile * kTile +
+         (ti - tile * TB) * a.G + hg;
+    return w1 - w0 + 1;
+  };
   if (a.n_groups) {
-    const int g = find(a.starts, a.n_groups + 1, b);
-    plen = plens[g];
+    const int g = warp_find(a.starts, a.n_groups + 1, b);
+    plen = cut[4 * kSchedStride + g];
     if (plen) {
-      const int gtok = a.off ? a.off[a.starts[g]] : a.starts[g];
-      const int gend = a.off ? a.off[a.starts[g + 1]] : a.starts[g + 1];
-      const int nt = div_up(plen, kTile), nb = div_up(gend - gtok, BT), j = (tok - gtok) / BT;
-      const int u = cum_g[g] + (kvh * nb + j) * nt, ti = tok - gtok - j * BT;
-      cs = cta_of(u, total, n_cta);
-      n_shared = cta_of(u + nt - 1, total, n_cta) - cs + 1;
-      rs = ti / TB * kTile + ti % TB * a.G + hg;
+      const int s0 = a.starts[g], s1 = a.starts[g + 1];
+      const int gtok = a.off ? a.off[s0] : s0, gT = (a.off ? a.off[s1] : s1) - gtok;
+      const int nt = key_tiles(0, plen), nb = pair_blocks(gT, TB), j = (tok - gtok) / BT;
+      const int line = j < nb ? 0 : 1;
+      const int begin = cut[2 * line * kSchedStride + g] +
+                        (line == 0 ? kvh * nb + j : kvh) * item_cost(nt);
+      n_shared = pieces(line, begin, nt, tok - gtok - j * BT, xs, ss);
     }
   }
-  const int jb = (tok - first) / BT, nt_own = own_tiles(len, T, plen, BT, jb);
+  const int nb = pair_blocks(T, TB), jb = (tok - first) / BT, line = jb < nb ? 0 : 1;
+  const int nt_own = key_tiles(plen, block_end(len, T, TB, jb));
   if (nt_own) {
-    int u = cum_s[b] + (cum_s[b + 1] - cum_s[b]) / a.Hkv * kvh;
-    for (int j = 0; j < jb; ++j) u += own_tiles(len, T, plen, BT, j);
-    const int ti = tok - first - jb * BT;
-    co = cta_of(u, total, n_cta);
-    n_own = cta_of(u + nt_own - 1, total, n_cta) - co + 1;
-    ro = ti / TB * kTile + ti % TB * a.G + hg;
+    const int32_t *cum = cut + (2 * line + 1) * kSchedStride;
+    int begin = cum[b] + (cum[b + 1] - cum[b]) / a.Hkv * kvh;
+    if (line == 0)
+      for (int j = 0; j < jb; ++j) begin += item_cost(key_tiles(plen, block_end(len, T, TB, j)));
+    n_own = pieces(line, begin, nt_own, tok - first - jb * BT, xo, so);
   }
   if (n_shared == 0 && n_own == 1) return; /* written by attn_tiles */
   const int n = n_shared + n_own;
-  const long long dense = (long long)a.n_tokens * a.Hq;
   auto place = [&](int i) -> long long { /* partial row of piece i */
     const bool own = i >= n_shared;
     const int k = own ? i - n_shared : i;
     if (k == 0) return own ? dense + orow : orow;
-    return 2 * dense + (long long)((own ? co : cs) + k) * 2 * kTile + (own ? ro : rs);
+    return own ? xo + (long long)k * so : xs + (long long)k * ss;
   };
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[place(i)].x);
@@ -1010,8 +1245,8 @@ mk_status mk_attn_create(const mk_attn_desc *d, void *stream, mk_attn **out) {
     delete at;
     return st;
   }
-  const size_t rows = 2 * (size_t)d->max_tokens * d->n_q_heads + (size_t)at->n_sm * 2 * kTile;
-  at->o_part = ((4 + 3 * (size_t)(kMaxSeqs + 1)) * 4 + 255) / 256 * 256;
+  const size_t rows = 2 * (size_t)d->max_tokens * d->n_q_heads + (size_t)at->n_sm * 4 * kTile;
+  at->o_part = ((4 + 5 * (size_t)kSchedStride) * 4 + 255) / 256 * 256;
   at->o_ml = at->o_part + rows * d->head_dim * 4;
   cudaError_t e = d->head_dim == 32 ? prepare<32>() : d->head_dim == 64 ? prepare<64>() : prepare<128>();
   if (e == cudaSuccess) e = cudaMalloc(&at->ws, at->o_ml + rows * sizeof(float2));
