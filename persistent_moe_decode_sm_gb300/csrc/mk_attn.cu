@@ -14,7 +14,7 @@
  * a captured call follows its batch.
  *
  * attn_tiles, one CTA per SM: producer warps move K and V tiles with TMA, one box
- * per page and 64 dims, into swizzled shared memory; one thread issues S = Q K^T
+ * per page and 64 dims, into swizzled shared memory; issuing warps start S = Q K^T
  * and O += P V on the tensor cores (tcgen05, 128 rows, accumulators in TMEM); two
  * warpgroups, the streams, turn S into P, one row a thread, P going back to TMEM
  * as the A operand.  A pair's two row tiles run on the two streams over the same
@@ -36,10 +36,11 @@
 
 namespace {
 
-constexpr int kThreads = 384;      /* two softmax warpgroups; two producers, the issuer */
+constexpr int kThreads = 384;      /* two softmax warpgroups, two producers, two issuers */
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88; /* 256 * 208 + 128 * 88 = 384 * 168 */
 constexpr int kTile = 128;         /* keys per tile; rows per row tile */
 constexpr int kItemCost = 2;       /* what an item's beginning and end cost, in tiles */
+constexpr int kQueue = 4;          /* pieces that a producer is ahead of its stream */
 constexpr int kMaxSeqs = 1024;     /* of a call: the cut's tables are in shared memory */
 constexpr uint64_t kWaitLimit = 2000000000ull; /* ns */
 /* The running maximum moves only when a score exceeds it by this much (in powers
@@ -56,6 +57,7 @@ struct Args {
   __nv_bfloat16 *out;
   float *lse;
   float scale_log2; /* scale * log2(e) */
+  uint32_t inv_g;   /* ceil(2^16 / G): r * inv_g >> 16 is r / G for r < 128 */
   int32_t *err_host;
   /* workspace */
   int32_t *sched;    /* the cut, for attn_merge: [0] bad, [1] [2] the lines' lengths, then
@@ -77,12 +79,23 @@ struct Cfg {
   static constexpr int SMEM = 1024 + TILE * (2 + 2 * STAGES);
 };
 
+/* One worker's part of an item. */
+struct Piece {
+  int line;            /* 0: a pair, 1: a single */
+  int own;             /* 1: a sequence's own keys, 0: a group's shared ones */
+  int seq;             /* whose table row names the pages */
+  int kvh, tok0, ntok; /* query tokens of the item */
+  int key0, kend;      /* the item's keys */
+  int t0, n, nt;       /* first tile and tiles of this piece (0: no more), tiles of the item */
+};
+
 struct Smem { /* behind the tiles */
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
-  uint64_t sfull[2], pready[2], qready[2], oready[2], drain;
+  uint64_t sfull[2], pready[2][2], qready[2], oready[2], drain[2];
+  uint64_t qfull[2][kQueue], qempty[2][kQueue];
+  Piece queue[2][kQueue];
   uint32_t tmem;
   int abort;
-  int piece_tiles[2]; /* from a stream to the issuer with Q: tiles of a single piece, 0: no more */
   unsigned long long sums[kThreads / 32];
   int total[2];       /* length of the pairs' line, of the singles' */
   int32_t off[kMaxSeqs + 1], len[kMaxSeqs];
@@ -136,25 +149,16 @@ __device__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
     }
   }
 }
-__device__ __forceinline__ bool bar_test(uint64_t *b, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(saddr(b)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
   return __all_sync(0xffffffffu, bar_wait(b, parity, abort));
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
-                                       uint64_t *bar) {
+                                       uint64_t *bar, uint32_t lead) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(saddr(bar))
+      "{\n .reg .pred e;\n setp.ne.u32 e, %5, 0;\n"
+      " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(saddr(bar)), "r"(lead)
       : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() {
@@ -166,47 +170,61 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   saddr(bar))
-               : "memory");
-}
-/* D (+)= A B with A and B in shared memory, or A in TMEM. */
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+/* The issuing warp runs its code as a whole, so that addresses and descriptors stay in
+ * uniform registers; `lead` is 1 in the one lane whose instruction counts.  (One lane
+ * alone in a branch issued a product in 100 cycles, more than the product takes.) */
+__device__ __forceinline__ uint32_t elect_lead() {
+  uint32_t p;
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n .reg .pred q;\n elect.sync _|q, 0xffffffff;\n selp.u32 %0, 1, 0, q;\n}\n" : "=r"(p));
+  return p;
+}
+__device__ __forceinline__ void tc_commit(uint64_t *bar, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.u32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          saddr(bar)),
+      "r"(lead)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+/* D (+)= A B with A and B in shared memory, or A in TMEM. */
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc, uint32_t lead) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n .reg .pred p, e;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 e, %5, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
       : "memory");
 }
 #define R8(x, i) x(i), x(i + 1), x(i + 2), x(i + 3), x(i + 4), x(i + 5), x(i + 6), x(i + 7)
 #define R32(x, i) R8(x, i), R8(x, i + 8), R8(x, i + 16), R8(x, i + 24)
 /* 16, 32 or 128 columns of this thread's TMEM lane.  The load and its wait are one
  * statement: between two, the compiler could move registers that have not landed. */
-__device__ __forceinline__ void tmem_ld32(uint32_t at, float *v) {
 #define OUT(i) "=f"(v[i])
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
-      : R32(OUT, 0)
-      : "r"(at)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_ld16(uint32_t at, float *v) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {"
       "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
       "tcgen05.wait::ld.sync.aligned;"
       : R8(OUT, 0), R8(OUT, 8)
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R32(OUT, 0)
       : "r"(at)
       : "memory");
 }
@@ -235,6 +253,13 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *v) {
       "%29, %30, %31};" ::R32(IN, 0),
       "r"(at)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15};" ::R8(IN, 0),
+      R8(IN, 8), "r"(at)
+      : "memory");
 #undef IN
 }
 __device__ __forceinline__ void tmem_wait_st() {
@@ -245,6 +270,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  return __ffma2_rn(a, b, c);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -284,9 +313,14 @@ __device__ __forceinline__ int key_tiles(int begin, int end) {
 }
 __device__ __forceinline__ int item_cost(int tiles) { return tiles ? tiles + kItemCost : 0; }
 /* The worker that owns place x of a line cut over n: worker w owns
- * [w total / n, (w + 1) total / n). */
+ * [w total / n, (w + 1) total / n), so it is the largest w with w total < (x + 1) n.
+ * An estimate in 32 bits is off by less than one. */
 __device__ __forceinline__ int worker_of(int x, int total, int n) {
-  return (int)((((long long)x + 1) * n - 1) / total);
+  const long long y = ((long long)x + 1) * n;
+  int w = (int)__fdividef((float)y, (float)total);
+  while ((long long)w * total >= y) --w;
+  while (((long long)w + 1) * total < y) ++w;
+  return w;
 }
 /* Last i in [0, n) with a[i] <= x (a not decreasing, a[0] <= x). */
 template <class T>
@@ -430,20 +464,12 @@ __device__ bool take_cut(const Args &a, Smem *sm) {
   return true;
 }
 
-/* One worker's part of an item. */
-struct Piece {
-  int own;             /* 1: a sequence's own keys, 0: a group's shared ones */
-  int seq;             /* whose table row names the pages */
-  int kvh, tok0, ntok; /* query tokens of the item */
-  int key0, kend;      /* the item's keys */
-  int t0, n, nt;       /* first tile and tiles of this piece, tiles of the item */
-};
-
 /* The piece at place x of a line, x < end; x moves behind it.  A share that ends
  * within an item's fixed cost has no tile of it: n is 0. */
 __device__ Piece next_piece(const Args &a, const Smem *sm, int line, int &x, int end) {
   const int TB = kTile / a.G;
   Piece p;
+  p.line = line;
   int j, begin; /* the item's block, its place */
   if (x < sm->cum_g[line][a.n_groups]) {
     const int g = find(sm->cum_g[line], a.n_groups, x);
@@ -484,56 +510,47 @@ __device__ Piece next_piece(const Args &a, const Smem *sm, int line, int &x, int
   x = min(end, begin + item_cost(p.nt));
   return p;
 }
-/* The next piece with tiles; n is 0 at the share's end. */
-__device__ Piece next_tiles(const Args &a, const Smem *sm, int line, int &x, int end) {
-  Piece p;
-  p.n = 0;
-  while (x < end) {
-    p = next_piece(a, sm, line, x, end);
-    if (p.n) break;
-  }
-  return p;
-}
-
 /* ---- the tiles ---------------------------------------------------------------- */
 
-/* Loads tile t of a piece (or nothing of it behind the last key): one box a lane. */
+/* Loads tile t of a piece, as far as its keys go: a box per page (or part of one) and
+ * 64 dims.  Lane i looks up the page of box i, a tile ahead. */
 template <int D>
 struct Loader {
   using C = Cfg<D>;
   const Args &a;
-  int box, half, page;
-  __device__ Loader(const Args &a_, int lane) : a(a_) {
-    const int boxes = kTile / a.box_rows;
-    box = lane % boxes;
-    half = lane / boxes;
+  int lane, boxes, page;
+  uint32_t lead;
+  __device__ Loader(const Args &a_, int lane_) : a(a_), lane(lane_) {
+    boxes = kTile / a.box_rows;
     page = -1;
+    lead = elect_lead();
   }
-  __device__ __forceinline__ int key(const Piece &p, int t) const {
-    return p.key0 + (p.t0 + t) * kTile + box * a.box_rows;
-  }
-  /* the page of this lane's box of tile t; -1: no box */
   __device__ __forceinline__ void look_up(const Piece &p, int t) {
-    const int k = key(p, t);
+    const int k = p.key0 + (p.t0 + t) * kTile + lane * a.box_rows;
     page = -1;
-    if (t < p.n && half < C::NH && k < p.kend)
+    if (t < p.n && lane < boxes && k < p.kend)
       page = __ldg(a.tables + (size_t)p.seq * a.max_pages + k / a.P);
   }
   __device__ __forceinline__ void load(const Piece &p, int t, int pg, const CUtensorMap *map,
-                                       uint8_t *tile, uint64_t *full, int lane) {
-    const int k = key(p, t);
-    bool mine = half < C::NH && k < p.kend;
-    if (mine && (unsigned)pg >= (unsigned)a.num_pages) {
-      mine = false;
-      *(volatile int32_t *)a.err_host = MK_ERR_PAGE_OOB;
-    }
-    const int boxes = __popc(__ballot_sync(0xffffffffu, mine));
+                                       uint8_t *tile, uint64_t *full) {
+    const int k0 = p.key0 + (p.t0 + t) * kTile;
+    const int k = k0 + lane * a.box_rows;
+    const bool mine = lane < boxes && k < p.kend;
+    const bool good = mine && (unsigned)pg < (unsigned)a.num_pages;
+    if (mine && !good) *(volatile int32_t *)a.err_host = MK_ERR_PAGE_OOB;
+    const unsigned set = __ballot_sync(0xffffffffu, good);
+    const int y = (pg * a.Hkv + p.kvh) * a.P + k % a.P;
     const uint32_t bytes = a.box_rows * C::ROWB;
-    if (lane == 0) bar_expect(full, boxes * bytes);
+    if (lead) bar_expect(full, __popc(set) * bytes * C::NH);
     __syncwarp();
-    if (mine)
-      tma_2d(saddr(tile + half * C::BLOCK + box * bytes), map, half * C::COLS,
-             (pg * a.Hkv + p.kvh) * a.P + k % a.P, full);
+    uint32_t dst = saddr(tile);
+#pragma unroll 4
+    for (int i = 0; i < boxes; ++i, dst += bytes) {
+      const int yi = __shfl_sync(0xffffffffu, y, i);
+      const uint32_t go = (set >> i & 1) ? lead : 0;
+#pragma unroll
+      for (int h = 0; h < C::NH; ++h) tma_2d(dst + h * C::BLOCK, map, h * C::COLS, yi, full, go);
+    }
   }
 };
 
@@ -547,22 +564,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t *base = (uint8_t *)(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   uint8_t *qs = base, *ks = qs + 2 * C::TILE, *vs = ks + C::STAGES * C::TILE;
   Smem *sm = (Smem *)(vs + C::STAGES * C::TILE);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0); /* uniform for the compiler too */
 
   if (tid == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
       bar_init(&sm->kfull[i], 1);
-      bar_init(&sm->kempty[i], 1);
+      bar_init(&sm->kempty[i], 2);
       bar_init(&sm->vfull[i], 1);
-      bar_init(&sm->vempty[i], 1);
+      bar_init(&sm->vempty[i], 2);
     }
     for (int s = 0; s < 2; ++s) {
       bar_init(&sm->sfull[s], 1);
-      bar_init(&sm->pready[s], 4);
+      bar_init(&sm->pready[s][0], 4);
+      bar_init(&sm->pready[s][1], 4);
       bar_init(&sm->qready[s], 4);
       bar_init(&sm->oready[s], 1);
+      bar_init(&sm->drain[s], 1);
+      for (int i = 0; i < kQueue; ++i) {
+        bar_init(&sm->qfull[s][i], 1);
+        bar_init(&sm->qempty[s][i], 5); /* the issuer, four softmax warps */
+      }
     }
-    bar_init(&sm->drain, 1);
     sm->abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -598,420 +621,391 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
   }
-  /* this worker's shares: of the pairs, and of the singles for each stream */
-  const int n_cta = gridDim.x;
-  int from[3] = {0, 0, 0}, to[3] = {0, 0, 0};
-  if (sound) {
-    const long long tp = sm->total[0], ts = sm->total[1];
-    const int c = blockIdx.x;
-    from[0] = (int)(c * tp / n_cta);
-    to[0] = (int)((c + 1) * tp / n_cta);
-    from[1] = (int)(2 * c * ts / (2 * n_cta));
-    to[1] = from[2] = (int)((2 * c + 1) * ts / (2 * n_cta));
-    to[2] = (int)((2 * c + 2) * ts / (2 * n_cta));
-  }
+  const long long n_cta = gridDim.x;
   const int TB = kTile / a.G; /* query tokens of a row tile */
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    const int s = warp & 1;
     if (warp < 10) {
-      /* ---- producers: of the pairs warp 8 loads K and warp 9 V; of the singles each
-       * loads both of its stream, K before V, the order in which the products need them */
-      const int s = warp - 8;
+      /* ---- producer of stream s.  It also takes the stream's pieces, some ahead: first the
+       * CTA's share of the pairs, the same for both, then the stream's share of the singles.
+       * Of the pairs stream 0's loads K and stream 1's loads V, into all slots; of the singles
+       * each loads both of its stream, K before V, the order in which the products need them. */
       Loader<D> ld(a, lane);
+      const uint32_t all = 2 * gridDim.x, me = 2 * blockIdx.x + s;
+      const unsigned long long tp = sound ? sm->total[0] : 0, ts = sound ? sm->total[1] : 0;
+      int x = (int)(blockIdx.x * tp / gridDim.x), end = (int)((blockIdx.x + 1) * tp / gridDim.x);
       uint32_t armed_k = 0, armed_v = 0; /* parities of each slot's next use */
       bool ok = true;
-      int it = 0;
-      for (int x = from[0]; ok && x < to[0];) {
-        const Piece p = next_tiles(a, sm, 0, x, to[0]);
-        ld.look_up(p, 0);
-        for (int t = 0; ok && t < p.n; ++t) {
-          const int page = ld.page, slot = it % C::STAGES;
-          ld.look_up(p, t + 1);
-          ok = warp_wait(s == 0 ? &sm->kempty[slot] : &sm->vempty[slot],
-                         ((it / C::STAGES) & 1) ^ 1, abort);
-          if (!ok) break;
-          ld.load(p, t, page, s == 0 ? &kmap : &vmap, (s == 0 ? ks : vs) + slot * C::TILE,
-                  s == 0 ? &sm->kfull[slot] : &sm->vfull[slot], lane);
-          ++it;
+      int line = 0, it = 0, ring = 0;
+      for (int put = 0; ok; ++put) {
+        Piece p;
+        p.n = 0;
+        while (p.n == 0 && line < 2) {
+          if (x < end) {
+            p = next_piece(a, sm, line, x, end);
+          } else if (++line == 1) {
+            x = (int)(me * ts / all);
+            end = (int)((me + 1) * ts / all);
+            for (int i = 0; i < C::STAGES; ++i) /* uses of each slot so far */
+              armed_k |= (uint32_t)(((it + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
+            armed_v = armed_k;
+          }
         }
-      }
-      /* uses of each slot so far: the other producer's too */
-      int pair_tiles = 0;
-      for (int x = from[0]; ok && x < to[0];) pair_tiles += next_tiles(a, sm, 0, x, to[0]).n;
-      for (int i = 0; i < C::STAGES; ++i)
-        armed_k |= (uint32_t)(((pair_tiles + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
-      armed_v = armed_k;
-      int ring = 0;
-      for (int x = from[1 + s]; ok && x < to[1 + s];) {
-        const Piece p = next_tiles(a, sm, 1, x, to[1 + s]);
+        const int qslot = put % kQueue;
+        ok = warp_wait(&sm->qempty[s][qslot], ((put / kQueue) & 1) ^ 1, abort);
+        if (!ok) break;
+        if (lane == 0) {
+          sm->queue[s][qslot] = p;
+          bar_arrive(&sm->qfull[s][qslot]);
+        }
+        __syncwarp();
+        if (p.n == 0) break;
         ld.look_up(p, 0);
+#pragma unroll 1
         for (int t = 0; ok && t < p.n; ++t) {
-          const int page = ld.page, slot = s * R + ring;
-          ring = ring + 1 == R ? 0 : ring + 1;
+          const int page = ld.page;
           ld.look_up(p, t + 1);
-          ok = warp_wait(&sm->kempty[slot], ((armed_k >> slot) & 1) ^ 1, abort);
-          if (!ok) break;
-          ld.load(p, t, page, &kmap, ks + slot * C::TILE, &sm->kfull[slot], lane);
-          armed_k ^= 1u << slot;
-          ok = warp_wait(&sm->vempty[slot], ((armed_v >> slot) & 1) ^ 1, abort);
-          if (!ok) break;
-          ld.load(p, t, page, &vmap, vs + slot * C::TILE, &sm->vfull[slot], lane);
-          armed_v ^= 1u << slot;
+          const int slot = line == 0 ? it % C::STAGES : s * R + ring;
+#pragma unroll 1
+          for (int kv = line == 0 ? s : 0; kv <= (line == 0 ? s : 1); ++kv) {
+            const uint32_t par = line == 0 ? it / C::STAGES : (kv ? armed_v : armed_k) >> slot;
+            ok = warp_wait(kv ? &sm->vempty[slot] : &sm->kempty[slot], (par & 1) ^ 1, abort);
+            if (!ok) break;
+            ld.load(p, t, page, kv ? &vmap : &kmap, (kv ? vs : ks) + slot * C::TILE,
+                    kv ? &sm->vfull[slot] : &sm->kfull[slot]);
+            if (line == 1) (kv ? armed_v : armed_k) ^= 1u << slot;
+          }
+          if (line == 0)
+            ++it;
+          else
+            ring = ring + 1 == R ? 0 : ring + 1;
         }
       }
       if (!ok) {
-        /* gave up: let the copies in flight land.  A slot that was filled and not yet
-         * consumed completes a phase; the parity before its next use names it. */
+        /* gave up: let the copies in flight land (each wait has its limit; a slot that
+         * was not filled since passes at once or by its earlier phase) */
         volatile int none = 0;
         for (int i = 0; i < C::STAGES; ++i) {
-          if (it > 0) {
-            const int last = it - 1 - (it - 1 - i + C::STAGES) % C::STAGES;
-            if (last >= 0)
-              warp_wait(s == 0 ? &sm->kfull[i] : &sm->vfull[i], (last / C::STAGES) & 1, &none);
-          }
-          if (i / R == s) {
-            if (from[1 + s] < to[1 + s] && ring >= 0) {
-              warp_wait(&sm->kfull[i], ((armed_k >> i) & 1) ^ 1, &none);
-              warp_wait(&sm->vfull[i], ((armed_v >> i) & 1) ^ 1, &none);
-            }
+          const int last = it - 1 - (it - 1 - i + 2 * C::STAGES) % C::STAGES;
+          if (line == 0 && it > 0 && last >= 0)
+            warp_wait(s == 0 ? &sm->kfull[i] : &sm->vfull[i], (last / C::STAGES) & 1, &none);
+          if (line > 0 && i / R == s) {
+            warp_wait(&sm->kfull[i], ((armed_k >> i) & 1) ^ 1, &none);
+            warp_wait(&sm->vfull[i], ((armed_v >> i) & 1) ^ 1, &none);
           }
         }
       }
-    } else if (warp == 10 && lane == 0) {
-      /* ---- issuer */
+    } else {
+      /* ---- issuer of stream s: S = Q K^T of a tile, then O += P V of its halves as P comes.
+       * The other stream's issuer fills the tensor cores meanwhile. */
       constexpr uint32_t id_qk = inst_desc(kTile, false), id_pv = inst_desc(D, true);
-      auto qk = [&](int s, int slot) {
-        const uint64_t q0 = mat_desc(saddr(qs + s * C::TILE), 16, 8 * C::ROWB, C::SWIZZLE);
-        const uint64_t k0 = mat_desc(saddr(ks + slot * C::TILE), 16, 8 * C::ROWB, C::SWIZZLE);
-#pragma unroll
-        for (int h = 0; h < C::NH; ++h)
-#pragma unroll
-          for (int c = 0; c < C::COLS / 16; ++c) {
-            const int o = (h * C::BLOCK + c * 32) >> 4;
-            mma_ss(tmem + s * kTile, q0 + o, k0 + o, id_qk, h + c > 0);
-          }
-      };
-      auto pv = [&](int s, int slot, bool acc) {
-        const uint64_t v0 = mat_desc(saddr(vs + slot * C::TILE), C::BLOCK, 8 * C::ROWB, C::SWIZZLE);
-#pragma unroll
-        for (int c = 0; c < kTile / 16; ++c)
-          mma_ts(tmem + 2 * kTile + s * kTile, tmem + s * kTile + c * 8,
-                 v0 + ((c * 16 * C::ROWB) >> 4), id_pv, acc || c > 0);
-      };
+      const uint32_t lead = elect_lead();
+      const uint32_t at_s = tmem + s * kTile, at_o = at_s + 2 * kTile;
+      const uint64_t q0 = mat_desc(saddr(qs + s * C::TILE), 16, 8 * C::ROWB, C::SWIZZLE);
+      const uint64_t k0 = mat_desc(saddr(ks), 16, 8 * C::ROWB, C::SWIZZLE);
+      const uint64_t v0 = mat_desc(saddr(vs), C::BLOCK, 8 * C::ROWB, C::SWIZZLE);
       bool ok = true;
-      uint32_t q_par = 0, p_par = 0, k_par = 0, v_par = 0; /* a bit per stream, slot */
-      int it = 0; /* pair tiles */
-      for (int x = from[0]; ok && x < to[0];) { /* pairs: both streams over the same K and V */
-        const int n = next_tiles(a, sm, 0, x, to[0]).n;
-        if (n == 0) break;
-        ok = bar_wait(&sm->qready[0], q_par & 1, abort) &&
-             bar_wait(&sm->qready[1], q_par & 1, abort);
+      int it = 0, ring = 0;
+      uint32_t par = 0, q_par = 0, p_par = 0; /* singles: parities of the stream's slots */
+      bool singles = false;
+      for (int got = 0;; ++got) {
+        const int qslot = got % kQueue;
+        ok = warp_wait(&sm->qfull[s][qslot], (got / kQueue) & 1, abort);
         if (!ok) break;
-        q_par ^= 3;
-        for (int t = 0; ok && t <= n; ++t) {
-          const int kslot = (it + t) % C::STAGES, vslot = (it + t - 1) % C::STAGES;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (ok && t > 0) {
-              if (s == 0) ok = bar_wait(&sm->vfull[vslot], (v_par >> vslot) & 1, abort);
-              ok = ok && bar_wait(&sm->pready[s], (p_par >> s) & 1, abort);
-              if (!ok) break;
-              p_par ^= 1u << s;
-              tc_fence_after();
-              pv(s, vslot, t > 1);
-              if (s == 1) {
-                tc_commit(&sm->vempty[vslot]);
-                v_par ^= 1u << vslot;
-              }
-              if (t == n) tc_commit(&sm->oready[s]);
-            }
-            if (ok && t < n) {
-              if (s == 0) ok = bar_wait(&sm->kfull[kslot], (k_par >> kslot) & 1, abort);
-              if (!ok) break;
-              tc_fence_after();
-              qk(s, kslot);
-              tc_commit(&sm->sfull[s]);
-              if (s == 1) {
-                tc_commit(&sm->kempty[kslot]);
-                k_par ^= 1u << kslot;
-              }
-            }
-          }
+        const int n = sm->queue[s][qslot].n, line = sm->queue[s][qslot].line;
+        __syncwarp();
+        if (lane == 0) bar_arrive(&sm->qempty[s][qslot]);
+        if (n == 0) break;
+        if (line == 1 && !singles) {
+          singles = true;
+          for (int i = 0; i < C::STAGES; ++i)
+            par |= (uint32_t)(((it + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
         }
-        it += n;
-      }
-      /* singles: whichever stream's next product is ready */
-      int left[2] = {0, 0}, done = 0, ring[2] = {0, 0};
-      bool want_pv[2] = {false, false}, fresh[2] = {false, false};
-      uint64_t since = 0;
-      for (int idle = 0; ok && done < 2;) {
-        bool moved = false;
+        ok = warp_wait(&sm->qready[s], q_par, abort);
+        if (!ok) break;
+        q_par ^= 1;
+#pragma unroll 1
+        for (int t = 0; t < n; ++t) {
+          const int slot = line == 0 ? it % C::STAGES : s * R + ring;
+          const uint32_t parity = (line == 0 ? it / C::STAGES : par >> slot) & 1;
+          const uint32_t o = (uint32_t)slot * (C::TILE >> 4);
+          ok = warp_wait(&sm->kfull[slot], parity, abort);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const int slot = s * R + ring[s];
-          if (left[s] < 0) continue;
-          if (left[s] == 0) { /* the next piece */
-            if (!bar_test(&sm->qready[s], (q_par >> s) & 1)) continue;
-            q_par ^= 1u << s;
-            left[s] = *(volatile int *)&sm->piece_tiles[s];
-            fresh[s] = true;
-            moved = true;
-            if (left[s] == 0) {
-              left[s] = -1;
-              ++done;
-              continue;
-            }
+          for (int c = 0; c < D / 16; ++c) {
+            const int oc = (c / (C::COLS / 16) * C::BLOCK + c % (C::COLS / 16) * 32) >> 4;
+            mma_ss(at_s, q0 + oc, k0 + o + oc, id_qk, c > 0, lead);
           }
-          if (!want_pv[s]) {
-            if (!bar_test(&sm->kfull[slot], (k_par >> slot) & 1)) continue;
-            k_par ^= 1u << slot;
+          tc_commit(&sm->sfull[s], lead);
+          /* a slot is free when both streams have read it: a single's reader counts twice */
+          tc_commit(&sm->kempty[slot], lead);
+          if (line == 1) tc_commit(&sm->kempty[slot], lead);
+          ok = warp_wait(&sm->vfull[slot], parity, abort);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && warp_wait(&sm->pready[s][h], p_par, abort);
+            if (!ok) break;
             tc_fence_after();
-            qk(s, slot);
-            tc_commit(&sm->sfull[s]);
-            tc_commit(&sm->kempty[slot]);
-            want_pv[s] = true;
-            moved = true;
+#pragma unroll
+            for (int c = h * (kTile / 32); c < (h + 1) * (kTile / 32); ++c)
+              mma_ts(at_o, at_s + c * 8, v0 + o + ((c * 16 * C::ROWB) >> 4), id_pv,
+                     t > 0 || c > 0, lead);
+          }
+          if (!ok) break;
+          p_par ^= 1;
+          if (t == n - 1) tc_commit(&sm->oready[s], lead);
+          tc_commit(&sm->vempty[slot], lead);
+          if (line == 1) tc_commit(&sm->vempty[slot], lead);
+          if (line == 0) {
+            ++it;
           } else {
-            if (!bar_test(&sm->vfull[slot], (v_par >> slot) & 1) ||
-                !bar_test(&sm->pready[s], (p_par >> s) & 1))
-              continue;
-            v_par ^= 1u << slot;
-            p_par ^= 1u << s;
-            tc_fence_after();
-            pv(s, slot, !fresh[s]);
-            fresh[s] = false;
-            tc_commit(&sm->vempty[slot]);
-            ring[s] = ring[s] + 1 == R ? 0 : ring[s] + 1;
-            want_pv[s] = false;
-            if (--left[s] == 0) tc_commit(&sm->oready[s]);
-            moved = true;
+            par ^= 1u << slot;
+            ring = ring + 1 == R ? 0 : ring + 1;
           }
         }
-        if (moved) {
-          idle = 0;
-          since = 0;
-        } else if ((++idle & 255) == 0) {
-          const uint64_t t = now_ns();
-          if (!since)
-            since = t;
-          else if (t - since > kWaitLimit)
-            *abort = 1;
-          if (*abort) ok = false;
-        }
+        if (!ok) break;
       }
       if (!ok) { /* gave up: let the products in flight end */
         volatile int none = 0;
-        tc_commit(&sm->drain);
-        bar_wait(&sm->drain, 0, &none);
+        tc_commit(&sm->drain[s], lead);
+        warp_wait(&sm->drain[s], 0, &none);
       }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     /* ---- softmax: stream s, one row a thread */
-    const int s = warp >> 2, r = tid & (kTile - 1);
+    const int s = warp >> 2, r = tid & (kTile - 1), w0 = (warp & 3) * 32;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21; /* this warp's TMEM lanes */
     const uint32_t at_s = tmem + lanes + s * kTile, at_o = at_s + 2 * kTile;
-    uint8_t *qd = qs + s * C::TILE + (warp & 3) * 32 * C::ROWB; /* this warp's rows of Q */
+    uint8_t *qd = qs + s * C::TILE + w0 * C::ROWB; /* this warp's rows of Q */
     const float c2 = a.scale_log2;
     uint32_t s_par = 0, o_par = 0;
     int it = 0, ring = 0;   /* pair tiles; this stream's slot */
     uint32_t v_par = 0;     /* parities of this stream's slots, set behind the pairs */
+    int got = 0;
     bool ok = true;
-    for (int line = 0; ok && line < 2; ++line) {
-      const bool pair = line == 0;
-      int x = pair ? from[0] : from[1 + s];
-      const int end = pair ? to[0] : to[1 + s];
-      if (!pair)
+    Piece p;
+    constexpr int PER = D / 8; /* 16-byte chunks of a row */
+    uint4 q[PER];
+    int tok0 = 0, rows = 0;
+    /* the next piece, and this warp's 32 rows of its Q on their way, zeros behind the last */
+    auto take = [&]() -> bool {
+      const int qslot = got % kQueue;
+      if (!warp_wait(&sm->qfull[s][qslot], (got / kQueue) & 1, abort)) return false;
+      ++got;
+      p = sm->queue[s][qslot];
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sm->qempty[s][qslot]);
+      tok0 = p.tok0 + (p.line == 0 ? s * TB : 0);
+      rows = p.n ? min(TB, p.tok0 + p.ntok - tok0) * a.G : 0;
+      int ln = lane;
+      asm volatile("" : "+r"(ln));
+      const __nv_bfloat16 *src = a.q + (long long)tok0 * a.q_stride + p.kvh * a.G * D + ln % PER * 8;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const int qr = w0 + ln / PER + i * (32 / PER), qt = (qr * a.inv_g) >> 16;
+        q[i] = make_uint4(0, 0, 0, 0);
+        if (qr < rows)
+          q[i] = __ldg((const uint4 *)(src + qt * a.q_stride + (qr - qt * a.G) * D));
+      }
+      return true;
+    };
+    ok = take();
+    while (ok && p.n) {
+      const bool pair = p.line == 0;
+      if (!pair && v_par >> 31 == 0) {
+        v_par = 1u << 31;
         for (int i = 0; i < C::STAGES; ++i)
           v_par |= (uint32_t)(((it + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
-      while (ok) {
-        const Piece p = next_tiles(a, sm, line, x, end);
-        if (pair && p.n == 0) break;
-        if (tid == s * kTile) *(volatile int *)&sm->piece_tiles[s] = p.n;
-        if (p.n == 0) {
-          __syncwarp();
-          if (lane == 0) bar_arrive(&sm->qready[s]);
-          break;
-        }
-        const int tok0 = p.tok0 + (pair ? s * TB : 0);
-        const int rows = min(TB, p.tok0 + p.ntok - tok0) * a.G;
-        /* this warp's 32 rows of Q into swizzled shared memory, zeros behind the last */
-        {
-          uint4 v[D / 8];
-          constexpr int PER = D / 8; /* 16-byte chunks of a row */
-          const int ch = lane % PER, r0 = (warp & 3) * 32 + lane / PER;
+      }
+      /* the lane again, so that addresses made of it are not kept across the pieces */
+      int ln = lane;
+      asm volatile("" : "+r"(ln));
+      /* Q into swizzled shared memory */
+      {
+        const int ch = ln % PER, hb = ch / (C::COLS / 8), cc = ch % (C::COLS / 8);
 #pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int qr = r0 + i * (32 / PER);
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (qr < rows) {
-              const int t = qr / a.G;
-              v[i] = __ldg((const uint4 *)(a.q + (tok0 + t) * a.q_stride +
-                                           (long long)(p.kvh * a.G + qr - t * a.G) * D + ch * 8));
-            }
-          }
-          const int hb = ch / (C::COLS / 8), cc = ch % (C::COLS / 8);
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const int qr = lane / PER + i * (32 / PER);
-            const int sw = D < 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
-            *(uint4 *)(qd + hb * C::BLOCK + qr * C::ROWB + sw * 16) = v[i];
-          }
+        for (int i = 0; i < PER; ++i) {
+          const int qr = ln / PER + i * (32 / PER);
+          const int sw = D < 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
+          *(uint4 *)(qd + hb * C::BLOCK + qr * C::ROWB + sw * 16) = q[i];
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&sm->qready[s]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sm->qready[s]);
 
-        const bool valid = r < rows, busy = (warp & 3) * 32 < rows;
-        const int tok = tok0 + (valid ? r / a.G : 0);
-        const int head = p.kvh * a.G + (valid ? r % a.G : 0);
-        const int b = p.own ? p.seq : a.off ? find(sm->off, a.n_seqs + 1, tok) : tok;
-        /* keys of the item that this row sees end here */
-        const int limit = min(p.kend, sm->len[b] - (sm->off[b + 1] - tok) + 1);
-        float m = -INFINITY, l = 0.0f; /* m in score units */
-        for (int t = 0; t < p.n; ++t) {
-          const int k0 = p.key0 + (p.t0 + t) * kTile;
-          ok = warp_wait(&sm->sfull[s], s_par, abort);
-          if (!ok) break;
-          s_par ^= 1;
-          tc_fence_after();
-          if (busy) {
-            float x[kTile];
-            tmem_ld128(at_s, x);
-            if (!__all_sync(0xffffffffu, limit >= k0 + kTile)) {
-#pragma unroll
-              for (int i = 0; i < kTile; ++i) x[i] = k0 + i < limit ? x[i] : -INFINITY;
-            }
-            float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int i = 4; i < kTile; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[i]);
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            if (t == 0) {
-              m = top;
-            } else {
-              const bool move = m == -INFINITY ? top > m : (top - m) * c2 > kSlack;
-              if (__any_sync(0xffffffffu, move)) {
-                /* the products into O so far are complete: they were issued before this S */
-                const float now = move ? top : m;
-                const float f = move ? exp2_approx((m - now) * c2) : 1.0f; /* m -inf: 0 */
+      const Piece c = p; /* the current piece: `take` moves on below */
+      const int ctok0 = tok0, crows = rows;
+      const bool valid = r < crows, busy = w0 < crows;
+      const int rt = valid ? (r * a.inv_g) >> 16 : 0, tok = ctok0 + rt;
+      const int b = c.own ? c.seq : a.off ? find(sm->off, a.n_seqs + 1, tok) : tok;
+      /* keys of the item that this row sees end here */
+      const int limit = min(c.kend, sm->len[b] - (sm->off[b + 1] - tok) + 1);
+      float m = -INFINITY, l = 0.0f; /* m in score units */
 #pragma unroll 1
-                for (int i = 0; i < D; i += 32) {
-                  float o[32];
-                  tmem_ld32(at_o + i, o);
-                  uint32_t w[32];
+      for (int t = 0; t < c.n; ++t) {
+        const int k0 = c.key0 + (c.t0 + t) * kTile;
+        ok = warp_wait(&sm->sfull[s], s_par, abort);
+        if (!ok) break;
+        s_par ^= 1;
+        tc_fence_after();
+        const int slot = pair ? it % C::STAGES : s * R + ring;
+        if (k0 + kTile > c.kend) {
+          /* zero the V rows behind the last key: what lies there may be NaN */
+          ok = warp_wait(&sm->vfull[slot], pair ? (it / C::STAGES) & 1 : (v_par >> slot) & 1,
+                         abort);
+          if (!ok) break;
+          if (k0 + r >= c.kend) {
+            uint8_t *vr = vs + slot * C::TILE + r * C::ROWB;
 #pragma unroll
-                  for (int k = 0; k < 32; ++k) w[k] = __float_as_uint(o[k] * f);
-                  tmem_st32(at_o + i, w);
-                }
-                l *= f;
-                m = now;
-              }
-            }
-            const float off = m == -INFINITY ? 0.0f : -m * c2;
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[32];
-#pragma unroll
-              for (int k = 0; k < 32; ++k) {
-                const float e0 = exp2_approx(fmaf(x[h * 64 + 2 * k], c2, off));
-                const float e1 = exp2_approx(fmaf(x[h * 64 + 2 * k + 1], c2, off));
-                sum[k & 1] += e0;
-                sum[2 + (k & 1)] += e1;
-                w[k] = pack_bf16(e0, e1);
-              }
-              tmem_st32(at_s + h * 32, w);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_wait_st();
+            for (int i = 0; i < D / 8; ++i)
+              *(uint4 *)(vr + i / (C::COLS / 8) * C::BLOCK + i % (C::COLS / 8) * 16) =
+                  make_uint4(0, 0, 0, 0);
           }
-          const int slot = pair ? it % C::STAGES : s * R + ring;
-          if (k0 + kTile > p.kend) {
-            /* zero the V rows behind the last key: what lies there may be NaN */
-            ok = warp_wait(&sm->vfull[slot],
-                           pair ? (it / C::STAGES) & 1 : (v_par >> slot) & 1, abort);
-            if (!ok) break;
-            if (k0 + r >= p.kend) {
-              uint8_t *vr = vs + slot * C::TILE + r * C::ROWB;
+          fence_async_smem();
+        }
+        if (pair) {
+          ++it;
+        } else {
+          v_par ^= 1u << slot;
+          ring = ring + 1 == R ? 0 : ring + 1;
+        }
+        if (!busy) {
+          __syncwarp();
+          if (lane == 0) {
+            bar_arrive(&sm->pready[s][0]);
+            bar_arrive(&sm->pready[s][1]);
+          }
+          continue;
+        }
+        float x[kTile];
+        tmem_ld128(at_s, x);
+        if (!__all_sync(0xffffffffu, limit >= k0 + kTile)) {
+          const int d = limit - k0;
 #pragma unroll
-              for (int i = 0; i < D / 8; ++i)
-                *(uint4 *)(vr + i / (C::COLS / 8) * C::BLOCK + i % (C::COLS / 8) * 16) =
-                    make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < kTile; ++i) x[i] = i < d ? x[i] : -INFINITY;
+        }
+        float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+        for (int i = 4; i < kTile; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mx[k] = i + k + 4 < kTile ? fmaxf(mx[k], fmaxf(x[i + k], x[i + k + 4]))
+                                      : fmaxf(mx[k], x[i + k]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        if (t == 0) {
+          m = top;
+        } else {
+          const bool move = m == -INFINITY ? top > m : (top - m) * c2 > kSlack;
+          if (__any_sync(0xffffffffu, move)) {
+            /* the products into O so far are complete: they were issued before this S */
+            const float now = move ? top : m;
+            const float f = move ? exp2_approx((m - now) * c2) : 1.0f; /* m -inf: 0 */
+#pragma unroll 1
+            for (int i = 0; i < D; i += 16) {
+              float o[16];
+              tmem_ld16(at_o + i, o);
+              uint32_t w[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(o[k] * f);
+              tmem_st16(at_o + i, w);
             }
-            fence_async_smem();
+            l *= f;
+            m = now;
           }
-          if (pair) {
-            ++it;
-          } else {
-            v_par ^= 1u << slot;
-            ring = ring + 1 == R ? 0 : ring + 1;
+        }
+        const float off = m == -INFINITY ? 0.0f : -m * c2;
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        /* P in two halves: the product of the first starts under the second */
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            float2 e = fma2(make_float2(x[h * 64 + 2 * k], x[h * 64 + 2 * k + 1]),
+                            make_float2(c2, c2), make_float2(off, off));
+            e.x = exp2_approx(e.x);
+            e.y = exp2_approx(e.y);
+            sum[k & 1] = add2(sum[k & 1], e);
+            w[k] = pack_bf16(e.x, e.y);
           }
+          tmem_st32(at_s + h * 32, w);
+          tmem_wait_st();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive(&sm->pready[s]);
+          if (lane == 0) bar_arrive(&sm->pready[s][h]);
         }
-        if (!ok) break;
-        ok = warp_wait(&sm->oready[s], o_par, abort);
-        if (!ok) break;
-        o_par ^= 1;
-        tc_fence_after();
-        if (busy) {
-          /* rows of O through this warp's part of Q (read by now), so that a row's
-           * columns are written together */
-          const bool whole = p.own && p.key0 == 0 && p.n == p.nt; /* nothing to merge */
-          const long long orow = (long long)tok * a.Hq + head;
-          const long long extra = 2ll * a.n_tokens * a.Hq +
-                                  (pair ? 2ll * blockIdx.x + s
-                                        : 2ll * n_cta + 2ll * blockIdx.x + s) * kTile;
-          const long long prow = p.t0 == 0 ? (long long)p.own * a.n_tokens * a.Hq + orow : extra + r;
-          const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-          constexpr int W = D / 2;            /* columns staged at a time */
-          constexpr int RL = W / 4, RI = 32 / RL; /* lanes of a row, rows at a time */
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      }
+      if (!ok) break;
+      ok = take(); /* under the last product */
+      if (!ok) break;
+      ok = warp_wait(&sm->oready[s], o_par, abort);
+      if (!ok) break;
+      o_par ^= 1;
+      tc_fence_after();
+      if (busy) {
+        /* rows of O through this warp's part of Q (read by now), so that a row's
+         * columns are written together */
+        const bool whole = c.own && c.key0 == 0 && c.n == c.nt; /* nothing to merge */
+        const int row0 = ctok0 * a.Hq + c.kvh * a.G;    /* output row of (token, head) 0 */
+        const long long dense = (long long)a.n_tokens * a.Hq;
+        const long long extra =
+            2 * dense + (pair ? 2ll * blockIdx.x + s : 2ll * n_cta + 2ll * blockIdx.x + s) * kTile;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        constexpr int W = D / 2, CR = C::ROWB / 16; /* columns staged at a time; float4 of a swizzled row */
+        constexpr int RL = W / 4, RI = 32 / RL;     /* lanes of a row, rows at a time */
+        constexpr int LW = W < 32 ? 16 : 32;
 #pragma unroll 1
-          for (int i0 = 0; i0 < D; i0 += W) {
+        for (int i0 = 0; i0 < D; i0 += W) {
 #pragma unroll
-            for (int i = 0; i < W; i += 16) {
-              float o[16];
+          for (int i = 0; i < W; i += LW) {
+            float o[LW];
+            if (LW == 32)
+              tmem_ld32(at_o + i0 + i, o);
+            else
               tmem_ld16(at_o + i0 + i, o);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int c = i / 4 + k; /* float4 of the row, 8 (4) to a swizzled row */
-                constexpr int CR = C::ROWB / 16;
-                *(float4 *)(qd + c / CR * C::BLOCK + lane * C::ROWB +
-                            ((c % CR) ^ (lane & (CR - 1))) * 16) =
-                    make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-              }
+            for (int k = 0; k < LW / 4; ++k) {
+              const int ch = i / 4 + k;
+              *(float4 *)(qd + ch / CR * C::BLOCK + ln * C::ROWB +
+                          ((ch % CR) ^ (ln & (CR - 1))) * 16) =
+                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 32 / RI; ++i) {
-              const int row = i * RI + lane / RL, c = lane % RL;
-              constexpr int CR = C::ROWB / 16;
-              const float4 o = *(const float4 *)(qd + c / CR * C::BLOCK + row * C::ROWB +
-                                                 ((c % CR) ^ (row & (CR - 1))) * 16);
-              const long long pr = __shfl_sync(0xffffffffu, prow, row);
-              const long long dr = __shfl_sync(0xffffffffu, orow, row);
-              const float f = __shfl_sync(0xffffffffu, inv, row);
-              if ((warp & 3) * 32 + row < rows) {
-                if (whole)
-                  *(uint2 *)(a.out + dr * D + i0 + c * 4) =
-                      make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
-                else
-                  *(float4 *)(a.part + pr * D + i0 + c * 4) = o;
-              }
+          }
+          __syncwarp();
+          const int ch = ln % RL;
+#pragma unroll 2
+          for (int i = 0; i < 32 / RI; ++i) {
+            const int row = i * RI + ln / RL, rr = w0 + row, qt = (rr * a.inv_g) >> 16;
+            const float4 o = *(const float4 *)(qd + ch / CR * C::BLOCK + row * C::ROWB +
+                                               ((ch % CR) ^ (row & (CR - 1))) * 16);
+            const long long dr = row0 + (long long)qt * a.Hq + (rr - qt * a.G);
+            const float f = __shfl_sync(0xffffffffu, inv, row);
+            if (rr < crows) {
+              if (whole)
+                *(uint2 *)(a.out + dr * D + i0 + ch * 4) =
+                    make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+              else
+                *(float4 *)(a.part + (c.t0 ? extra + rr : c.own * dense + dr) * D + i0 + ch * 4) = o;
             }
-            __syncwarp();
           }
-          if (valid && whole) {
-            if (a.lse)
-              a.lse[orow] = l > 0.0f ? (m * c2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
-          } else if (valid) {
-            a.part_ml[prow] = make_float2(m == -INFINITY ? m : m * c2, l);
-          }
+          __syncwarp();
         }
-        tc_fence_before();
+        const long long orow = row0 + (long long)rt * a.Hq + (r - rt * a.G);
+        if (valid && whole) {
+          if (a.lse)
+            a.lse[orow] = l > 0.0f ? (m * c2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        } else if (valid) {
+          a.part_ml[c.t0 ? extra + r : c.own * dense + orow] =
+              make_float2(m == -INFINITY ? m : m * c2, l);
+        }
       }
+      tc_fence_before();
     }
   }
   __syncthreads();
@@ -1316,6 +1310,7 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   a.out = (__nv_bfloat16 *)out;
   a.lse = lse;
   a.scale_log2 = at->scale_log2;
+  a.inv_g = (65536 + a.G - 1) / a.G;
   a.err_host = at->err_dev;
   a.sched = (int32_t *)at->ws;
   a.part = (float *)(at->ws + at->o_part);
