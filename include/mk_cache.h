@@ -107,7 +107,7 @@ typedef struct {
   int32_t n_q_heads, n_kv_heads, head_dim;   /* as mk_create; n_q_heads / n_kv_heads <= 64 */
   int32_t page_size, num_pages;              /* page_size a multiple of 16, at most 256 */
   int32_t max_tokens;                        /* query tokens of a call, at most 2^20 */
-  int32_t max_seqs, max_groups;              /* of a call, at most 1024 each */
+  int32_t max_seqs, max_groups;              /* of a call, at most 1024 and 512 */
   int32_t n_layers;
   const void *const *k_caches;               /* HOST arrays [n_layers] of DEVICE pools */
   const void *const *v_caches;

@@ -142,7 +142,7 @@ class PrefixAttention:
     (it sizes the workspace).  scale: of the scores, None for 1 / sqrt(head_dim)."""
 
     def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, layers,
-                 max_tokens: int, max_seqs: int = 1024, max_groups: int = 1024,
+                 max_tokens: int, max_seqs: int = 1024, max_groups: int = 512,
                  scale: float = None, stream=None):
         import torch
 

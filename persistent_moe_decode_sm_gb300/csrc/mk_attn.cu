@@ -5,21 +5,21 @@
  * The work is cut into tiles of 128 keys.  An item is a range of keys that a
  * set of query rows reads: a group's shared pages with the rows (query tokens x
  * heads of one kv head) of the group's sequences, or one sequence's own pages
- * with that sequence's rows.  Items of more than 128 rows (up to 256: pairs) and
- * items of at most 128 rows (singles) lie end to end on a line each, and each
- * line is cut evenly, the pairs over the SMs and the singles over twice as many
- * streams.  A share may begin and end inside an item; every piece leaves a
- * partial (maximum, sum, weighted sum) per row, and attn_merge joins them.  The
- * cut follows from the lengths on the device: each CTA takes it itself, so that
- * a captured call follows its batch.
+ * with that sequence's rows.  Items of more than 128 rows (up to 256: pairs), then
+ * items of at most 128 rows (singles) lie end to end on a line, each as long as
+ * its tiles and a fixed cost, and the line is cut evenly over the SMs.  An SM's
+ * share may begin and end inside an item; every piece leaves a partial (maximum,
+ * sum, weighted sum) per row, and attn_merge joins them.  The cut follows from
+ * the lengths on the device: each CTA takes it itself, so that a captured call
+ * follows its batch.
  *
  * attn_tiles, one CTA per SM: producer warps move K and V tiles with TMA, one box
  * per page and 64 dims, into swizzled shared memory; issuing warps start S = Q K^T
  * and O += P V on the tensor cores (tcgen05, 128 rows, accumulators in TMEM); two
  * warpgroups, the streams, turn S into P, one row a thread, P going back to TMEM
  * as the A operand.  A pair's two row tiles run on the two streams over the same
- * K and V; of the singles each stream has its own share.  Either way one stream's
- * softmax, and its piece's beginning and end, run under the other's products.
+ * K and V; of the CTA's singles each stream has its own half.  Either way one
+ * stream's softmax runs under the other's products.
  */
 #include <cuda.h> /* tensor-map types; the encoder is reached through the runtime */
 #include <cuda_bf16.h>
@@ -39,15 +39,16 @@ namespace {
 constexpr int kThreads = 384;      /* two softmax warpgroups, two producers, two issuers */
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88; /* 256 * 208 + 128 * 88 = 384 * 168 */
 constexpr int kTile = 128;         /* keys per tile; rows per row tile */
-constexpr int kItemCost = 2;       /* what an item's beginning and end cost, in tiles */
+constexpr int kPairCost = 3, kSingleCost = 2; /* an item's beginning and end, in tiles */
 constexpr int kQueue = 4;          /* pieces that a producer is ahead of its stream */
-constexpr int kMaxSeqs = 1024;     /* of a call: the cut's tables are in shared memory */
+constexpr int kMaxSeqs = 1024, kMaxGroups = 512; /* of a call: the cut's tables are in shared memory */
 constexpr uint64_t kWaitLimit = 2000000000ull; /* ns */
 /* The running maximum moves only when a score exceeds it by this much (in powers
  * of two): P then stays below 2^8, exact in its relative precision, and the
  * accumulator is rescaled a few times per row rather than in most tiles. */
 constexpr float kSlack = 8.0f;
 constexpr int kSchedStride = kMaxSeqs + 1;
+constexpr int kFewRows = 4096; /* up to this many output rows attn_merge has a block for each */
 
 struct Args {
   int32_t Hq, Hkv, G, P, num_pages, max_pages, n_seqs, n_tokens, n_groups, box_rows;
@@ -57,12 +58,14 @@ struct Args {
   __nv_bfloat16 *out;
   float *lse;
   float scale_log2; /* scale * log2(e) */
+  int32_t TB;       /* query tokens of a row tile: 128 / G */
   uint32_t inv_g;   /* ceil(2^16 / G): r * inv_g >> 16 is r / G for r < 128 */
+  unsigned long long inv_p; /* ceil(2^38 / P): k * inv_p >> 38 is k / P for k < 2^30 */
   int32_t *err_host;
   /* workspace */
-  int32_t *sched;    /* the cut, for attn_merge: [0] bad, [1] [2] the lines' lengths, then
-                      * kSchedStride each: the groups' and the sequences' beginnings on the
-                      * pairs' line, on the singles' line, the groups' shared keys */
+  int32_t *sched;    /* the cut, for attn_merge: [0] bad, [1] the line's length, [2] where its
+                      * singles begin, then kSchedStride each: the groups' and the sequences'
+                      * beginnings among the pairs, among the singles, the groups' shared keys */
   float *part;       /* [2 * n_tokens * Hq + 4 * SMs * 128][D] weighted sums */
   float2 *part_ml;   /* the same rows: maximum (in powers of two), sum */
 };
@@ -96,12 +99,12 @@ struct Smem { /* behind the tiles */
   Piece queue[2][kQueue];
   uint32_t tmem;
   int abort;
-  unsigned long long sums[kThreads / 32];
-  int total[2];       /* length of the pairs' line, of the singles' */
+  unsigned long long sums[2][kThreads / 32];
+  int total, pairs;   /* length of the line, of its pairs */
   int32_t off[kMaxSeqs + 1], len[kMaxSeqs];
-  int32_t cum_g[2][kMaxSeqs + 1], cum_s[2][kMaxSeqs + 1]; /* beginnings on the two lines */
-  int32_t plen[kMaxSeqs];
-  uint16_t gs[kMaxSeqs + 1], lead[kMaxSeqs]; /* a group's first sequence, its first that reads */
+  int32_t cum_s[2][kMaxSeqs + 1], cum_g[2][kMaxGroups + 1]; /* beginnings: pairs, singles */
+  int32_t plen[kMaxGroups], lead[kMaxGroups]; /* a group's prefix, its first sequence that reads */
+  uint16_t gs[kMaxGroups + 1];                /* a group's first sequence */
 };
 
 /* ---- PTX -------------------------------------------------------------------- */
@@ -293,34 +296,43 @@ __host__ __device__ constexpr uint32_t inst_desc(int n, bool b_n_major) {
 
 /* ---- the cut ------------------------------------------------------------------ */
 
-__host__ __device__ __forceinline__ int div_up(int a, int b) { return (a + b - 1) / b; }
-
 /* Query tokens come in blocks of two row tiles.  T tokens: this many blocks have
  * more than one row tile (pairs); a last one may have one (a single). */
 __device__ __forceinline__ int pair_blocks(int T, int TB) {
-  return T / (2 * TB) + (T % (2 * TB) > TB);
+  if (T <= TB) return 0;
+  const int n = T / (2 * TB);
+  return n + (T - n * 2 * TB > TB);
 }
-__device__ __forceinline__ bool has_single(int T, int TB) {
-  const int r = T % (2 * TB);
-  return r > 0 && r <= TB;
+__device__ __forceinline__ bool has_single(int T, int TB, int pairs) {
+  return T > pairs * 2 * TB; /* else the last pair holds the rest */
 }
 /* Keys that the last token of block j of a sequence sees. */
 __device__ __forceinline__ int block_end(int len, int T, int TB, int j) {
   return min(len, len - T + min(T, (j + 1) * 2 * TB));
 }
 __device__ __forceinline__ int key_tiles(int begin, int end) {
-  return end > begin ? div_up(end - begin, kTile) : 0;
+  return end > begin ? (end - begin + kTile - 1) / kTile : 0;
 }
-__device__ __forceinline__ int item_cost(int tiles) { return tiles ? tiles + kItemCost : 0; }
-/* The worker that owns place x of a line cut over n: worker w owns
- * [w total / n, (w + 1) total / n), so it is the largest w with w total < (x + 1) n.
- * An estimate in 32 bits is off by less than one. */
-__device__ __forceinline__ int worker_of(int x, int total, int n) {
+__device__ __forceinline__ int fixed_cost(int line) { return line ? kSingleCost : kPairCost; }
+__device__ __forceinline__ int item_cost(int line, int tiles) {
+  return tiles ? tiles + fixed_cost(line) : 0;
+}
+/* CTAs that take part: each has two places of the line at least, one a stream. */
+__device__ __forceinline__ int active_ctas(int total, int n_cta) {
+  return max(1, min(n_cta, total >> 1));
+}
+/* Where CTA c's share of the line begins. */
+__device__ __forceinline__ int share_begin(int c, int total, int n) {
+  return (int)((unsigned long long)c * (unsigned)total / (unsigned)n);
+}
+/* The CTA that owns place x: the largest c with c total < (x + 1) n.  An estimate in
+ * 32 bits is off by less than one. */
+__device__ __forceinline__ int cta_of(int x, int total, int n) {
   const long long y = ((long long)x + 1) * n;
-  int w = (int)__fdividef((float)y, (float)total);
-  while ((long long)w * total >= y) --w;
-  while (((long long)w + 1) * total < y) ++w;
-  return w;
+  int c = (int)__fdividef((float)y, (float)total);
+  while ((long long)c * total >= y) --c;
+  while (((long long)c + 1) * total < y) ++c;
+  return c;
 }
 /* Last i in [0, n) with a[i] <= x (a not decreasing, a[0] <= x). */
 template <class T>
@@ -335,182 +347,225 @@ __device__ __forceinline__ int find(const T *a, int n, int x) {
   }
   return lo;
 }
+/* The same by a whole warp: 32 places a round, so one or two loads deep. */
+template <class T>
+__device__ __forceinline__ int warp_find(const T *a, int n, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, len = n; /* the answer is in [lo, lo + len) */
+  while (len > 1) {
+    const int step = (len + 31) >> 5, i = lane * step;
+    const unsigned le = __ballot_sync(0xffffffffu, i < len && (int)a[lo + i] <= x);
+    const int k = 31 - __clz(le | 1u);
+    lo += k * step;
+    len = min(step, len - k * step);
+  }
+  return lo;
+}
 
-/* Exclusive prefix sums over the CTA, two 32-bit counts in one word. */
-__device__ unsigned long long cta_scan(unsigned long long v, Smem *sm, unsigned long long *total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o *= 2) {
-    const unsigned long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sm->sums[warp] = x;
-  __syncthreads();
-  unsigned long long before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sm->sums[w];
-    all += sm->sums[w];
-  }
-  *total = all;
-  __syncthreads();
-  return before + x - v;
+/* A group's shared keys: whole pages that every one of its sequences with something
+ * to read has; a group of one reads them with its own. */
+__device__ __forceinline__ int shared_keys(const Args &a, const Smem *sm, int g) {
+  if ((int)sm->gs[g + 1] - sm->lead[g] < 2) return 0;
+  return (int)(((unsigned long long)sm->plen[g] * a.inv_p) >> 38) * a.P;
 }
 __device__ __forceinline__ unsigned long long two(int pairs, int singles) {
   return (unsigned long long)(unsigned)pairs << 32 | (unsigned)singles;
 }
 
 /* Loads and checks the batch and cuts it.  False (for the whole CTA, and every
- * CTA alike) if it is not sound. */
+ * CTA alike) if it is not sound.  Most of its time goes to fetching its own
+ * instructions and to its chain of loads, so it is short code with few barriers
+ * rather than fast code: 384 entries a turn, one turn for most batches. */
 __device__ bool take_cut(const Args &a, Smem *sm) {
-  constexpr int N = (kMaxSeqs + kThreads) / kThreads; /* entries a thread: all loads at once */
-  const int tid = threadIdx.x, TB = kTile / a.G;
-  const int ns = a.n_seqs, ng = a.n_groups;
-  const long long cap = (long long)a.max_pages * a.P;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ns = a.n_seqs, ng = a.n_groups, TB = a.TB;
+  const int turns = (max(ns, ng) + kThreads) / kThreads; /* ns + 1 offsets */
   bool bad = false;
-  {
-    int l[N], o[N], g[N], p[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int i = tid + k * kThreads;
-      l[k] = i < ns ? a.lens[i] : 0;
-      o[k] = !a.off ? i : i <= ns ? a.off[i] : 0;
-      g[k] = i <= ng && ng ? a.starts[i] : 0;
-      p[k] = i < ng ? a.prefix[i] : 0;
+#pragma unroll 1
+  for (int k = 0; k < turns; ++k) {
+    const int i = tid + k * kThreads;
+    int l = 0, o = i, o1 = i + 1, g = 0, g1 = 0, p = 0;
+    if (i < ns) l = a.lens[i];
+    if (a.off && i <= ns) {
+      o = a.off[i];
+      if (i < ns) o1 = a.off[i + 1];
     }
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int i = tid + k * kThreads;
-      bad |= l[k] < 0 || l[k] > cap || p[k] < 0 || g[k] < 0 || g[k] > ns;
-      if (i < ns) sm->len[i] = l[k];
-      if (i <= ns) sm->off[i] = o[k];
-      if (i <= ng) sm->gs[i] = (uint16_t)g[k];
+    if (ng && i <= ng) {
+      g = a.starts[i];
       if (i < ng) {
-        sm->plen[i] = p[k];
-        sm->lead[i] = (uint16_t)ns;
+        g1 = a.starts[i + 1];
+        p = a.prefix[i];
       }
     }
+    if (i < ns) {
+      bad |= l < 0 || l > (long long)a.max_pages * a.P || o1 < o;
+      sm->len[i] = l;
+    }
+    if (i <= ns) {
+      bad |= (i == 0 && o != 0) || (i == ns && o > a.n_tokens);
+      sm->off[i] = o;
+    }
+    if (i <= ng) {
+      bad |= (i == 0 && g != 0) || (i == ng && ng && g != ns) || (i < ng && (g1 < g || p < 0));
+      sm->gs[i] = (uint16_t)g;
+    }
+    if (i < ng) {
+      sm->plen[i] = p;
+      sm->lead[i] = ns;
+    }
   }
-  __syncthreads();
-  for (int i = tid; i < ns; i += kThreads) bad |= sm->off[i + 1] < sm->off[i];
-  for (int i = tid; i < ng; i += kThreads) bad |= sm->gs[i + 1] < sm->gs[i];
-  if (tid == 0)
-    bad |= sm->off[0] != 0 || sm->off[ns] > a.n_tokens || (ng && (sm->gs[0] != 0 || sm->gs[ng] != ns));
   if (__syncthreads_or(bad)) return false;
-  /* shared keys: whole pages that every sequence with something to read has; a
-   * group of one reads them with its own */
   if (ng) {
+#pragma unroll 1
     for (int i = tid; i < ns; i += kThreads)
       if (sm->len[i] > 0 && sm->off[i + 1] > sm->off[i]) {
         const int g = find(sm->gs, ng + 1, i);
         atomicMin(&sm->plen[g], sm->len[i]);
-        /* the first that reads: the lowest index behind which none of the group reads */
-        bool first = true;
-        for (int j = sm->gs[g]; first && j < i; ++j)
-          first = !(sm->len[j] > 0 && sm->off[j + 1] > sm->off[j]);
-        if (first) sm->lead[g] = (uint16_t)i;
+        atomicMin(&sm->lead[g], i);
       }
     __syncthreads();
-    for (int i = tid; i < ng; i += kThreads)
-      sm->plen[i] = (int)sm->gs[i + 1] - sm->lead[i] < 2 ? 0 : sm->plen[i] / a.P * a.P;
-    __syncthreads();
   }
-  unsigned long long base = 0;
-  for (int i0 = 0; i0 < ng; i0 += kThreads) {
-    const int i = i0 + tid;
-    unsigned long long cost = 0;
+  /* lengths of the groups' and of the sequences' items, pairs and singles, summed up */
+  unsigned long long base_g = 0, base_s = 0;
+#pragma unroll 1
+  for (int k = 0; k < turns; ++k) {
+    const int i = tid + k * kThreads;
+    unsigned long long vg = 0, vs = 0;
     if (i < ng) {
       const int T = sm->off[sm->gs[i + 1]] - sm->off[sm->gs[i]];
-      const int c = a.Hkv * item_cost(key_tiles(0, sm->plen[i]));
-      cost = two(pair_blocks(T, TB) * c, has_single(T, TB) ? c : 0);
+      const int nt = key_tiles(0, shared_keys(a, sm, i)), nb = pair_blocks(T, TB);
+      vg = two(nb * a.Hkv * item_cost(0, nt), has_single(T, TB, nb) ? a.Hkv * item_cost(1, nt) : 0);
     }
-    unsigned long long total;
-    const unsigned long long at = base + cta_scan(cost, sm, &total);
-    if (i < ng) {
-      sm->cum_g[0][i] = (int)(at >> 32);
-      sm->cum_g[1][i] = (int)at;
-    }
-    base += total;
-  }
-  if (tid == 0) {
-    sm->cum_g[0][ng] = (int)(base >> 32);
-    sm->cum_g[1][ng] = (int)base;
-  }
-  for (int i0 = 0; i0 < ns; i0 += kThreads) {
-    const int i = i0 + tid;
-    unsigned long long cost = 0;
     if (i < ns) {
       const int T = sm->off[i + 1] - sm->off[i], len = sm->len[i];
-      const int start = ng ? sm->plen[find(sm->gs, ng + 1, i)] : 0, nb = pair_blocks(T, TB);
+      const int start = ng ? shared_keys(a, sm, find(sm->gs, ng + 1, i)) : 0;
+      const int nb = pair_blocks(T, TB);
       int pairs = 0, singles = 0;
-      for (int j = 0; j < nb; ++j) pairs += item_cost(key_tiles(start, block_end(len, T, TB, j)));
-      if (has_single(T, TB)) singles = item_cost(key_tiles(start, block_end(len, T, TB, nb)));
-      cost = two(pairs * a.Hkv, singles * a.Hkv);
+#pragma unroll 1
+      for (int j = 0; j < nb; ++j) pairs += item_cost(0, key_tiles(start, block_end(len, T, TB, j)));
+      if (has_single(T, TB, nb)) singles = item_cost(1, key_tiles(start, block_end(len, T, TB, nb)));
+      vs = two(pairs * a.Hkv, singles * a.Hkv);
     }
-    unsigned long long total;
-    const unsigned long long at = base + cta_scan(cost, sm, &total);
-    if (i < ns) {
-      sm->cum_s[0][i] = (int)(at >> 32);
-      sm->cum_s[1][i] = (int)at;
+    unsigned long long xg = vg, xs = vs;
+#pragma unroll 1
+    for (int o = 1; o < 32; o *= 2) {
+      const unsigned long long yg = __shfl_up_sync(0xffffffffu, xg, o);
+      const unsigned long long ys = __shfl_up_sync(0xffffffffu, xs, o);
+      if (lane >= o) {
+        xg += yg;
+        xs += ys;
+      }
     }
-    base += total;
+    if (lane == 31) {
+      sm->sums[0][warp] = xg;
+      sm->sums[1][warp] = xs;
+    }
+    __syncthreads();
+    xg += base_g - vg;
+    xs += base_s - vs;
+#pragma unroll 4
+    for (int w = 0; w < kThreads / 32; ++w) {
+      const unsigned long long g = sm->sums[0][w], q = sm->sums[1][w];
+      if (w < warp) {
+        xg += g;
+        xs += q;
+      }
+      base_g += g;
+      base_s += q;
+    }
+    if (i <= ng) {
+      sm->cum_g[0][i] = (int)(xg >> 32);
+      sm->cum_g[1][i] = (int)xg;
+    }
+    if (i <= ns) { /* behind the groups': added by the reader */
+      sm->cum_s[0][i] = (int)(xs >> 32);
+      sm->cum_s[1][i] = (int)xs;
+    }
+    __syncthreads();
   }
   if (tid == 0) {
-    sm->cum_s[0][ns] = sm->total[0] = (int)(base >> 32);
-    sm->cum_s[1][ns] = sm->total[1] = (int)base;
+    sm->pairs = (int)(base_g >> 32) + (int)(base_s >> 32);
+    sm->total = sm->pairs + (int)base_g + (int)base_s;
   }
   __syncthreads();
   return true;
 }
 
-/* The piece at place x of a line, x < end; x moves behind it.  A share that ends
- * within an item's fixed cost has no tile of it: n is 0. */
-__device__ Piece next_piece(const Args &a, const Smem *sm, int line, int &x, int end) {
-  const int TB = kTile / a.G;
+/* The piece at place x of the pairs (line 0) or the singles (1), x < end; x moves
+ * behind it.  A share that ends within an item's fixed cost has no tile of it: n is
+ * 0.  By a whole warp. */
+__device__ __forceinline__ Piece next_piece(const Args &a, const Smem *sm, int line, int &x, int end) {
+  const int TB = a.TB, ng = a.n_groups, fixed = fixed_cost(line);
+  const int in_groups = sm->cum_g[line][ng];
   Piece p;
   p.line = line;
-  int j, begin; /* the item's block, its place */
-  if (x < sm->cum_g[line][a.n_groups]) {
-    const int g = find(sm->cum_g[line], a.n_groups, x);
-    const int first = sm->off[sm->gs[g]], T = sm->off[sm->gs[g + 1]] - first;
-    p.own = 0;
+  p.own = x >= in_groups;
+  int j, begin, first, T; /* the item's block, its place; the block's tokens */
+  if (!p.own) {
+    const int g = warp_find(sm->cum_g[line], ng, x);
+    first = sm->off[sm->gs[g]];
+    T = sm->off[sm->gs[g + 1]] - first;
     p.seq = sm->lead[g];
     p.key0 = 0;
-    p.kend = sm->plen[g];
+    p.kend = shared_keys(a, sm, g);
     p.nt = key_tiles(0, p.kend);
-    const int nb = pair_blocks(T, TB), per = line == 0 ? nb : 1, cost = item_cost(p.nt);
-    const int item = (x - sm->cum_g[line][g]) / cost;
-    begin = sm->cum_g[line][g] + item * cost;
-    p.kvh = item / per;
-    j = line == 0 ? item - p.kvh * per : nb;
-    p.tok0 = first + j * 2 * TB;
-    p.ntok = min(2 * TB, T - j * 2 * TB);
+    const int nb = pair_blocks(T, TB);
+    begin = sm->cum_g[line][g];
+    const int item = (x - begin) / (p.nt + fixed);
+    begin += item * (p.nt + fixed);
+    p.kvh = line == 0 ? item / nb : item;
+    j = line == 0 ? item - p.kvh * nb : nb;
   } else {
-    const int b = find(sm->cum_s[line], a.n_seqs, x);
-    const int T = sm->off[b + 1] - sm->off[b], len = sm->len[b];
-    p.own = 1;
+    const int b = warp_find(sm->cum_s[line], a.n_seqs, x - in_groups);
+    const int len = sm->len[b];
+    first = sm->off[b];
+    T = sm->off[b + 1] - first;
     p.seq = b;
-    p.key0 = a.n_groups ? sm->plen[find(sm->gs, a.n_groups + 1, b)] : 0;
+    p.key0 = ng ? shared_keys(a, sm, warp_find(sm->gs, ng + 1, b)) : 0;
+    begin = in_groups + sm->cum_s[line][b];
     const int per = (sm->cum_s[line][b + 1] - sm->cum_s[line][b]) / a.Hkv;
-    p.kvh = (x - sm->cum_s[line][b]) / per;
-    begin = sm->cum_s[line][b] + p.kvh * per;
+    p.kvh = (x - begin) / per;
+    begin += p.kvh * per;
+#pragma unroll 1
     for (j = line == 0 ? 0 : pair_blocks(T, TB);; ++j) {
       p.kend = block_end(len, T, TB, j);
       p.nt = key_tiles(p.key0, p.kend);
-      const int cost = item_cost(p.nt);
+      const int cost = item_cost(line, p.nt);
       if (x < begin + cost) break;
       begin += cost;
     }
-    p.tok0 = sm->off[b] + j * 2 * TB;
-    p.ntok = min(2 * TB, T - j * 2 * TB);
   }
-  p.t0 = max(0, x - begin - kItemCost);
-  p.n = max(0, min(p.nt, end - begin - kItemCost) - p.t0);
-  x = min(end, begin + item_cost(p.nt));
+  p.tok0 = first + j * 2 * TB;
+  p.ntok = min(2 * TB, T - j * 2 * TB);
+  p.t0 = max(0, x - begin - fixed);
+  p.n = max(0, min(p.nt, end - begin - fixed) - p.t0);
+  x = min(end, begin + p.nt + fixed);
   return p;
 }
+
 /* ---- the tiles ---------------------------------------------------------------- */
+
+/* S = Q K^T of a tile; half h of O (+)= P V: P's keys 64 h .. 64 h + 63. */
+template <int D>
+__device__ __forceinline__ void issue_qk(uint32_t s, uint64_t q, uint64_t k, uint32_t lead) {
+  using C = Cfg<D>;
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {
+    const int o = (c / (C::COLS / 16) * C::BLOCK + c % (C::COLS / 16) * 32) >> 4;
+    mma_ss(s, q + o, k + o, inst_desc(kTile, false), c > 0, lead);
+  }
+}
+template <int D>
+__device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, int h, bool acc,
+                                         uint32_t lead) {
+  using C = Cfg<D>;
+  p += h * (kTile / 4);
+  v += h * ((kTile / 2 * C::ROWB) >> 4);
+#pragma unroll
+  for (int c = 0; c < kTile / 32; ++c)
+    mma_ts(o, p + c * 8, v + ((c * 16 * C::ROWB) >> 4), inst_desc(D, true), acc || h > 0 || c > 0,
+           lead);
+}
 
 /* Loads tile t of a piece, as far as its keys go: a box per page (or part of one) and
  * 64 dims.  Lane i looks up the page of box i, a tile ahead. */
@@ -525,11 +580,14 @@ struct Loader {
     page = -1;
     lead = elect_lead();
   }
+  __device__ __forceinline__ int page_of(int k) const {
+    return (int)(((unsigned long long)k * a.inv_p) >> 38);
+  }
   __device__ __forceinline__ void look_up(const Piece &p, int t) {
     const int k = p.key0 + (p.t0 + t) * kTile + lane * a.box_rows;
     page = -1;
     if (t < p.n && lane < boxes && k < p.kend)
-      page = __ldg(a.tables + (size_t)p.seq * a.max_pages + k / a.P);
+      page = __ldg(a.tables + (size_t)p.seq * a.max_pages + page_of(k));
   }
   __device__ __forceinline__ void load(const Piece &p, int t, int pg, const CUtensorMap *map,
                                        uint8_t *tile, uint64_t *full) {
@@ -539,7 +597,7 @@ struct Loader {
     const bool good = mine && (unsigned)pg < (unsigned)a.num_pages;
     if (mine && !good) *(volatile int32_t *)a.err_host = MK_ERR_PAGE_OOB;
     const unsigned set = __ballot_sync(0xffffffffu, good);
-    const int y = (pg * a.Hkv + p.kvh) * a.P + k % a.P;
+    const int y = (pg * a.Hkv + p.kvh) * a.P + k - page_of(k) * a.P;
     const uint32_t bytes = a.box_rows * C::ROWB;
     if (lead) bar_expect(full, __popc(set) * bytes * C::NH);
     __syncwarp();
@@ -603,26 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
   volatile int *abort = &sm->abort;
-  if (blockIdx.x == 0) {
-    if (tid == 0) {
-      a.sched[0] = !sound;
-      a.sched[1] = sound ? sm->total[0] : 0;
-      a.sched[2] = sound ? sm->total[1] : 0;
-      if (!sound) *(volatile int32_t *)a.err_host = MK_ERR_INVALID_ARG;
-    }
-    if (sound) {
-      int32_t *w = a.sched + 4;
-      for (int i = tid; i <= max(a.n_groups, a.n_seqs); i += kThreads)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          if (i <= a.n_groups) w[2 * k * kSchedStride + i] = sm->cum_g[k][i];
-          if (i <= a.n_seqs) w[(2 * k + 1) * kSchedStride + i] = sm->cum_s[k][i];
-          if (i < a.n_groups) w[4 * kSchedStride + i] = sm->plen[i];
-        }
-    }
-  }
   const long long n_cta = gridDim.x;
-  const int TB = kTile / a.G; /* query tokens of a row tile */
+  const int TB = a.TB;
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
@@ -633,9 +673,18 @@ __global__ void __launch_bounds__(kThreads, 1)
        * Of the pairs stream 0's loads K and stream 1's loads V, into all slots; of the singles
        * each loads both of its stream, K before V, the order in which the products need them. */
       Loader<D> ld(a, lane);
-      const uint32_t all = 2 * gridDim.x, me = 2 * blockIdx.x + s;
-      const unsigned long long tp = sound ? sm->total[0] : 0, ts = sound ? sm->total[1] : 0;
-      int x = (int)(blockIdx.x * tp / gridDim.x), end = (int)((blockIdx.x + 1) * tp / gridDim.x);
+      int x = 0, end = 0, x1 = 0, end1 = 0; /* this stream's share of the pairs, the singles */
+      if (sound) {
+        const int total = sm->total, pairs = sm->pairs, n = active_ctas(total, gridDim.x);
+        if ((int)blockIdx.x < n) {
+          const int lo = share_begin(blockIdx.x, total, n), hi = share_begin(blockIdx.x + 1, total, n);
+          x = min(lo, pairs);
+          end = min(hi, pairs);
+          const int s0 = max(lo, pairs) - pairs, s1 = max(hi, pairs) - pairs, mid = (s0 + s1 + 1) >> 1;
+          x1 = s ? mid : s0;
+          end1 = s ? s1 : mid;
+        }
+      }
       uint32_t armed_k = 0, armed_v = 0; /* parities of each slot's next use */
       bool ok = true;
       int line = 0, it = 0, ring = 0;
@@ -646,8 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (x < end) {
             p = next_piece(a, sm, line, x, end);
           } else if (++line == 1) {
-            x = (int)(me * ts / all);
-            end = (int)((me + 1) * ts / all);
+            x = x1;
+            end = end1;
             for (int i = 0; i < C::STAGES; ++i) /* uses of each slot so far */
               armed_k |= (uint32_t)(((it + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
             armed_v = armed_k;
@@ -700,10 +749,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       /* ---- issuer of stream s: S = Q K^T of a tile, then O += P V of its halves as P comes.
        * The other stream's issuer fills the tensor cores meanwhile. */
-      constexpr uint32_t id_qk = inst_desc(kTile, false), id_pv = inst_desc(D, true);
       const uint32_t lead = elect_lead();
       const uint32_t at_s = tmem + s * kTile, at_o = at_s + 2 * kTile;
-      const uint64_t q0 = mat_desc(saddr(qs + s * C::TILE), 16, 8 * C::ROWB, C::SWIZZLE);
+      const uint64_t q0 = mat_desc(saddr(qs), 16, 8 * C::ROWB, C::SWIZZLE);
       const uint64_t k0 = mat_desc(saddr(ks), 16, 8 * C::ROWB, C::SWIZZLE);
       const uint64_t v0 = mat_desc(saddr(vs), C::BLOCK, 8 * C::ROWB, C::SWIZZLE);
       bool ok = true;
@@ -718,7 +766,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) bar_arrive(&sm->qempty[s][qslot]);
         if (n == 0) break;
-        if (line == 1 && !singles) {
+        if (line == 0) {
+          /* a pair: stream 0's issuer works for both, one stream's products and then the
+           * other's.  (Two issuers' products mix, so that both streams' tiles end at once and
+           * their softmaxes run side by side with no product under them.) */
+          ok = warp_wait(&sm->qready[s], q_par, abort);
+          if (!ok) break;
+          q_par ^= 1;
+          if (s == 1) {
+            it += n;
+            p_par ^= n & 1;
+            continue;
+          }
+          ok = warp_wait(&sm->qready[1], q_par ^ 1, abort);
+#pragma unroll 1
+          for (int j = 0; ok && j < 2 * n + 2; ++j) { /* PV of tile t - 1, QK of tile t of stream c */
+            const int c = j & 1, t = j >> 1;
+            const uint32_t c_s = tmem + c * kTile, c_o = c_s + 2 * kTile;
+            if (t > 0) {
+              const int slot = (it - 1) % C::STAGES;
+              if (c == 0) ok = warp_wait(&sm->vfull[slot], ((it - 1) / C::STAGES) & 1, abort);
+              for (int h = 0; ok && h < 2; ++h) {
+                ok = warp_wait(&sm->pready[c][h], p_par, abort);
+                tc_fence_after();
+                if (ok)
+                  issue_pv<D>(c_o, c_s, v0 + (uint32_t)slot * (C::TILE >> 4), h, t > 1, lead);
+              }
+              if (!ok) break;
+              if (t == n) tc_commit(&sm->oready[c], lead);
+              if (c == 1) {
+                p_par ^= 1;
+                tc_commit(&sm->vempty[slot], lead);
+                tc_commit(&sm->vempty[slot], lead);
+              }
+            }
+            if (t < n) {
+              const int slot = it % C::STAGES;
+              if (c == 0) ok = warp_wait(&sm->kfull[slot], (it / C::STAGES) & 1, abort);
+              if (!ok) break;
+              tc_fence_after();
+              issue_qk<D>(c_s, q0 + (uint32_t)c * (C::TILE >> 4), k0 + (uint32_t)slot * (C::TILE >> 4),
+                          lead);
+              tc_commit(&sm->sfull[c], lead);
+              if (c == 1) {
+                tc_commit(&sm->kempty[slot], lead);
+                tc_commit(&sm->kempty[slot], lead);
+                ++it;
+              }
+            } else if (c == 0) {
+              continue;
+            }
+          }
+          if (!ok) break;
+          continue;
+        }
+        if (!singles) {
           singles = true;
           for (int i = 0; i < C::STAGES; ++i)
             par |= (uint32_t)(((it + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
@@ -728,43 +830,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         q_par ^= 1;
 #pragma unroll 1
         for (int t = 0; t < n; ++t) {
-          const int slot = line == 0 ? it % C::STAGES : s * R + ring;
-          const uint32_t parity = (line == 0 ? it / C::STAGES : par >> slot) & 1;
-          const uint32_t o = (uint32_t)slot * (C::TILE >> 4);
+          const int slot = s * R + ring;
+          const uint32_t parity = (par >> slot) & 1, o = (uint32_t)slot * (C::TILE >> 4);
           ok = warp_wait(&sm->kfull[slot], parity, abort);
           if (!ok) break;
           tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            const int oc = (c / (C::COLS / 16) * C::BLOCK + c % (C::COLS / 16) * 32) >> 4;
-            mma_ss(at_s, q0 + oc, k0 + o + oc, id_qk, c > 0, lead);
-          }
+          issue_qk<D>(at_s, q0 + (uint32_t)s * (C::TILE >> 4), k0 + o, lead);
           tc_commit(&sm->sfull[s], lead);
-          /* a slot is free when both streams have read it: a single's reader counts twice */
+          tc_commit(&sm->kempty[slot], lead); /* twice: a pair's two readers count one each */
           tc_commit(&sm->kempty[slot], lead);
-          if (line == 1) tc_commit(&sm->kempty[slot], lead);
           ok = warp_wait(&sm->vfull[slot], parity, abort);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ok = ok && warp_wait(&sm->pready[s][h], p_par, abort);
-            if (!ok) break;
+          for (int h = 0; ok && h < 2; ++h) {
+            ok = warp_wait(&sm->pready[s][h], p_par, abort);
             tc_fence_after();
-#pragma unroll
-            for (int c = h * (kTile / 32); c < (h + 1) * (kTile / 32); ++c)
-              mma_ts(at_o, at_s + c * 8, v0 + o + ((c * 16 * C::ROWB) >> 4), id_pv,
-                     t > 0 || c > 0, lead);
+            if (ok) issue_pv<D>(at_o, at_s, v0 + o, h, t > 0, lead);
           }
           if (!ok) break;
           p_par ^= 1;
           if (t == n - 1) tc_commit(&sm->oready[s], lead);
           tc_commit(&sm->vempty[slot], lead);
-          if (line == 1) tc_commit(&sm->vempty[slot], lead);
-          if (line == 0) {
-            ++it;
-          } else {
-            par ^= 1u << slot;
-            ring = ring + 1 == R ? 0 : ring + 1;
-          }
+          tc_commit(&sm->vempty[slot], lead);
+          par ^= 1u << slot;
+          ring = ring + 1 == R ? 0 : ring + 1;
         }
         if (!ok) break;
       }
@@ -1008,6 +1095,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
     }
   }
+  /* the cut for attn_merge, off the way to the first product */
+  if (blockIdx.x == 0) {
+    if (tid == 0) {
+      a.sched[0] = !sound;
+      a.sched[1] = sound ? sm->total : 0;
+      a.sched[2] = sound ? sm->pairs : 0;
+      if (!sound) *(volatile int32_t *)a.err_host = MK_ERR_INVALID_ARG;
+    }
+    if (sound) {
+      int32_t *w = a.sched + 4;
+      for (int i = tid; i <= max(a.n_groups, a.n_seqs); i += kThreads)
+        for (int k = 0; k < 2; ++k) {
+          if (i <= a.n_groups) w[2 * k * kSchedStride + i] = sm->cum_g[k][i];
+          if (i <= a.n_seqs) w[(2 * k + 1) * kSchedStride + i] = sm->cum_s[k][i];
+          if (i < a.n_groups) w[4 * kSchedStride + i] = shared_keys(a, sm, i);
+        }
+    }
+  }
   __syncthreads();
   if (tid == 0 && *abort) *(volatile int32_t *)a.err_host = MK_ERR_DEVICE_TIMEOUT;
   if (warp == 10) {
@@ -1018,50 +1123,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 /* ---- the join ----------------------------------------------------------------- */
 
-/* find() by a whole warp: 32 places a round, so one or two loads deep. */
-__device__ __forceinline__ int warp_find(const int32_t *a, int n, int x) {
-  const int lane = threadIdx.x & 31;
-  int lo = 0, len = n; /* the answer is in [lo, lo + len) */
-  while (len > 1) {
-    const int step = (len + 31) / 32, i = lane * step;
-    const unsigned le = __ballot_sync(0xffffffffu, i < len && a[lo + i] <= x);
-    const int k = 31 - __clz(le | 1u);
-    lo += k * step;
-    len = min(step, len - k * step);
-  }
-  return lo;
-}
-
-/* One warp per output row: M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
- * Reads L2: the partials were written just before. */
-template <int D>
+/* M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over a row's pieces, by
+ * W warps a row: one where rows are many, all eight of a block where they are few and
+ * have many pieces each.  Reads L2: the partials were written just before.  What bounds
+ * it is its chain of loads, so look-ups go 32 places at a time and a lane's row of
+ * pieces is in flight together. */
+template <int D, int W>
 __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a, int n_cta) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const long long orow = ((long long)blockIdx.x * 256 + threadIdx.x) >> 5;
-  if (a.sched[0]) return;
-  const int tok = (int)(orow / a.Hq), head = (int)(orow - (long long)tok * a.Hq);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long orow = (long long)blockIdx.x * (8 / W) + warp / W;
+  const int part = warp % W;
+  const int bad = a.sched[0], total = a.sched[1], n_pairs = a.sched[2];
   const int tokens = a.off ? a.off[a.n_seqs] : a.n_seqs;
-  if (tok >= tokens) return;
-  const int TB = kTile / a.G, BT = 2 * TB;
+  const int tok = (int)(orow / a.Hq), head = (int)(orow - (long long)tok * a.Hq);
+  if (bad || tok >= tokens) return; /* the same for all W warps */
+  const int TB = a.TB, BT = 2 * TB, ctas = active_ctas(total, n_cta);
   const int kvh = head / a.G, hg = head - kvh * a.G;
   const int32_t *cut = a.sched + 4;
   const int b = a.off ? warp_find(a.off, a.n_seqs + 1, tok) : tok;
   const int first = a.off ? a.off[b] : b, T = a.off ? a.off[b + 1] - first : 1, len = a.lens[b];
-  int plen = 0, n_shared = 0, n_own = 0;      /* pieces */
-  long long xs = 0, xo = 0;                   /* where those behind the first are: one tile a worker */
-  int ss = 0, so = 0;                         /* rows from a worker's slot to the next */
+  int plen = 0, n_shared = 0, n_own = 0;  /* pieces */
+  int ws = 0, wo = 0;                     /* their first workers: CTAs, or streams */
+  long long xs = 0, xo = 0;               /* this row in worker 0's own place */
+  int ss = 0, so = 0;                     /* rows from one worker's place to the next */
   const long long dense = (long long)a.n_tokens * a.Hq;
-  auto pieces = [&](int line, int begin, int tiles, int ti, long long &at, int &step) {
-    const int total = a.sched[1 + line], n = line == 0 ? n_cta : 2 * n_cta;
-    const int w0 = worker_of(begin + kItemCost, total, n);
-    const int w1 = worker_of(begin + kItemCost + tiles - 1, total, n);
-    const int tile = ti / TB;                 /* of a pair */
+  /* a stream without singles between two that have some: only of the CTA whose share
+   * holds the last pairs and one place of the singles */
+  int none = -1;
+  if (n_pairs > 0 && n_pairs < total) {
+    const int c = cta_of(n_pairs, total, ctas);
+    if (share_begin(c + 1, total, ctas) - n_pairs == 1) none = 2 * c + 1;
+  }
+  auto worker = [&](int line, int x) {
+    if (line == 0) return cta_of(x, total, ctas);
+    const int c = cta_of(n_pairs + x, total, ctas);
+    const int s0 = max(share_begin(c, total, ctas), n_pairs) - n_pairs;
+    const int s1 = share_begin(c + 1, total, ctas) - n_pairs;
+    return 2 * c + (x >= ((s0 + s1 + 1) >> 1));
+  };
+  auto pieces = [&](int line, int begin, int tiles, int ti, int &w0, long long &at, int &step) {
+    w0 = worker(line, begin + fixed_cost(line));
+    const int w1 = worker(line, begin + fixed_cost(line) + tiles - 1);
+    const int tile = ti >= TB; /* of a pair */
     step = line == 0 ? 2 * kTile : kTile;
-    at = 2 * dense + (line == 0 ? 0 : 2ll * n_cta * kTile) + (long long)w0 * step + tile * kTile +
-         (ti - tile * TB) * a.G + hg;
-    return w1 - w0 + 1;
+    at = 2 * dense + (line == 0 ? 0 : 2ll * n_cta * kTile) + tile * kTile + (ti - tile * TB) * a.G + hg;
+    return w1 - w0 + 1 - (line == 1 && w0 < none && none < w1);
   };
   if (a.n_groups) {
     const int g = warp_find(a.starts, a.n_groups + 1, b);
@@ -1069,21 +1177,22 @@ __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a
     if (plen) {
       const int s0 = a.starts[g], s1 = a.starts[g + 1];
       const int gtok = a.off ? a.off[s0] : s0, gT = (a.off ? a.off[s1] : s1) - gtok;
-      const int nt = key_tiles(0, plen), nb = pair_blocks(gT, TB), j = (tok - gtok) / BT;
-      const int line = j < nb ? 0 : 1;
+      const int nt = key_tiles(0, plen), nb = pair_blocks(gT, TB);
+      const int j = gT <= BT ? 0 : (tok - gtok) / BT, line = j < nb ? 0 : 1;
       const int begin = cut[2 * line * kSchedStride + g] +
-                        (line == 0 ? kvh * nb + j : kvh) * item_cost(nt);
-      n_shared = pieces(line, begin, nt, tok - gtok - j * BT, xs, ss);
+                        (line == 0 ? kvh * nb + j : kvh) * item_cost(line, nt);
+      n_shared = pieces(line, begin, nt, tok - gtok - j * BT, ws, xs, ss);
     }
   }
-  const int nb = pair_blocks(T, TB), jb = (tok - first) / BT, line = jb < nb ? 0 : 1;
+  const int nb = pair_blocks(T, TB), jb = T <= BT ? 0 : (tok - first) / BT, line = jb < nb ? 0 : 1;
   const int nt_own = key_tiles(plen, block_end(len, T, TB, jb));
   if (nt_own) {
     const int32_t *cum = cut + (2 * line + 1) * kSchedStride;
-    int begin = cum[b] + (cum[b + 1] - cum[b]) / a.Hkv * kvh;
+    const int in_groups = cut[2 * line * kSchedStride + a.n_groups];
+    int begin = in_groups + cum[b] + (cum[b + 1] - cum[b]) / a.Hkv * kvh;
     if (line == 0)
-      for (int j = 0; j < jb; ++j) begin += item_cost(key_tiles(plen, block_end(len, T, TB, j)));
-    n_own = pieces(line, begin, nt_own, tok - first - jb * BT, xo, so);
+      for (int j = 0; j < jb; ++j) begin += item_cost(0, key_tiles(plen, block_end(len, T, TB, j)));
+    n_own = pieces(line, begin, nt_own, tok - first - jb * BT, wo, xo, so);
   }
   if (n_shared == 0 && n_own == 1) return; /* written by attn_tiles */
   const int n = n_shared + n_own;
@@ -1091,7 +1200,10 @@ __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a
     const bool own = i >= n_shared;
     const int k = own ? i - n_shared : i;
     if (k == 0) return own ? dense + orow : orow;
-    return own ? xo + (long long)k * so : xs + (long long)k * ss;
+    const int step = own ? so : ss, w0 = own ? wo : ws;
+    int w = w0 + k;
+    if (step == kTile && w0 < none && none <= w) ++w;
+    return (own ? xo : xs) + (long long)w * step;
   };
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[place(i)].x);
@@ -1102,26 +1214,51 @@ __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a
   if (M != -INFINITY) {
     for (int i0 = 0; i0 < n; i0 += 32) {
       float f = 0.0f;
+      long long at = 0;
       if (i0 + lane < n) {
-        const float2 ml = a.part_ml[place(i0 + lane)];
+        at = place(i0 + lane);
+        const float2 ml = a.part_ml[at];
         f = exp2_approx(ml.x - M);
         l += f * ml.y;
       }
       const int m = min(32, n - i0);
 #pragma unroll 4
-      for (int i = 0; i < m; ++i) {
+      for (int i = part; i < m; i += W) {
         const float w = __shfl_sync(0xffffffffu, f, i);
-        const float *src = a.part + place(i0 + i) * D + lane * N;
+        const float *src = a.part + __shfl_sync(0xffffffffu, at, i) * D + lane * N;
+        float v[N];
+        if (N == 4)
+          *(float4 *)v = *(const float4 *)src;
+        else if (N == 2)
+          *(float2 *)v = *(const float2 *)src;
+        else
+          v[0] = src[0];
 #pragma unroll
-        for (int k = 0; k < N; ++k) o[k] = fmaf(w, src[k], o[k]);
+        for (int k = 0; k < N; ++k) o[k] = fmaf(w, v[k], o[k]);
       }
     }
 #pragma unroll
     for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  if (W > 1) { /* the warps' sums, in order */
+    __shared__ float sums[W > 1 ? W : 1][D];
 #pragma unroll
-  for (int k = 0; k < N; ++k) a.out[orow * D + lane * N + k] = __float2bfloat16_rn(o[k] * inv);
+    for (int k = 0; k < N; ++k) sums[part][k * 32 + lane] = o[k];
+    __syncthreads();
+    if (part) return;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      for (int w = 1; w < W; ++w) o[k] += sums[w][k * 32 + lane];
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  __nv_bfloat16 *dst = a.out + orow * D + lane * N;
+  if (N == 4) {
+    *(uint2 *)dst = make_uint2(pack_bf16(o[0] * inv, o[1 % N] * inv), pack_bf16(o[2 % N] * inv, o[3 % N] * inv));
+  } else if (N == 2) {
+    *(uint32_t *)dst = pack_bf16(o[0] * inv, o[1 % N] * inv);
+  } else {
+    *dst = __float2bfloat16_rn(o[0] * inv);
+  }
   if (a.lse && lane == 0)
     a.lse[orow] = l > 0.0f ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
@@ -1162,6 +1299,7 @@ namespace {
 
 template <int D>
 cudaError_t prepare() {
+  static_assert(Cfg<D>::SMEM + sizeof(Smem) <= 232448, "shared memory of a CTA");
   return cudaFuncSetAttribute(attn_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               Cfg<D>::SMEM + (int)sizeof(Smem));
 }
@@ -1181,10 +1319,13 @@ cudaError_t launch(const mk_attn *at, int layer, const Args &a) {
   cudaError_t e =
       cudaLaunchKernelEx(&cfg, attn_tiles<D>, at->maps[2 * layer], at->maps[2 * layer + 1], a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)(((long long)a.n_tokens * a.Hq + 7) / 8));
+  const long long rows = (long long)a.n_tokens * a.Hq;
+  const bool few = rows <= kFewRows;
+  cfg.gridDim = dim3((unsigned)(few ? rows : (rows + 7) / 8));
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_merge<D>, a, at->n_sm);
+  return few ? cudaLaunchKernelEx(&cfg, attn_merge<D, 8>, a, at->n_sm)
+             : cudaLaunchKernelEx(&cfg, attn_merge<D, 1>, a, at->n_sm);
 }
 
 }  // namespace
@@ -1200,7 +1341,7 @@ mk_status mk_attn_create(const mk_attn_desc *d, void *stream, mk_attn **out) {
     return MK_ERR_INVALID_ARG;
   if ((d->head_dim != 32 && d->head_dim != 64 && d->head_dim != 128) || d->page_size % 16 ||
       d->page_size > 256 || d->n_q_heads / d->n_kv_heads > 64 || d->n_q_heads > 1024 ||
-      d->max_tokens > (1 << 20) || d->max_seqs > kMaxSeqs || d->max_groups > kMaxSeqs ||
+      d->max_tokens > (1 << 20) || d->max_seqs > kMaxSeqs || d->max_groups > kMaxGroups ||
       (int64_t)d->num_pages * d->n_kv_heads * d->page_size > INT32_MAX)
     return MK_ERR_UNSUPPORTED;
   if (!d->k_caches || !d->v_caches) return MK_ERR_INVALID_ARG;
@@ -1310,7 +1451,9 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   a.out = (__nv_bfloat16 *)out;
   a.lse = lse;
   a.scale_log2 = at->scale_log2;
+  a.TB = kTile / a.G;
   a.inv_g = (65536 + a.G - 1) / a.G;
+  a.inv_p = ((1ull << 38) + a.P - 1) / a.P;
   a.err_host = at->err_dev;
   a.sched = (int32_t *)at->ws;
   a.part = (float *)(at->ws + at->o_part);
