@@ -239,6 +239,24 @@ mk_status mk_encode_rows_map(const mk_attn_desc *d, const void *pool, int box_ro
   return MK_OK;
 }
 
+mk_status mk_encode_q_map(const mk_attn_desc *d, const void *q, int n_tokens, int64_t token_stride,
+                          int box_tokens, void *host_out) {
+  EncodeTiledFn enc = tensor_map_encoder();
+  if (!enc) return MK_ERR_CUDA;
+  const int cols = mk_box_inner(d->head_dim);
+  const cuuint64_t dims[3] = {(cuuint64_t)d->head_dim, (cuuint64_t)d->n_q_heads, (cuuint64_t)n_tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)d->head_dim * 2, (cuuint64_t)token_stride * 2};
+  const cuuint32_t box[3] = {(cuuint32_t)cols, (cuuint32_t)(d->n_q_heads / d->n_kv_heads),
+                             (cuuint32_t)box_tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  if (enc((CUtensorMap *)host_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(q), dims,
+          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          cols < 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return MK_ERR_INVALID_ARG;
+  return MK_OK;
+}
+
 extern "C" {
 
 const char *mk_status_string(mk_status s) {

@@ -47,14 +47,13 @@ constexpr uint64_t kWaitLimit = 2000000000ull; /* ns */
  * of two): P then stays below 2^8, exact in its relative precision, and the
  * accumulator is rescaled a few times per row rather than in most tiles. */
 constexpr float kSlack = 8.0f;
-constexpr int kSchedStride = kMaxSeqs + 1;
-constexpr int kFewRows = 4096; /* up to this many output rows attn_merge has a block for each */
+/* Stream 1 begins a pair this many cycles behind stream 0, so that one's softmax runs
+ * under the other's products; in step, both softmaxes would leave the tensor cores idle. */
+constexpr int kPairLag = 1200;
 
 struct Args {
   int32_t Hq, Hkv, G, P, num_pages, max_pages, n_seqs, n_tokens, n_groups, box_rows;
   const int32_t *tables, *lens, *off, *starts, *prefix;
-  const __nv_bfloat16 *q;
-  long long q_stride;
   __nv_bfloat16 *out;
   float *lse;
   float scale_log2; /* scale * log2(e) */
@@ -63,9 +62,11 @@ struct Args {
   unsigned long long inv_p; /* ceil(2^38 / P): k * inv_p >> 38 is k / P for k < 2^30 */
   int32_t *err_host;
   /* workspace */
-  int32_t *sched;    /* the cut, for attn_merge: [0] bad, [1] the line's length, [2] where its
-                      * singles begin, then kSchedStride each: the groups' and the sequences'
-                      * beginnings among the pairs, among the singles, the groups' shared keys */
+  int32_t *bad;      /* the batch is not sound */
+  int4 *where;       /* [2][n_tokens][Hkv], zero between calls: where a token's partials are, of
+                      * the shared keys and of its own.  x: pieces + 1, 1: written already, 0:
+                      * none; y: the first piece's worker; z: a worker to leave out, or -1; w:
+                      * the token's first row in worker 0's place, bit 30: workers are streams */
   float *part;       /* [2 * n_tokens * Hq + 4 * SMs * 128][D] weighted sums */
   float2 *part_ml;   /* the same rows: maximum (in powers of two), sum */
 };
@@ -90,12 +91,14 @@ struct Piece {
   int kvh, tok0, ntok; /* query tokens of the item */
   int key0, kend;      /* the item's keys */
   int t0, n, nt;       /* first tile and tiles of this piece (0: no more), tiles of the item */
+  int begin;           /* the item's first place */
 };
 
 struct Smem { /* behind the tiles */
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
-  uint64_t sfull[2], pready[2][2], qready[2], oready[2], drain[2];
-  uint64_t qfull[2][kQueue], qempty[2][kQueue];
+  uint64_t sfull[2], pready[2][2], oready[2], drain[2];
+  uint64_t q_full[2], q_free[2];              /* Q of a stream's piece */
+  uint64_t qfull[2][kQueue], qempty[2][kQueue]; /* the queue's */
   Piece queue[2][kQueue];
   uint32_t tmem;
   int abort;
@@ -127,33 +130,33 @@ __device__ __forceinline__ uint64_t now_ns() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
+__device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(saddr(b)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 /* Waits for a phase; false when another role gave up or the limit ran out. */
-__device__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
-  const uint32_t a = saddr(b);
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
   uint64_t since = 0;
   for (int i = 0;; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(a), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (*abort) return false;
+    if (__all_sync(0xffffffffu, bar_try(b, parity))) return true;
+    if (__any_sync(0xffffffffu, *abort != 0)) return false;
     if ((i & 63) == 63) {
       const uint64_t t = now_ns();
       if (!since)
         since = t;
-      else if (t - since > kWaitLimit) {
+      else if (t - since > kWaitLimit)
         *abort = 1;
-        return false;
-      }
     }
   }
 }
 __device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
-  return __all_sync(0xffffffffu, bar_wait(b, parity, abort));
+  return __all_sync(0xffffffffu, bar_try(b, parity)) || bar_wait(b, parity, abort);
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
                                        uint64_t *bar, uint32_t lead) {
@@ -162,6 +165,15 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int
       " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(saddr(bar)), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z,
+                                       uint64_t *bar, uint32_t lead) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.u32 e, %6, 0;\n"
+      " @e cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(saddr(bar)), "r"(lead)
       : "memory");
 }
 __device__ __forceinline__ void fence_async_smem() {
@@ -540,7 +552,42 @@ __device__ __forceinline__ Piece next_piece(const Args &a, const Smem *sm, int l
   p.t0 = max(0, x - begin - fixed);
   p.n = max(0, min(p.nt, end - begin - fixed) - p.t0);
   x = min(end, begin + p.nt + fixed);
+  p.begin = begin;
   return p;
+}
+
+/* An item's first piece tells attn_merge where the item's partials are.  By a whole
+ * warp, a token a lane. */
+__device__ __forceinline__ void tell_merge(const Args &a, const Smem *sm, const Piece &p) {
+  const int total = sm->total, pairs = sm->pairs, n = active_ctas(total, gridDim.x);
+  int w[2];
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) { /* the workers of the item's first tile and its last */
+    const int x = p.begin + fixed_cost(p.line) + (k ? p.nt - 1 : 0) + (p.line ? pairs : 0);
+    const int c = cta_of(x, total, n);
+    w[k] = c;
+    if (p.line) {
+      const int s0 = max(share_begin(c, total, n), pairs), s1 = share_begin(c + 1, total, n);
+      w[k] = 2 * c + (x - pairs >= ((s0 + s1 - 2 * pairs + 1) >> 1));
+    }
+  }
+  /* a stream without singles between two that have some: only of the CTA whose share
+   * holds the last pairs and one place of the singles */
+  int none = -1;
+  if (p.line && pairs > 0) {
+    const int c = cta_of(pairs, total, n);
+    if (share_begin(c + 1, total, n) - pairs == 1 && w[0] < 2 * c + 1 && 2 * c + 1 < w[1])
+      none = 2 * c + 1;
+  }
+  const bool whole = p.own && p.key0 == 0 && p.n == p.nt;
+  const int pieces = w[1] - w[0] + 1 - (none >= 0);
+  const int lane = threadIdx.x & 31;
+  for (int i = lane; i < p.ntok; i += 32) {
+    const int tile = i >= a.TB;
+    const int row = (p.line ? 2 * (int)gridDim.x * kTile : tile * kTile) + (i - tile * a.TB) * a.G;
+    a.where[((long long)p.own * a.n_tokens + p.tok0 + i) * a.Hkv + p.kvh] =
+        make_int4(whole ? 1 : pieces + 1, w[0], none, row | p.line << 30);
+  }
 }
 
 /* ---- the tiles ---------------------------------------------------------------- */
@@ -614,8 +661,8 @@ struct Loader {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tiles(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-               const __grid_constant__ Args a) {
+    attn_tiles(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+               const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
   using C = Cfg<D>;
   constexpr int R = C::STAGES / 2; /* K (and V) slots of a stream; pairs use all of both */
   extern __shared__ uint8_t raw[];
@@ -636,7 +683,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&sm->sfull[s], 1);
       bar_init(&sm->pready[s][0], 4);
       bar_init(&sm->pready[s][1], 4);
-      bar_init(&sm->qready[s], 4);
+      bar_init(&sm->q_full[s], 1);
+      bar_init(&sm->q_free[s], 4);
       bar_init(&sm->oready[s], 1);
       bar_init(&sm->drain[s], 1);
       for (int i = 0; i < kQueue; ++i) {
@@ -687,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       uint32_t armed_k = 0, armed_v = 0; /* parities of each slot's next use */
       bool ok = true;
-      int line = 0, it = 0, ring = 0;
+      int line = 0, it = 0, ring = 0, q_uses = 0;
       for (int put = 0; ok; ++put) {
         Piece p;
         p.n = 0;
@@ -712,6 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (p.n == 0) break;
         ld.look_up(p, 0);
+        const int q_tok = p.tok0 + (line == 0 ? s * TB : 0);
 #pragma unroll 1
         for (int t = 0; ok && t < p.n; ++t) {
           const int page = ld.page;
@@ -725,7 +774,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             ld.load(p, t, page, kv ? &vmap : &kmap, (kv ? vs : ks) + slot * C::TILE,
                     kv ? &sm->vfull[slot] : &sm->kfull[slot]);
             if (line == 1) (kv ? armed_v : armed_k) ^= 1u << slot;
+            if (t == 0 && (line == 0 || kv == 0)) {
+              /* Q: [tokens][heads of the group][64 dims], the rows' order.  Rows behind the
+               * last token are other rows of Q or zeros, and are not looked at. */
+              ok = warp_wait(&sm->q_free[s], (q_uses & 1) ^ 1, abort);
+              if (!ok) break;
+              ++q_uses;
+              if (ld.lead) bar_expect(&sm->q_full[s], C::NH * C::ROWB * TB * a.G);
+              __syncwarp();
+#pragma unroll
+              for (int h = 0; h < C::NH; ++h)
+                tma_3d(saddr(qs + s * C::TILE + h * C::BLOCK), &qmap, h * C::COLS, p.kvh * a.G, q_tok,
+                       &sm->q_full[s], ld.lead);
+            }
           }
+          if (t == 0 && p.t0 == 0 && (line == 1 || s == 0)) tell_merge(a, sm, p);
           if (line == 0)
             ++it;
           else
@@ -745,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             warp_wait(&sm->vfull[i], ((armed_v >> i) & 1) ^ 1, &none);
           }
         }
+        if (q_uses) warp_wait(&sm->q_full[s], (q_uses - 1) & 1, &none);
       }
     } else {
       /* ---- issuer of stream s: S = Q K^T of a tile, then O += P V of its halves as P comes.
@@ -766,79 +830,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) bar_arrive(&sm->qempty[s][qslot]);
         if (n == 0) break;
-        if (line == 0) {
-          /* a pair: stream 0's issuer works for both, one stream's products and then the
-           * other's.  (Two issuers' products mix, so that both streams' tiles end at once and
-           * their softmaxes run side by side with no product under them.) */
-          ok = warp_wait(&sm->qready[s], q_par, abort);
-          if (!ok) break;
-          q_par ^= 1;
-          if (s == 1) {
-            it += n;
-            p_par ^= n & 1;
-            continue;
-          }
-          ok = warp_wait(&sm->qready[1], q_par ^ 1, abort);
-#pragma unroll 1
-          for (int j = 0; ok && j < 2 * n + 2; ++j) { /* PV of tile t - 1, QK of tile t of stream c */
-            const int c = j & 1, t = j >> 1;
-            const uint32_t c_s = tmem + c * kTile, c_o = c_s + 2 * kTile;
-            if (t > 0) {
-              const int slot = (it - 1) % C::STAGES;
-              if (c == 0) ok = warp_wait(&sm->vfull[slot], ((it - 1) / C::STAGES) & 1, abort);
-              for (int h = 0; ok && h < 2; ++h) {
-                ok = warp_wait(&sm->pready[c][h], p_par, abort);
-                tc_fence_after();
-                if (ok)
-                  issue_pv<D>(c_o, c_s, v0 + (uint32_t)slot * (C::TILE >> 4), h, t > 1, lead);
-              }
-              if (!ok) break;
-              if (t == n) tc_commit(&sm->oready[c], lead);
-              if (c == 1) {
-                p_par ^= 1;
-                tc_commit(&sm->vempty[slot], lead);
-                tc_commit(&sm->vempty[slot], lead);
-              }
-            }
-            if (t < n) {
-              const int slot = it % C::STAGES;
-              if (c == 0) ok = warp_wait(&sm->kfull[slot], (it / C::STAGES) & 1, abort);
-              if (!ok) break;
-              tc_fence_after();
-              issue_qk<D>(c_s, q0 + (uint32_t)c * (C::TILE >> 4), k0 + (uint32_t)slot * (C::TILE >> 4),
-                          lead);
-              tc_commit(&sm->sfull[c], lead);
-              if (c == 1) {
-                tc_commit(&sm->kempty[slot], lead);
-                tc_commit(&sm->kempty[slot], lead);
-                ++it;
-              }
-            } else if (c == 0) {
-              continue;
-            }
-          }
-          if (!ok) break;
-          continue;
-        }
-        if (!singles) {
+        if (line == 1 && !singles) {
           singles = true;
           for (int i = 0; i < C::STAGES; ++i)
             par |= (uint32_t)(((it + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
         }
-        ok = warp_wait(&sm->qready[s], q_par, abort);
+        ok = warp_wait(&sm->q_full[s], q_par, abort);
         if (!ok) break;
         q_par ^= 1;
+        if (line == 0 && s == 1 && n > 4) {
+          const long long since = clock64();
+          while (clock64() - since < kPairLag)
+            ;
+        }
 #pragma unroll 1
         for (int t = 0; t < n; ++t) {
-          const int slot = s * R + ring;
-          const uint32_t parity = (par >> slot) & 1, o = (uint32_t)slot * (C::TILE >> 4);
+          const int slot = line == 0 ? it % C::STAGES : s * R + ring;
+          const uint32_t parity = (line == 0 ? it / C::STAGES : par >> slot) & 1;
+          const uint32_t o = (uint32_t)slot * (C::TILE >> 4);
           ok = warp_wait(&sm->kfull[slot], parity, abort);
           if (!ok) break;
           tc_fence_after();
           issue_qk<D>(at_s, q0 + (uint32_t)s * (C::TILE >> 4), k0 + o, lead);
           tc_commit(&sm->sfull[s], lead);
-          tc_commit(&sm->kempty[slot], lead); /* twice: a pair's two readers count one each */
           tc_commit(&sm->kempty[slot], lead);
+          if (line == 1) tc_commit(&sm->kempty[slot], lead); /* a pair's two readers count one each */
           ok = warp_wait(&sm->vfull[slot], parity, abort);
           for (int h = 0; ok && h < 2; ++h) {
             ok = warp_wait(&sm->pready[s][h], p_par, abort);
@@ -849,9 +865,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           p_par ^= 1;
           if (t == n - 1) tc_commit(&sm->oready[s], lead);
           tc_commit(&sm->vempty[slot], lead);
-          tc_commit(&sm->vempty[slot], lead);
-          par ^= 1u << slot;
-          ring = ring + 1 == R ? 0 : ring + 1;
+          if (line == 1) {
+            tc_commit(&sm->vempty[slot], lead);
+            par ^= 1u << slot;
+            ring = ring + 1 == R ? 0 : ring + 1;
+          } else {
+            ++it;
+          }
         }
         if (!ok) break;
       }
@@ -874,59 +894,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t v_par = 0;     /* parities of this stream's slots, set behind the pairs */
     int got = 0;
     bool ok = true;
-    Piece p;
-    constexpr int PER = D / 8; /* 16-byte chunks of a row */
-    uint4 q[PER];
-    int tok0 = 0, rows = 0;
-    /* the next piece, and this warp's 32 rows of its Q on their way, zeros behind the last */
-    auto take = [&]() -> bool {
+    for (; ok; ++got) {
       const int qslot = got % kQueue;
-      if (!warp_wait(&sm->qfull[s][qslot], (got / kQueue) & 1, abort)) return false;
-      ++got;
-      p = sm->queue[s][qslot];
+      ok = warp_wait(&sm->qfull[s][qslot], (got / kQueue) & 1, abort);
+      if (!ok) break;
+      const Piece c = sm->queue[s][qslot];
       __syncwarp();
       if (lane == 0) bar_arrive(&sm->qempty[s][qslot]);
-      tok0 = p.tok0 + (p.line == 0 ? s * TB : 0);
-      rows = p.n ? min(TB, p.tok0 + p.ntok - tok0) * a.G : 0;
-      int ln = lane;
-      asm volatile("" : "+r"(ln));
-      const __nv_bfloat16 *src = a.q + (long long)tok0 * a.q_stride + p.kvh * a.G * D + ln % PER * 8;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int qr = w0 + ln / PER + i * (32 / PER), qt = (qr * a.inv_g) >> 16;
-        q[i] = make_uint4(0, 0, 0, 0);
-        if (qr < rows)
-          q[i] = __ldg((const uint4 *)(src + qt * a.q_stride + (qr - qt * a.G) * D));
-      }
-      return true;
-    };
-    ok = take();
-    while (ok && p.n) {
-      const bool pair = p.line == 0;
+      if (c.n == 0) break;
+      const bool pair = c.line == 0;
       if (!pair && v_par >> 31 == 0) {
         v_par = 1u << 31;
         for (int i = 0; i < C::STAGES; ++i)
           v_par |= (uint32_t)(((it + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
       }
-      /* the lane again, so that addresses made of it are not kept across the pieces */
-      int ln = lane;
-      asm volatile("" : "+r"(ln));
-      /* Q into swizzled shared memory */
-      {
-        const int ch = ln % PER, hb = ch / (C::COLS / 8), cc = ch % (C::COLS / 8);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int qr = ln / PER + i * (32 / PER);
-          const int sw = D < 64 ? cc ^ ((qr >> 1) & 3) : cc ^ (qr & 7);
-          *(uint4 *)(qd + hb * C::BLOCK + qr * C::ROWB + sw * 16) = q[i];
-        }
-      }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) bar_arrive(&sm->qready[s]);
-
-      const Piece c = p; /* the current piece: `take` moves on below */
-      const int ctok0 = tok0, crows = rows;
+      const int ctok0 = c.tok0 + (pair ? s * TB : 0);
+      const int crows = min(TB, c.tok0 + c.ntok - ctok0) * a.G;
       const bool valid = r < crows, busy = w0 < crows;
       const int rt = valid ? (r * a.inv_g) >> 16 : 0, tok = ctok0 + rt;
       const int b = c.own ? c.seq : a.off ? find(sm->off, a.n_seqs + 1, tok) : tok;
@@ -1029,13 +1012,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
-      ok = take(); /* under the last product */
-      if (!ok) break;
       ok = warp_wait(&sm->oready[s], o_par, abort);
       if (!ok) break;
       o_par ^= 1;
       tc_fence_after();
       if (busy) {
+        /* the lane again, so that addresses made of it are not kept across the pieces */
+        int ln = lane;
+        asm volatile("" : "+r"(ln));
         /* rows of O through this warp's part of Q (read by now), so that a row's
          * columns are written together */
         const bool whole = c.own && c.key0 == 0 && c.n == c.nt; /* nothing to merge */
@@ -1093,25 +1077,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();
+      fence_async_smem(); /* this warp's part of Q may be loaded over */
+      __syncwarp();
+      if (lane == 0) bar_arrive(&sm->q_free[s]);
     }
   }
-  /* the cut for attn_merge, off the way to the first product */
-  if (blockIdx.x == 0) {
-    if (tid == 0) {
-      a.sched[0] = !sound;
-      a.sched[1] = sound ? sm->total : 0;
-      a.sched[2] = sound ? sm->pairs : 0;
-      if (!sound) *(volatile int32_t *)a.err_host = MK_ERR_INVALID_ARG;
-    }
-    if (sound) {
-      int32_t *w = a.sched + 4;
-      for (int i = tid; i <= max(a.n_groups, a.n_seqs); i += kThreads)
-        for (int k = 0; k < 2; ++k) {
-          if (i <= a.n_groups) w[2 * k * kSchedStride + i] = sm->cum_g[k][i];
-          if (i <= a.n_seqs) w[(2 * k + 1) * kSchedStride + i] = sm->cum_s[k][i];
-          if (i < a.n_groups) w[4 * kSchedStride + i] = shared_keys(a, sm, i);
-        }
-    }
+  if (blockIdx.x == 0 && tid == 0) {
+    *a.bad = !sound;
+    if (!sound) *(volatile int32_t *)a.err_host = MK_ERR_INVALID_ARG;
   }
   __syncthreads();
   if (tid == 0 && *abort) *(volatile int32_t *)a.err_host = MK_ERR_DEVICE_TIMEOUT;
@@ -1123,144 +1096,103 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 /* ---- the join ----------------------------------------------------------------- */
 
-/* M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over a row's pieces, by
- * W warps a row: one where rows are many, all eight of a block where they are few and
- * have many pieces each.  Reads L2: the partials were written just before.  What bounds
- * it is its chain of loads, so look-ups go 32 places at a time and a lane's row of
- * pieces is in flight together. */
-template <int D, int W>
+/* M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over a row's pieces.  A
+ * block has a token and kv head; its warps take the heads of the group, several a head
+ * where there are fewer than eight.  Reads L2: the partials were written just before.
+ * What bounds it is its chain of three loads (where, maxima and sums, weighted sums), so
+ * 32 pieces' maxima and eight pieces' sums are in flight together. */
+template <int D>
 __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a, int n_cta) {
+  __shared__ float sums[8][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tok = blockIdx.x / a.Hkv, kvh = blockIdx.x - tok * a.Hkv;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long orow = (long long)blockIdx.x * (8 / W) + warp / W;
-  const int part = warp % W;
-  const int bad = a.sched[0], total = a.sched[1], n_pairs = a.sched[2];
-  const int tokens = a.off ? a.off[a.n_seqs] : a.n_seqs;
-  const int tok = (int)(orow / a.Hq), head = (int)(orow - (long long)tok * a.Hq);
-  if (bad || tok >= tokens) return; /* the same for all W warps */
-  const int TB = a.TB, BT = 2 * TB, ctas = active_ctas(total, n_cta);
-  const int kvh = head / a.G, hg = head - kvh * a.G;
-  const int32_t *cut = a.sched + 4;
-  const int b = a.off ? warp_find(a.off, a.n_seqs + 1, tok) : tok;
-  const int first = a.off ? a.off[b] : b, T = a.off ? a.off[b + 1] - first : 1, len = a.lens[b];
-  int plen = 0, n_shared = 0, n_own = 0;  /* pieces */
-  int ws = 0, wo = 0;                     /* their first workers: CTAs, or streams */
-  long long xs = 0, xo = 0;               /* this row in worker 0's own place */
-  int ss = 0, so = 0;                     /* rows from one worker's place to the next */
+  int4 *at = a.where + blockIdx.x; /* and as many behind as there are blocks */
+  const int bad = *a.bad, tokens = a.off ? a.off[a.n_seqs] : a.n_seqs;
+  const int4 ws = at[0], wo = at[gridDim.x];
+  if (bad || tok >= tokens) return;
+  __syncthreads(); /* read by all: cleared for the next call */
+  if (threadIdx.x < 2) at[threadIdx.x * gridDim.x] = make_int4(0, 0, 0, 0);
+  if (wo.x == 1) return; /* written by attn_tiles */
+  const int n_shared = ws.x ? ws.x - 1 : 0, n = n_shared + (wo.x ? wo.x - 1 : 0);
+  int split = 8; /* warps a head */
+  while (split > 1 && 8 / split < a.G) split >>= 1;
+  const int part = warp % split, lanes_of_heads = 8 / split;
   const long long dense = (long long)a.n_tokens * a.Hq;
-  /* a stream without singles between two that have some: only of the CTA whose share
-   * holds the last pairs and one place of the singles */
-  int none = -1;
-  if (n_pairs > 0 && n_pairs < total) {
-    const int c = cta_of(n_pairs, total, ctas);
-    if (share_begin(c + 1, total, ctas) - n_pairs == 1) none = 2 * c + 1;
-  }
-  auto worker = [&](int line, int x) {
-    if (line == 0) return cta_of(x, total, ctas);
-    const int c = cta_of(n_pairs + x, total, ctas);
-    const int s0 = max(share_begin(c, total, ctas), n_pairs) - n_pairs;
-    const int s1 = share_begin(c + 1, total, ctas) - n_pairs;
-    return 2 * c + (x >= ((s0 + s1 + 1) >> 1));
-  };
-  auto pieces = [&](int line, int begin, int tiles, int ti, int &w0, long long &at, int &step) {
-    w0 = worker(line, begin + fixed_cost(line));
-    const int w1 = worker(line, begin + fixed_cost(line) + tiles - 1);
-    const int tile = ti >= TB; /* of a pair */
-    step = line == 0 ? 2 * kTile : kTile;
-    at = 2 * dense + (line == 0 ? 0 : 2ll * n_cta * kTile) + tile * kTile + (ti - tile * TB) * a.G + hg;
-    return w1 - w0 + 1 - (line == 1 && w0 < none && none < w1);
-  };
-  if (a.n_groups) {
-    const int g = warp_find(a.starts, a.n_groups + 1, b);
-    plen = cut[4 * kSchedStride + g];
-    if (plen) {
-      const int s0 = a.starts[g], s1 = a.starts[g + 1];
-      const int gtok = a.off ? a.off[s0] : s0, gT = (a.off ? a.off[s1] : s1) - gtok;
-      const int nt = key_tiles(0, plen), nb = pair_blocks(gT, TB);
-      const int j = gT <= BT ? 0 : (tok - gtok) / BT, line = j < nb ? 0 : 1;
-      const int begin = cut[2 * line * kSchedStride + g] +
-                        (line == 0 ? kvh * nb + j : kvh) * item_cost(line, nt);
-      n_shared = pieces(line, begin, nt, tok - gtok - j * BT, ws, xs, ss);
-    }
-  }
-  const int nb = pair_blocks(T, TB), jb = T <= BT ? 0 : (tok - first) / BT, line = jb < nb ? 0 : 1;
-  const int nt_own = key_tiles(plen, block_end(len, T, TB, jb));
-  if (nt_own) {
-    const int32_t *cum = cut + (2 * line + 1) * kSchedStride;
-    const int in_groups = cut[2 * line * kSchedStride + a.n_groups];
-    int begin = in_groups + cum[b] + (cum[b + 1] - cum[b]) / a.Hkv * kvh;
-    if (line == 0)
-      for (int j = 0; j < jb; ++j) begin += item_cost(0, key_tiles(plen, block_end(len, T, TB, j)));
-    n_own = pieces(line, begin, nt_own, tok - first - jb * BT, wo, xo, so);
-  }
-  if (n_shared == 0 && n_own == 1) return; /* written by attn_tiles */
-  const int n = n_shared + n_own;
-  auto place = [&](int i) -> long long { /* partial row of piece i */
-    const bool own = i >= n_shared;
-    const int k = own ? i - n_shared : i;
-    if (k == 0) return own ? dense + orow : orow;
-    const int step = own ? so : ss, w0 = own ? wo : ws;
-    int w = w0 + k;
-    if (step == kTile && w0 < none && none <= w) ++w;
-    return (own ? xo : xs) + (long long)w * step;
-  };
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[place(i)].x);
+  for (int hg0 = 0; hg0 < a.G; hg0 += lanes_of_heads) {
+    const int hg = hg0 + warp / split;
+    const bool mine = hg < a.G;
+    const long long orow = (long long)tok * a.Hq + kvh * a.G + min(hg, a.G - 1);
+    auto place = [&](int i) -> long long { /* partial row of piece i */
+      const bool own = i >= n_shared;
+      const int k = own ? i - n_shared : i;
+      if (k == 0) return (own ? dense : 0) + orow;
+      const int4 w = own ? wo : ws;
+      int worker = w.y + k;
+      if (w.z >= 0 && worker >= w.z) ++worker;
+      const int step = w.w >> 30 ? kTile : 2 * kTile;
+      return 2 * dense + (long long)worker * step + (w.w & 0x3fffffff) + hg;
+    };
+    constexpr int N = D / 32; /* columns a lane */
+    float o[N] = {}, l = 0.0f, M = -INFINITY;
+    if (mine)
+      for (int i = lane; i < n; i += 32) M = fmaxf(M, a.part_ml[place(i)].x);
 #pragma unroll
-  for (int w = 16; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-  constexpr int N = D / 32; /* columns a lane */
-  float o[N] = {}, l = 0.0f;
-  if (M != -INFINITY) {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      float f = 0.0f;
-      long long at = 0;
-      if (i0 + lane < n) {
-        at = place(i0 + lane);
-        const float2 ml = a.part_ml[at];
-        f = exp2_approx(ml.x - M);
-        l += f * ml.y;
+    for (int w = 16; w; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    if (M != -INFINITY) {
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        float f = 0.0f;
+        long long row = 0;
+        if (i0 + lane < n) {
+          row = place(i0 + lane);
+          const float2 ml = a.part_ml[row];
+          f = exp2_approx(ml.x - M);
+          l += f * ml.y;
+        }
+        const int m = min(32, n - i0);
+#pragma unroll 8
+        for (int i = part; i < m; i += split) {
+          const float w = __shfl_sync(0xffffffffu, f, i);
+          const float *src = a.part + __shfl_sync(0xffffffffu, row, i) * D + lane * N;
+          float v[N];
+          if (N == 4)
+            *(float4 *)v = *(const float4 *)src;
+          else if (N == 2)
+            *(float2 *)v = *(const float2 *)src;
+          else
+            v[0] = src[0];
+#pragma unroll
+          for (int k = 0; k < N; ++k) o[k] = fmaf(w, v[k], o[k]);
+        }
       }
-      const int m = min(32, n - i0);
-#pragma unroll 4
-      for (int i = part; i < m; i += W) {
-        const float w = __shfl_sync(0xffffffffu, f, i);
-        const float *src = a.part + __shfl_sync(0xffffffffu, at, i) * D + lane * N;
-        float v[N];
-        if (N == 4)
-          *(float4 *)v = *(const float4 *)src;
-        else if (N == 2)
-          *(float2 *)v = *(const float2 *)src;
-        else
-          v[0] = src[0];
 #pragma unroll
-        for (int k = 0; k < N; ++k) o[k] = fmaf(w, v[k], o[k]);
-      }
+      for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
     }
+    if (split > 1) { /* the warps' sums, in order */
 #pragma unroll
-    for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(0xffffffffu, l, w);
-  }
-  if (W > 1) { /* the warps' sums, in order */
-    __shared__ float sums[W > 1 ? W : 1][D];
+      for (int k = 0; k < N; ++k) sums[warp][k * 32 + lane] = o[k];
+      __syncthreads();
+      if (part == 0)
+        for (int w = 1; w < split; ++w)
 #pragma unroll
-    for (int k = 0; k < N; ++k) sums[part][k * 32 + lane] = o[k];
-    __syncthreads();
-    if (part) return;
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-      for (int w = 1; w < W; ++w) o[k] += sums[w][k * 32 + lane];
+          for (int k = 0; k < N; ++k) o[k] += sums[warp + w][k * 32 + lane];
+      __syncthreads();
+    }
+    if (!mine || part) continue;
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    __nv_bfloat16 *dst = a.out + orow * D + lane * N;
+    if (N == 4) {
+      *(uint2 *)dst =
+          make_uint2(pack_bf16(o[0] * inv, o[1 % N] * inv), pack_bf16(o[2 % N] * inv, o[3 % N] * inv));
+    } else if (N == 2) {
+      *(uint32_t *)dst = pack_bf16(o[0] * inv, o[1 % N] * inv);
+    } else {
+      *dst = __float2bfloat16_rn(o[0] * inv);
+    }
+    if (a.lse && lane == 0)
+      a.lse[orow] = l > 0.0f ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-  __nv_bfloat16 *dst = a.out + orow * D + lane * N;
-  if (N == 4) {
-    *(uint2 *)dst = make_uint2(pack_bf16(o[0] * inv, o[1 % N] * inv), pack_bf16(o[2 % N] * inv, o[3 % N] * inv));
-  } else if (N == 2) {
-    *(uint32_t *)dst = pack_bf16(o[0] * inv, o[1 % N] * inv);
-  } else {
-    *dst = __float2bfloat16_rn(o[0] * inv);
-  }
-  if (a.lse && lane == 0)
-    a.lse[orow] = l > 0.0f ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 /* Makes `dev` current for a scope. */
@@ -1291,7 +1223,7 @@ struct mk_attn {
   cudaStream_t stream = nullptr;
   int dev = 0, n_sm = 0;
   uint8_t *ws = nullptr;
-  size_t o_part = 0, o_ml = 0;
+  size_t o_where = 0, o_part = 0, o_ml = 0;
   int32_t *err_host = nullptr, *err_dev = nullptr;
 };
 
@@ -1305,7 +1237,7 @@ cudaError_t prepare() {
 }
 
 template <int D>
-cudaError_t launch(const mk_attn *at, int layer, const Args &a) {
+cudaError_t launch(const mk_attn *at, int layer, const CUtensorMap &qmap, const Args &a) {
   cudaLaunchAttribute pdl[1];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
@@ -1316,16 +1248,13 @@ cudaError_t launch(const mk_attn *at, int layer, const Args &a) {
   cfg.stream = at->stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  cudaError_t e =
-      cudaLaunchKernelEx(&cfg, attn_tiles<D>, at->maps[2 * layer], at->maps[2 * layer + 1], a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tiles<D>, qmap, at->maps[2 * layer],
+                                     at->maps[2 * layer + 1], a);
   if (e != cudaSuccess) return e;
-  const long long rows = (long long)a.n_tokens * a.Hq;
-  const bool few = rows <= kFewRows;
-  cfg.gridDim = dim3((unsigned)(few ? rows : (rows + 7) / 8));
+  cfg.gridDim = dim3((unsigned)a.n_tokens * a.Hkv);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return few ? cudaLaunchKernelEx(&cfg, attn_merge<D, 8>, a, at->n_sm)
-             : cudaLaunchKernelEx(&cfg, attn_merge<D, 1>, a, at->n_sm);
+  return cudaLaunchKernelEx(&cfg, attn_merge<D>, a, at->n_sm);
 }
 
 }  // namespace
@@ -1381,10 +1310,13 @@ mk_status mk_attn_create(const mk_attn_desc *d, void *stream, mk_attn **out) {
     return st;
   }
   const size_t rows = 2 * (size_t)d->max_tokens * d->n_q_heads + (size_t)at->n_sm * 4 * kTile;
-  at->o_part = ((4 + 5 * (size_t)kSchedStride) * 4 + 255) / 256 * 256;
+  at->o_where = 256;
+  at->o_part = at->o_where + (2 * (size_t)d->max_tokens * d->n_kv_heads * sizeof(int4) + 255) / 256 * 256;
   at->o_ml = at->o_part + rows * d->head_dim * 4;
   cudaError_t e = d->head_dim == 32 ? prepare<32>() : d->head_dim == 64 ? prepare<64>() : prepare<128>();
   if (e == cudaSuccess) e = cudaMalloc(&at->ws, at->o_ml + rows * sizeof(float2));
+  if (e == cudaSuccess) e = cudaMemsetAsync(at->ws, 0, at->o_part, at->stream);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(at->stream);
   if (e == cudaSuccess) e = cudaHostAlloc(&at->err_host, 64, cudaHostAllocMapped);
   if (e == cudaSuccess) {
     std::memset(at->err_host, 0, 64);
@@ -1446,8 +1378,6 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   a.off = b->q_offsets;
   a.starts = b->group_starts;
   a.prefix = b->prefix_lens;
-  a.q = (const __nv_bfloat16 *)q;
-  a.q_stride = q_token_stride;
   a.out = (__nv_bfloat16 *)out;
   a.lse = lse;
   a.scale_log2 = at->scale_log2;
@@ -1455,12 +1385,16 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   a.inv_g = (65536 + a.G - 1) / a.G;
   a.inv_p = ((1ull << 38) + a.P - 1) / a.P;
   a.err_host = at->err_dev;
-  a.sched = (int32_t *)at->ws;
+  a.bad = (int32_t *)at->ws;
+  a.where = (int4 *)(at->ws + at->o_where);
   a.part = (float *)(at->ws + at->o_part);
   a.part_ml = (float2 *)(at->ws + at->o_ml);
-  const cudaError_t e = d.head_dim == 32   ? launch<32>(at, layer, a)
-                        : d.head_dim == 64 ? launch<64>(at, layer, a)
-                                           : launch<128>(at, layer, a);
+  CUtensorMap qmap;
+  const mk_status st = mk_encode_q_map(&d, q, b->n_tokens, q_token_stride, a.TB, &qmap);
+  if (st != MK_OK) return st;
+  const cudaError_t e = d.head_dim == 32   ? launch<32>(at, layer, qmap, a)
+                        : d.head_dim == 64 ? launch<64>(at, layer, qmap, a)
+                                           : launch<128>(at, layer, qmap, a);
   return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 

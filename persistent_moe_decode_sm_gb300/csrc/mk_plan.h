@@ -54,6 +54,12 @@ int mk_fold_rows(const mk_model_dims *d);
  * columns, box_rows rows}, swizzled over the box's row (64 or 128 bytes). */
 mk_status mk_encode_rows_map(const mk_attn_desc *d, const void *pool, int box_rows, void *host_out);
 
+/* Encodes a 3-D TMA tensor map (128 bytes) over query rows [n_tokens][n_q_heads]
+ * [head_dim] with token_stride elements from a token to the next: box {min(head_dim, 64)
+ * dims, the heads of one kv head, box_tokens}, swizzled like the K and V boxes. */
+mk_status mk_encode_q_map(const mk_attn_desc *d, const void *q, int n_tokens, int64_t token_stride,
+                          int box_tokens, void *host_out);
+
 mk_status mk_validate_dims(const mk_model_dims *d);
 /* u_seen > 0: the distinct experts per layer observed at this batch size,
  * used in place of the uniform-routing expectation for the role split. */
