@@ -260,15 +260,7 @@ __device__ __forceinline__ void tmem_ld128(uint32_t at, float *v) {
       : "memory");
 #undef OUT
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *v) {
 #define IN(i) "r"(v[i])
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-      "%29, %30, %31};" ::R32(IN, 0),
-      "r"(at)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *v) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -915,6 +907,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int b = c.own ? c.seq : a.off ? find(sm->off, a.n_seqs + 1, tok) : tok;
       /* keys of the item that this row sees end here */
       const int limit = min(c.kend, sm->len[b] - (sm->off[b + 1] - tok) + 1);
+      const int warp_limit = __reduce_min_sync(0xffffffffu, limit);
       float m = -INFINITY, l = 0.0f; /* m in score units */
 #pragma unroll 1
       for (int t = 0; t < c.n; ++t) {
@@ -954,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float x[kTile];
         tmem_ld128(at_s, x);
-        if (!__all_sync(0xffffffffu, limit >= k0 + kTile)) {
+        if (warp_limit < k0 + kTile) {
           const int d = limit - k0;
 #pragma unroll
           for (int i = 0; i < kTile; ++i) x[i] = i < d ? x[i] : -INFINITY;
@@ -990,24 +983,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float off = m == -INFINITY ? 0.0f : -m * c2;
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        /* P in two halves: the product of the first starts under the second */
+        /* P in quarters; the product of the first half starts under the second.  A quarter's
+         * store lands while the next is computed. */
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+        for (int h = 0; h < 4; ++h) {
+          uint32_t w[16];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            float2 e = fma2(make_float2(x[h * 64 + 2 * k], x[h * 64 + 2 * k + 1]),
+          for (int k = 0; k < 16; ++k) {
+            float2 e = fma2(make_float2(x[h * 32 + 2 * k], x[h * 32 + 2 * k + 1]),
                             make_float2(c2, c2), make_float2(off, off));
             e.x = exp2_approx(e.x);
             e.y = exp2_approx(e.y);
             sum[k & 1] = add2(sum[k & 1], e);
             w[k] = pack_bf16(e.x, e.y);
           }
-          tmem_st32(at_s + h * 32, w);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) bar_arrive(&sm->pready[s][h]);
+          if (h != 2) tmem_st16(at_s + h * 16, w);
+          if (h >= 2) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm->pready[s][h - 2]);
+          }
+          if (h == 2) tmem_st16(at_s + h * 16, w);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
@@ -1097,33 +1094,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 /* ---- the join ----------------------------------------------------------------- */
 
 /* M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over a row's pieces.  A
- * block has a token and kv head; its warps take the heads of the group, several a head
+ * block has a token and kv head, or some heads of its group (`blocks` blocks, a cluster,
+ * share it) where there are too few for all SMs; its warps take the heads, several a head
  * where there are fewer than eight.  Reads L2: the partials were written just before.
  * What bounds it is its chain of three loads (where, maxima and sums, weighted sums), so
  * 32 pieces' maxima and eight pieces' sums are in flight together. */
 template <int D>
-__global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a, int n_cta) {
+__global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a, int n_cta, int blocks) {
   __shared__ float sums[8][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tok = blockIdx.x / a.Hkv, kvh = blockIdx.x - tok * a.Hkv;
+  const int unit = blockIdx.x / blocks, rank = blockIdx.x - unit * blocks, units = a.n_tokens * a.Hkv;
+  const int tok = unit / a.Hkv, kvh = unit - tok * a.Hkv;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  int4 *at = a.where + blockIdx.x; /* and as many behind as there are blocks */
   const int bad = *a.bad, tokens = a.off ? a.off[a.n_seqs] : a.n_seqs;
-  const int4 ws = at[0], wo = at[gridDim.x];
+  const int4 ws = a.where[unit], wo = a.where[units + unit];
   if (bad || tok >= tokens) return;
-  __syncthreads(); /* read by all: cleared for the next call */
-  if (threadIdx.x < 2) at[threadIdx.x * gridDim.x] = make_int4(0, 0, 0, 0);
+  /* read by all: cleared for the next call */
+  __syncthreads();
+  if (blocks > 1)
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+  if (rank == 0 && threadIdx.x < 2) a.where[threadIdx.x * units + unit] = make_int4(0, 0, 0, 0);
   if (wo.x == 1) return; /* written by attn_tiles */
   const int n_shared = ws.x ? ws.x - 1 : 0, n = n_shared + (wo.x ? wo.x - 1 : 0);
+  const int heads = (a.G + blocks - 1) / blocks, h0 = rank * heads, h1 = min(a.G, h0 + heads);
   int split = 8; /* warps a head */
-  while (split > 1 && 8 / split < a.G) split >>= 1;
-  const int part = warp % split, lanes_of_heads = 8 / split;
+  while (split > 1 && 8 / split < heads) split >>= 1;
+  const int part = warp % split, at_once = 8 / split;
   const long long dense = (long long)a.n_tokens * a.Hq;
-  for (int hg0 = 0; hg0 < a.G; hg0 += lanes_of_heads) {
-    const int hg = hg0 + warp / split;
-    const bool mine = hg < a.G;
-    const long long orow = (long long)tok * a.Hq + kvh * a.G + min(hg, a.G - 1);
+  for (int hg0 = h0; hg0 < h1; hg0 += at_once) {
+    const int hg = min(hg0 + warp / split, a.G - 1);
+    const bool mine = hg0 + warp / split < h1;
+    const long long orow = (long long)tok * a.Hq + kvh * a.G + hg;
     auto place = [&](int i) -> long long { /* partial row of piece i */
       const bool own = i >= n_shared;
       const int k = own ? i - n_shared : i;
@@ -1238,7 +1240,7 @@ cudaError_t prepare() {
 
 template <int D>
 cudaError_t launch(const mk_attn *at, int layer, const CUtensorMap &qmap, const Args &a) {
-  cudaLaunchAttribute pdl[1];
+  cudaLaunchAttribute pdl[2];
   pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   pdl[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
@@ -1251,10 +1253,15 @@ cudaError_t launch(const mk_attn *at, int layer, const CUtensorMap &qmap, const 
   cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tiles<D>, qmap, at->maps[2 * layer],
                                      at->maps[2 * layer + 1], a);
   if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((unsigned)a.n_tokens * a.Hkv);
+  int blocks = 1;
+  while (2 * blocks <= a.G && blocks < 8 && a.n_tokens * a.Hkv * blocks < 2 * at->n_sm) blocks *= 2;
+  pdl[1].id = cudaLaunchAttributeClusterDimension;
+  pdl[1].val.clusterDim = {(unsigned)blocks, 1, 1};
+  cfg.numAttrs = 2;
+  cfg.gridDim = dim3((unsigned)a.n_tokens * a.Hkv * blocks);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_merge<D>, a, at->n_sm);
+  return cudaLaunchKernelEx(&cfg, attn_merge<D>, a, at->n_sm, blocks);
 }
 
 }  // namespace
