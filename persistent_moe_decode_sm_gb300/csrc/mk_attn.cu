@@ -39,7 +39,11 @@ namespace {
 constexpr int kThreads = 384;      /* two softmax warpgroups, two producers, two issuers */
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88; /* 256 * 208 + 128 * 88 = 384 * 168 */
 constexpr int kTile = 128;         /* keys per tile; rows per row tile */
-constexpr int kPairCost = 3, kSingleCost = 2; /* an item's beginning and end, in tiles */
+/* The line's unit is about 1100 cycles.  A tile takes 3300 of a CTA in a pair (its two
+ * products and softmaxes, mostly hidden under one another) and 2300 in a single (64 KB at
+ * the SM's share of HBM); an item's beginning and end take 8000 and 4000 on top. */
+constexpr int kPairTile = 3, kSingleTile = 2, kPairItem = 8, kSingleItem = 4;
+constexpr int kShare = 6; /* a CTA's share at least: each of its streams meets a tile of a long item */
 constexpr int kQueue = 4;          /* pieces that a producer is ahead of its stream */
 constexpr int kMaxSeqs = 1024, kMaxGroups = 512; /* of a call: the cut's tables are in shared memory */
 constexpr uint64_t kWaitLimit = 2000000000ull; /* ns */
@@ -65,8 +69,8 @@ struct Args {
   int32_t *bad;      /* the batch is not sound */
   int4 *where;       /* [2][n_tokens][Hkv], zero between calls: where a token's partials are, of
                       * the shared keys and of its own.  x: pieces + 1, 1: written already, 0:
-                      * none; y: the first piece's worker; z: a worker to leave out, or -1; w:
-                      * the token's first row in worker 0's place, bit 30: workers are streams */
+                      * none; y: the first piece's worker; z: the token's first row in worker 0's
+                      * place; w: rows from a worker's place to the next */
   float *part;       /* [2 * n_tokens * Hq + 4 * SMs * 128][D] weighted sums */
   float2 *part_ml;   /* the same rows: maximum (in powers of two), sum */
 };
@@ -221,7 +225,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
 }
 #define R8(x, i) x(i), x(i + 1), x(i + 2), x(i + 3), x(i + 4), x(i + 5), x(i + 6), x(i + 7)
 #define R32(x, i) R8(x, i), R8(x, i + 8), R8(x, i + 16), R8(x, i + 24)
-/* 16, 32 or 128 columns of this thread's TMEM lane.  The load and its wait are one
+/* 16, 32, 64 or 128 columns of this thread's TMEM lane.  The load and its wait are one
  * statement: between two, the compiler could move registers that have not landed. */
 #define OUT(i) "=f"(v[i])
 __device__ __forceinline__ void tmem_ld16(uint32_t at, float *v) {
@@ -240,6 +244,18 @@ __device__ __forceinline__ void tmem_ld32(uint32_t at, float *v) {
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
       "tcgen05.wait::ld.sync.aligned;"
       : R32(OUT, 0)
+      : "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld64(uint32_t at, float *v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
+      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : R32(OUT, 0), R32(OUT, 32)
       : "r"(at)
       : "memory");
 }
@@ -317,13 +333,20 @@ __device__ __forceinline__ int block_end(int len, int T, int TB, int j) {
 __device__ __forceinline__ int key_tiles(int begin, int end) {
   return end > begin ? (end - begin + kTile - 1) / kTile : 0;
 }
-__device__ __forceinline__ int fixed_cost(int line) { return line ? kSingleCost : kPairCost; }
+/* An item begins with its fixed cost; tile t then begins t tile costs further on, and
+ * belongs to the worker that owns its first place. */
+__device__ __forceinline__ int fixed_cost(int line) { return line ? kSingleItem : kPairItem; }
+__device__ __forceinline__ int tile_cost(int line) { return line ? kSingleTile : kPairTile; }
 __device__ __forceinline__ int item_cost(int line, int tiles) {
-  return tiles ? tiles + fixed_cost(line) : 0;
+  return tiles ? tiles * tile_cost(line) + fixed_cost(line) : 0;
 }
-/* CTAs that take part: each has two places of the line at least, one a stream. */
+/* CTAs that take part.  With kShare places each, every worker whose share lies between an
+ * item's first tile and its last has a tile of it: a CTA's 6 places hold one of a pair's
+ * tiles, a stream's 3 one of a single's.  (The CTA whose share holds the last pairs may have
+ * fewer singles, but those begin with an item's fixed cost: with up to 4 of them no tile, with
+ * up to 8 the first tile in stream 1, with 9 or more tiles in both.) */
 __device__ __forceinline__ int active_ctas(int total, int n_cta) {
-  return max(1, min(n_cta, total >> 1));
+  return max(1, min(n_cta, total / kShare));
 }
 /* Where CTA c's share of the line begins. */
 __device__ __forceinline__ int share_begin(int c, int total, int n) {
@@ -499,7 +522,7 @@ __device__ bool take_cut(const Args &a, Smem *sm) {
  * behind it.  A share that ends within an item's fixed cost has no tile of it: n is
  * 0.  By a whole warp. */
 __device__ __forceinline__ Piece next_piece(const Args &a, const Smem *sm, int line, int &x, int end) {
-  const int TB = a.TB, ng = a.n_groups, fixed = fixed_cost(line);
+  const int TB = a.TB, ng = a.n_groups;
   const int in_groups = sm->cum_g[line][ng];
   Piece p;
   p.line = line;
@@ -515,8 +538,8 @@ __device__ __forceinline__ Piece next_piece(const Args &a, const Smem *sm, int l
     p.nt = key_tiles(0, p.kend);
     const int nb = pair_blocks(T, TB);
     begin = sm->cum_g[line][g];
-    const int item = (x - begin) / (p.nt + fixed);
-    begin += item * (p.nt + fixed);
+    const int cost = item_cost(line, p.nt), item = (x - begin) / cost;
+    begin += item * cost;
     p.kvh = line == 0 ? item / nb : item;
     j = line == 0 ? item - p.kvh * nb : nb;
   } else {
@@ -541,9 +564,12 @@ __device__ __forceinline__ Piece next_piece(const Args &a, const Smem *sm, int l
   }
   p.tok0 = first + j * 2 * TB;
   p.ntok = min(2 * TB, T - j * 2 * TB);
-  p.t0 = max(0, x - begin - fixed);
-  p.n = max(0, min(p.nt, end - begin - fixed) - p.t0);
-  x = min(end, begin + p.nt + fixed);
+  const int tile = tile_cost(line), at = begin + fixed_cost(line);
+  p.t0 = line ? (max(0, x - at) + kSingleTile - 1) / kSingleTile : (max(0, x - at) + kPairTile - 1) / kPairTile;
+  const int t1 = line ? (max(0, end - at) + kSingleTile - 1) / kSingleTile
+                      : (max(0, end - at) + kPairTile - 1) / kPairTile;
+  p.n = max(0, min(p.nt, t1) - p.t0);
+  x = min(end, at + p.nt * tile);
   p.begin = begin;
   return p;
 }
@@ -555,7 +581,8 @@ __device__ __forceinline__ void tell_merge(const Args &a, const Smem *sm, const 
   int w[2];
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) { /* the workers of the item's first tile and its last */
-    const int x = p.begin + fixed_cost(p.line) + (k ? p.nt - 1 : 0) + (p.line ? pairs : 0);
+    const int x = p.begin + fixed_cost(p.line) + (k ? (p.nt - 1) * tile_cost(p.line) : 0) +
+                  (p.line ? pairs : 0);
     const int c = cta_of(x, total, n);
     w[k] = c;
     if (p.line) {
@@ -563,22 +590,14 @@ __device__ __forceinline__ void tell_merge(const Args &a, const Smem *sm, const 
       w[k] = 2 * c + (x - pairs >= ((s0 + s1 - 2 * pairs + 1) >> 1));
     }
   }
-  /* a stream without singles between two that have some: only of the CTA whose share
-   * holds the last pairs and one place of the singles */
-  int none = -1;
-  if (p.line && pairs > 0) {
-    const int c = cta_of(pairs, total, n);
-    if (share_begin(c + 1, total, n) - pairs == 1 && w[0] < 2 * c + 1 && 2 * c + 1 < w[1])
-      none = 2 * c + 1;
-  }
   const bool whole = p.own && p.key0 == 0 && p.n == p.nt;
-  const int pieces = w[1] - w[0] + 1 - (none >= 0);
+  const int pieces = w[1] - w[0] + 1;
   const int lane = threadIdx.x & 31;
   for (int i = lane; i < p.ntok; i += 32) {
     const int tile = i >= a.TB;
     const int row = (p.line ? 2 * (int)gridDim.x * kTile : tile * kTile) + (i - tile * a.TB) * a.G;
     a.where[((long long)p.own * a.n_tokens + p.tok0 + i) * a.Hkv + p.kvh] =
-        make_int4(whole ? 1 : pieces + 1, w[0], none, row | p.line << 30);
+        make_int4(whole ? 1 : pieces + 1, w[0], row, p.line ? kTile : 2 * kTile);
   }
 }
 
@@ -1024,43 +1043,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long dense = (long long)a.n_tokens * a.Hq;
         const long long extra =
             2 * dense + (pair ? 2ll * blockIdx.x + s : 2ll * n_cta + 2ll * blockIdx.x + s) * kTile;
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
         constexpr int W = D / 2, CR = C::ROWB / 16; /* columns staged at a time; float4 of a swizzled row */
         constexpr int RL = W / 4, RI = 32 / RL;     /* lanes of a row, rows at a time */
-        constexpr int LW = W < 32 ? 16 : 32;
+        const int ch = ln % RL, mine = min(32, crows - w0); /* rows of this warp */
+        float *to = a.part + (c.t0 ? extra : c.own * dense + row0) * D + ch * 4;
+        const float f = !whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll 1
         for (int i0 = 0; i0 < D; i0 += W) {
+          float o[W];
+          if (W == 64)
+            tmem_ld64(at_o + i0, o);
+          else if (W == 32)
+            tmem_ld32(at_o + i0, o);
+          else
+            tmem_ld16(at_o + i0, o);
 #pragma unroll
-          for (int i = 0; i < W; i += LW) {
-            float o[LW];
-            if (LW == 32)
-              tmem_ld32(at_o + i0 + i, o);
-            else
-              tmem_ld16(at_o + i0 + i, o);
-#pragma unroll
-            for (int k = 0; k < LW / 4; ++k) {
-              const int ch = i / 4 + k;
-              *(float4 *)(qd + ch / CR * C::BLOCK + ln * C::ROWB +
-                          ((ch % CR) ^ (ln & (CR - 1))) * 16) =
-                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            }
-          }
+          for (int k = 0; k < W / 4; ++k)
+            *(float4 *)(qd + k / CR * C::BLOCK + ln * C::ROWB + ((k % CR) ^ (ln & (CR - 1))) * 16) =
+                make_float4(o[4 * k] * f, o[4 * k + 1] * f, o[4 * k + 2] * f, o[4 * k + 3] * f);
           __syncwarp();
-          const int ch = ln % RL;
-#pragma unroll 2
-          for (int i = 0; i < 32 / RI; ++i) {
-            const int row = i * RI + ln / RL, rr = w0 + row, qt = (rr * a.inv_g) >> 16;
-            const float4 o = *(const float4 *)(qd + ch / CR * C::BLOCK + row * C::ROWB +
+#pragma unroll 4
+          for (int row = ln / RL; row < mine; row += RI) {
+            const int rr = w0 + row, qt = (rr * a.inv_g) >> 16;
+            const float4 v = *(const float4 *)(qd + ch / CR * C::BLOCK + row * C::ROWB +
                                                ((ch % CR) ^ (row & (CR - 1))) * 16);
-            const long long dr = row0 + (long long)qt * a.Hq + (rr - qt * a.G);
-            const float f = __shfl_sync(0xffffffffu, inv, row);
-            if (rr < crows) {
-              if (whole)
-                *(uint2 *)(a.out + dr * D + i0 + ch * 4) =
-                    make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
-              else
-                *(float4 *)(a.part + (c.t0 ? extra + rr : c.own * dense + dr) * D + i0 + ch * 4) = o;
-            }
+            const int at = c.t0 ? rr : qt * a.Hq + (rr - qt * a.G); /* row behind `to` */
+            if (whole)
+              *(uint2 *)(a.out + (long long)(row0 + at) * D + ch * 4 + i0) =
+                  make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+            else
+              *(float4 *)(to + (long long)at * D + i0) = v;
           }
           __syncwarp();
         }
@@ -1131,10 +1143,7 @@ __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a
       const int k = own ? i - n_shared : i;
       if (k == 0) return (own ? dense : 0) + orow;
       const int4 w = own ? wo : ws;
-      int worker = w.y + k;
-      if (w.z >= 0 && worker >= w.z) ++worker;
-      const int step = w.w >> 30 ? kTile : 2 * kTile;
-      return 2 * dense + (long long)worker * step + (w.w & 0x3fffffff) + hg;
+      return 2 * dense + (long long)(w.y + k) * w.w + w.z + hg;
     };
     constexpr int N = D / 32; /* columns a lane */
     float o[N] = {}, l = 0.0f, M = -INFINITY;
