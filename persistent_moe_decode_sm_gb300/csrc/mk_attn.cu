@@ -51,10 +51,6 @@ constexpr uint64_t kWaitLimit = 2000000000ull; /* ns */
  * of two): P then stays below 2^8, exact in its relative precision, and the
  * accumulator is rescaled a few times per row rather than in most tiles. */
 constexpr float kSlack = 8.0f;
-/* Stream 1 begins a pair this many cycles behind stream 0, so that one's softmax runs
- * under the other's products; in step, both softmaxes would leave the tensor cores idle. */
-constexpr int kPairLag = 1200;
-
 struct Args {
   int32_t Hq, Hkv, G, P, num_pages, max_pages, n_seqs, n_tokens, n_groups, box_rows;
   const int32_t *tables, *lens, *off, *starts, *prefix;
@@ -101,6 +97,7 @@ struct Piece {
 struct Smem { /* behind the tiles */
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
   uint64_t sfull[2], pready[2][2], oready[2], drain[2];
+  uint64_t turn[2];                           /* of a pair's softmaxes */
   uint64_t q_full[2], q_free[2];              /* Q of a stream's piece */
   uint64_t qfull[2][kQueue], qempty[2][kQueue]; /* the queue's */
   Piece queue[2][kQueue];
@@ -697,6 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_init(&sm->q_full[s], 1);
       bar_init(&sm->q_free[s], 4);
       bar_init(&sm->oready[s], 1);
+      bar_init(&sm->turn[s], 4);
       bar_init(&sm->drain[s], 1);
       for (int i = 0; i < kQueue; ++i) {
         bar_init(&sm->qfull[s][i], 1);
@@ -849,11 +847,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(&sm->q_full[s], q_par, abort);
         if (!ok) break;
         q_par ^= 1;
-        if (line == 0 && s == 1 && n > 4) {
-          const long long since = clock64();
-          while (clock64() - since < kPairLag)
-            ;
-        }
 #pragma unroll 1
         for (int t = 0; t < n; ++t) {
           const int slot = line == 0 ? it % C::STAGES : s * R + ring;
@@ -935,6 +928,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         s_par ^= 1;
         tc_fence_after();
+        if (pair && it + s > 0) {
+          /* The streams of a pair take turns, stream 0's tile before stream 1's: side by
+           * side they would share the exponential unit and then leave it, and the tensor
+           * cores, idle together. */
+          ok = warp_wait(&sm->turn[s], (it - 1 + s) & 1, abort);
+          if (!ok) break;
+        }
         const int slot = pair ? it % C::STAGES : s * R + ring;
         if (k0 + kTile > c.kend) {
           /* zero the V rows behind the last key: what lies there may be NaN */
@@ -961,6 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) {
             bar_arrive(&sm->pready[s][0]);
             bar_arrive(&sm->pready[s][1]);
+            if (pair) bar_arrive(&sm->turn[1 - s]);
           }
           continue;
         }
@@ -1021,7 +1022,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(&sm->pready[s][h - 2]);
+            if (lane == 0) {
+              bar_arrive(&sm->pready[s][h - 2]);
+              if (h == 3 && pair) bar_arrive(&sm->turn[1 - s]);
+            }
           }
           if (h == 2) tmem_st16(at_s + h * 16, w);
         }

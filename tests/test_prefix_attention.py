@@ -267,9 +267,12 @@ def test_scales_and_peaked_scores(scale):
 
 
 @gpu
-def test_rising_scores_move_the_maximum():
-    """Every block of keys beats the last one by far, so the running maximum moves each time."""
-    c = Case([(0, [(1500, 1)]), (256, [(700, 1), (20, 1)])], (4, 2, 64))
+@pytest.mark.parametrize("scale", [None, 1.0, 3.0])
+@pytest.mark.parametrize("each", [1, 40])
+def test_rising_scores_move_the_maximum(scale, each):
+    """Every block of keys beats the last one, up to e^1152 over the row, so the reference of
+    the softmax has to move along; with one row tile and with two."""
+    c = Case([(0, [(1500, each)]), (256, [(700, 1), (20, 1)])], (16, 2, 64), scale=scale)
     t = c.t
     c.q[:] = 1.0
     for b, r in enumerate(c.rows):
