@@ -41,8 +41,8 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88; /* 256 * 208 + 128 * 88 = 384
 constexpr int kTile = 128;         /* keys per tile; rows per row tile */
 /* The line's unit is about 1100 cycles.  A tile takes 3300 of a CTA in a pair (its two
  * products and softmaxes, mostly hidden under one another) and 2300 in a single (64 KB at
- * the SM's share of HBM); an item's beginning and end take 8000 and 4000 on top. */
-constexpr int kPairTile = 3, kSingleTile = 2, kPairItem = 8, kSingleItem = 4;
+ * the SM's share of HBM); an item's beginning and end take 12000 and 4000 on top. */
+constexpr int kPairTile = 3, kSingleTile = 2, kPairItem = 11, kSingleItem = 4;
 constexpr int kShare = 6; /* a CTA's share at least: each of its streams meets a tile of a long item */
 constexpr int kQueue = 4;          /* pieces that a producer is ahead of its stream */
 constexpr int kMaxSeqs = 1024, kMaxGroups = 512; /* of a call: the cut's tables are in shared memory */
@@ -1114,9 +1114,10 @@ __global__ void __launch_bounds__(kThreads, 1)
  * share it) where there are too few for all SMs; its warps take the heads, several a head
  * where there are fewer than eight.  Reads L2: the partials were written just before.
  * What bounds it is its chain of three loads (where, maxima and sums, weighted sums), so
- * 32 pieces' maxima and eight pieces' sums are in flight together. */
-template <int D>
-__global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a, int n_cta, int blocks) {
+ * 32 pieces' maxima and eight pieces' sums are in flight together; where blocks are MANY,
+ * more of them a SM instead. */
+template <int D, bool MANY>
+__global__ void __launch_bounds__(256, MANY ? 7 : 2) attn_merge(const __grid_constant__ Args a, int n_cta, int blocks) {
   __shared__ float sums[8][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int unit = blockIdx.x / blocks, rank = blockIdx.x - unit * blocks, units = a.n_tokens * a.Hkv;
@@ -1137,17 +1138,17 @@ __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a
   int split = 8; /* warps a head */
   while (split > 1 && 8 / split < heads) split >>= 1;
   const int part = warp % split, at_once = 8 / split;
-  const long long dense = (long long)a.n_tokens * a.Hq;
+  const uint32_t dense = (uint32_t)a.n_tokens * a.Hq; /* rows: below 2^32 by the limits of create */
   for (int hg0 = h0; hg0 < h1; hg0 += at_once) {
     const int hg = min(hg0 + warp / split, a.G - 1);
     const bool mine = hg0 + warp / split < h1;
-    const long long orow = (long long)tok * a.Hq + kvh * a.G + hg;
-    auto place = [&](int i) -> long long { /* partial row of piece i */
-      const bool own = i >= n_shared;
-      const int k = own ? i - n_shared : i;
-      if (k == 0) return (own ? dense : 0) + orow;
-      const int4 w = own ? wo : ws;
-      return 2 * dense + (long long)(w.y + k) * w.w + w.z + hg;
+    const uint32_t orow = (uint32_t)tok * a.Hq + kvh * a.G + hg;
+    const uint32_t at_s = 2 * dense + ws.y * ws.w + ws.z + hg;
+    const uint32_t at_o = 2 * dense + wo.y * wo.w + wo.z + hg;
+    auto place = [&](int i) -> uint32_t { /* partial row of piece i */
+      const int k = i - n_shared;
+      if (k < 0) return i ? at_s + i * ws.w : orow;
+      return k ? at_o + k * wo.w : dense + orow;
     };
     constexpr int N = D / 32; /* columns a lane */
     float o[N] = {}, l = 0.0f, M = -INFINITY;
@@ -1158,7 +1159,7 @@ __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a
     if (M != -INFINITY) {
       for (int i0 = 0; i0 < n; i0 += 32) {
         float f = 0.0f;
-        long long row = 0;
+        uint32_t row = 0;
         if (i0 + lane < n) {
           row = place(i0 + lane);
           const float2 ml = a.part_ml[row];
@@ -1166,10 +1167,10 @@ __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a
           l += f * ml.y;
         }
         const int m = min(32, n - i0);
-#pragma unroll 8
+#pragma unroll(MANY ? 2 : 8)
         for (int i = part; i < m; i += split) {
           const float w = __shfl_sync(0xffffffffu, f, i);
-          const float *src = a.part + __shfl_sync(0xffffffffu, row, i) * D + lane * N;
+          const float *src = a.part + (size_t)__shfl_sync(0xffffffffu, row, i) * D + lane * N;
           float v[N];
           if (N == 4)
             *(float4 *)v = *(const float4 *)src;
@@ -1196,7 +1197,7 @@ __global__ void __launch_bounds__(256) attn_merge(const __grid_constant__ Args a
     }
     if (!mine || part) continue;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    __nv_bfloat16 *dst = a.out + orow * D + lane * N;
+    __nv_bfloat16 *dst = a.out + (size_t)orow * D + lane * N;
     if (N == 4) {
       *(uint2 *)dst =
           make_uint2(pack_bf16(o[0] * inv, o[1 % N] * inv), pack_bf16(o[2 % N] * inv, o[3 % N] * inv));
@@ -1274,7 +1275,9 @@ cudaError_t launch(const mk_attn *at, int layer, const CUtensorMap &qmap, const 
   cfg.gridDim = dim3((unsigned)a.n_tokens * a.Hkv * blocks);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, attn_merge<D>, a, at->n_sm, blocks);
+  return a.n_tokens * a.Hkv >= 16 * at->n_sm
+             ? cudaLaunchKernelEx(&cfg, attn_merge<D, true>, a, at->n_sm, blocks)
+             : cudaLaunchKernelEx(&cfg, attn_merge<D, false>, a, at->n_sm, blocks);
 }
 
 }  // namespace
