@@ -42,10 +42,10 @@ extern "C" {
 
 typedef struct {
   int32_t n_pools;            /* K and V pools of every layer: 2 * n_layers (at most 512) */
-  int32_t num_pages;          /* pages in each pool (at most 2^21) */
+  int32_t num_pages;          /* pages in each pool (at most 2^20) */
   int32_t page_size;          /* tokens per page */
   int32_t n_seqs;             /* table rows (at most 65536) */
-  int32_t max_pages_per_seq;  /* entries per row */
+  int32_t max_pages_per_seq;  /* entries per row; n_seqs rows have at most 2^30 */
   int64_t page_bytes;         /* bytes of a page in one pool: n_kv_heads * page_size * head_dim * 2 */
   void *const *pools;         /* HOST array [n_pools] of DEVICE pointers, 16-byte aligned */
   int32_t *page_tables;       /* DEVICE [n_seqs][max_pages_per_seq] */

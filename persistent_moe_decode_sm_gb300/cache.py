@@ -65,7 +65,7 @@ class KvCache:
         if seq_lens.numel() != page_tables.shape[0] or page_refs.numel() != shape[0]:
             raise ValueError("seq_lens has an entry for each table row, page_refs for each page")
         self.handle = None
-        self.device = dev
+        self.device, self._index, self._int32 = dev, page_refs.get_device(), torch.int32
         self.pools, self.page_tables = pools, page_tables
         self.seq_lens, self.page_refs = seq_lens, page_refs
         self.n_seqs, self.max_pages_per_seq = page_tables.shape
@@ -81,11 +81,15 @@ class KvCache:
         self.handle = h.value
 
     def _two(self, a, b, what_a, what_b):
-        _want(a, what_a, "int32", self.device, 1)
-        _want(b, what_b, "int32", self.device, 1)
-        if a.numel() != b.numel():
+        for t, what in ((a, what_a), (b, what_b)):
+            # the quick look first: these calls take a few microseconds
+            if not (getattr(t, "dtype", None) is self._int32 and t.get_device() == self._index
+                    and t.dim() == 1 and t.is_contiguous()):
+                _want(t, what, "int32", self.device, 1)
+        n = a.numel()
+        if n != b.numel():
             raise ValueError(f"{what_a} and {what_b} have different lengths")
-        return self.handle, a.numel(), a.data_ptr(), b.data_ptr()
+        return self.handle, n, a.data_ptr(), b.data_ptr()
 
     def copy_pages(self, src_pages, dst_pages):
         """Copies page src_pages[i] over page dst_pages[i] in every pool."""
@@ -163,6 +167,7 @@ class PrefixAttention:
         self.handle = None
         self.device, self.layers, self.max_tokens = dev, layers, max_tokens
         self.heads, self.head_dim = n_q_heads, head_dim
+        self._index, self._bf16, self._f32 = layers[0][0].get_device(), torch.bfloat16, torch.float32
         self._lib = lib()
         n = len(layers)
         ks = (ctypes.c_void_p * n)(*[k.data_ptr() for k, _ in layers])
@@ -210,14 +215,19 @@ class PrefixAttention:
         lse (fp32 [n_tokens][n_q_heads]) receives the logarithm of the softmax sums.  q may
         have a token stride of its own (the q part of a fused projection)."""
         rows = (batch.n_tokens, self.heads, self.head_dim)
-        if (q.shape != rows or q.dtype != self.layers[0][0].dtype or q.device != self.device
+        if (q.shape != rows or q.dtype is not self._bf16 or q.get_device() != self._index
                 or q.stride(2) != 1 or q.stride(1) != self.head_dim):
             raise ValueError(f"q has to be bfloat16 {rows} with contiguous heads on {self.device}")
-        _want(out, "out", "bfloat16", self.device)
+        # the quick look first: a call takes some tens of microseconds
+        if not (out.dtype is self._bf16 and out.get_device() == self._index
+                and out.is_contiguous()):
+            _want(out, "out", "bfloat16", self.device)
         if out.shape != rows:
             raise ValueError(f"out has to be {rows}")
         if lse is not None:
-            _want(lse, "lse", "float32", self.device)
+            if not (lse.dtype is self._f32 and lse.get_device() == self._index
+                    and lse.is_contiguous()):
+                _want(lse, "lse", "float32", self.device)
             if lse.shape != rows[:2]:
                 raise ValueError(f"lse has to be {rows[:2]}")
         _check(self._lib.mk_prefix_attention(

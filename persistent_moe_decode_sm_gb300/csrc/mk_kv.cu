@@ -1,7 +1,7 @@
 /*
  * mk_kv.cu -- page ownership of the paged KV cache (include/mk_cache.h).
  *
- * Each call is two kernels.  kv_plan, one cluster of 8 CTAs, does the
+ * Each call is two kernels.  kv_plan, one cluster of up to 16 CTAs, does the
  * bookkeeping: it checks the arguments, adds up the holders that pages gain and
  * lose in a copy of the counts, ranks the free pages, and only then -- behind
  * the last point where the call can be refused -- writes tables, lengths and
@@ -21,9 +21,8 @@
 
 namespace {
 
-constexpr int kCluster = 8;
-constexpr int kPlanThreads = 512;
-constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kMaxCluster = 16;
+constexpr int kPlanThreads = 1024; /* at most */
 constexpr int kSeg = 128;          /* table entries of one warp's item: 4 independent loads a lane */
 constexpr int kMoveThreads = 256;
 constexpr int kMoveChunk = 4096;   /* bytes of one warp's copy: 8 16-byte loads in flight a lane */
@@ -41,7 +40,8 @@ struct Ctrl {
 };
 
 struct Params {
-  int32_t num_pages, page_size, n_seqs, max_pages, n;
+  int32_t num_pages, page_size, n_seqs, max_pages, n_pools, n;
+  int64_t page_bytes;
   int32_t *tables, *lens, *refs;
   const int32_t *a, *b;        /* the call's DEVICE arguments */
   int32_t *page_map;           /* compact: caller's, may be NULL */
@@ -51,15 +51,11 @@ struct Params {
   int32_t *new_refs, *claim, *fresh, *copy_src, *copy_dst; /* claim [max(pages, seqs)], else [pages] */
   int32_t *need, *first, *len0, *len1;                     /* [n_seqs] */
   int32_t *stage;                                          /* [n_seqs][max_pages] */
+  char *const *pools;                                      /* [n_pools] */
 };
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ int cluster_rank() {
-  int r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
 }
 __device__ __forceinline__ void dependents_may_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -88,17 +84,17 @@ __device__ int block_scan(int v, int *sums, int *total) {
   if (lane == 31) sums[warp] = x;
   __syncthreads();
   if (warp == 0) {
-    int s = lane < kPlanWarps ? sums[lane] : 0;
+    int s = lane < (int)(blockDim.x >> 5) ? sums[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const int y = __shfl_up_sync(0xffffffffu, s, o);
       if (lane >= o) s += y;
     }
-    if (lane < kPlanWarps) sums[lane] = s;
+    if (lane < (int)(blockDim.x >> 5)) sums[lane] = s;
   }
   __syncthreads();
   const int before = warp ? sums[warp - 1] : 0;
-  *total = sums[kPlanWarps - 1];
+  *total = sums[(blockDim.x >> 5) - 1];
   __syncthreads();
   return before + x - v;
 }
@@ -125,15 +121,14 @@ __device__ __forceinline__ void list_copy(const Params &p, int src, int dst) {
 /* What bounds it: latency.  A plan reads and writes some tens to hundreds of
  * KB; its time is its chain of dependent loads (argument, length, table entry,
  * count) and its 3 to 5 cluster barriers, so every phase spreads its entries
- * over all 128 warps with several loads in flight a lane. */
+ * over all warps with several loads in flight a lane. */
 template <int OP>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
-    kv_plan(const Params p) {
+__global__ void __launch_bounds__(kPlanThreads) kv_plan(const Params p) {
   __shared__ int sums[32];
   __shared__ int my_count, my_holes;
   const int tid = threadIdx.x, lane = tid & 31;
-  const int rank = cluster_rank();
-  const int gtid = rank * kPlanThreads + tid, nthr = kCluster * kPlanThreads;
+  const int rank = blockIdx.x, ctas = gridDim.x, threads = blockDim.x; /* one cluster */
+  const int gtid = rank * threads + tid, nthr = ctas * threads;
   const int gwarp = gtid >> 5, nwarp = nthr >> 5;
   const int P = p.page_size, M = p.max_pages, N = p.num_pages;
 
@@ -171,12 +166,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         refuse(p, MK_ERR_INVALID_ARG);
     }
   }
-  const int nseg = (M + kSeg - 1) / kSeg;
-  const long long items =
-      OP == OP_COMPACT ? (long long)p.n_seqs * nseg : (long long)p.n * nseg;
+  const unsigned nseg = (M + kSeg - 1) / kSeg;
+  const unsigned items = (unsigned)(OP == OP_COMPACT ? p.n_seqs : p.n) * nseg; /* below 2^31: see create */
   if (OP == OP_FORK || OP == OP_RESIZE) {
-    for (long long it = gwarp; it < items; it += nwarp) {
-      const int i = (int)(it / nseg), seg = (int)(it - (long long)i * nseg);
+    for (unsigned it = gwarp; it < items; it += nwarp) {
+      const int i = (int)(it / nseg), seg = (int)(it - (unsigned)i * nseg);
       const int s = p.a[i], d = OP == OP_FORK ? p.b[i] : s;
       if ((unsigned)s >= (unsigned)p.n_seqs || (unsigned)d >= (unsigned)p.n_seqs) {
         if (lane == 0) refuse(p, MK_ERR_INVALID_ARG);
@@ -245,11 +239,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     }
   }
   int holes = 0, live = 0; /* of this CTA's range of pages */
-  const int per = (N + kCluster - 1) / kCluster;
+  const int per = (N + ctas - 1) / ctas;
   const int lo = min(N, rank * per), hi = min(N, lo + per);
   if (OP == OP_COMPACT) {
-    for (long long it = gwarp; it < items; it += nwarp) {
-      const int s = (int)(it / nseg), seg = (int)(it - (long long)s * nseg);
+    for (unsigned it = gwarp; it < items; it += nwarp) {
+      const int s = (int)(it / nseg), seg = (int)(it - (unsigned)s * nseg);
       const int ls = p.lens[s];
       if (ls < 0 || ls > (long long)M * P) {
         if (lane == 0) refuse(p, MK_ERR_PAGE_OOB);
@@ -262,7 +256,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
         if (j < us) held_page(p, p.tables[(size_t)s * M + j]);
       }
     }
-    for (int i = lo + tid; i < hi; i += kPlanThreads) {
+    for (int i = lo + tid; i < hi; i += threads) {
       const int v = p.refs[i];
       live += v > 0;
       if (v < 0) refuse(p, MK_ERR_INVALID_ARG);
@@ -287,9 +281,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
      * may refuse while this phase runs. */
     const bool sound = __syncthreads_or(__ldcg(&p.ctrl->call_err) != 0) == 0;
     if (sound) {
-      for (int i0 = 0; i0 < p.n; i0 += kPlanThreads) {
+      for (int i0 = 0; i0 < p.n; i0 += threads) {
         const int i = i0 + tid;
-        const int v = i < p.n ? min(__ldcg(p.need + i), N + 1) : 0; /* 512 * 2^21: no overflow */
+        const int v = i < p.n ? min(__ldcg(p.need + i), N + 1) : 0; /* 1024 * 2^20: no overflow */
         int total;
         const int at = block_scan(v, sums, &total);
         if (rank == 0 && i < p.n) p.first[i] = wanted + at;
@@ -297,7 +291,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
       }
     }
     int count = 0;
-    for (int i = lo + tid; i < hi; i += kPlanThreads) {
+    for (int i = lo + tid; i < hi; i += threads) {
       const int v = __ldcg(p.new_refs + i);
       count += v == 0;
       if (v < 0 || (v & ~kSource) > kMaxRefs) refuse(p, MK_ERR_INVALID_ARG);
@@ -308,13 +302,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   }
   if (OP == OP_COMPACT) {
     int before = 0;
-    for (int r = 0; r < kCluster; ++r) {
+    for (int r = 0; r < ctas; ++r) {
       const int c = peer_load(&my_count, r);
       if (r < rank) before += c;
       n_live += c;
     }
     int base = before;
-    for (int i0 = lo; i0 < hi; i0 += kPlanThreads) {
+    for (int i0 = lo; i0 < hi; i0 += threads) {
       const int i = i0 + tid;
       const int v = i < hi && p.refs[i] > 0;
       int total;
@@ -339,7 +333,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   int err = __ldcg(&p.ctrl->call_err);
   int before = 0, n_free = 0;
   if ((OP == OP_FORK || OP == OP_RESIZE) && err == 0) {
-    for (int r = 0; r < kCluster; ++r) {
+    for (int r = 0; r < ctas; ++r) {
       const int c = peer_load(&my_count, r);
       if (r < rank) before += c;
       n_free += c;
@@ -348,8 +342,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   }
   int n_moves = 0;
   if (OP == OP_COMPACT)
-    for (int r = 0; r < kCluster; ++r) n_moves += peer_load(&my_holes, r);
-  cluster_sync(); /* the peers' counts are read: their CTAs may end */
+    for (int r = 0; r < ctas; ++r) n_moves += peer_load(&my_holes, r);
   if (err != 0) {
     if (gtid == 0) {
       p.ctrl->status = err;
@@ -357,6 +350,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
       *(volatile int32_t *)p.err_host = err;
       __threadfence_system();
     }
+    cluster_sync(); /* no CTA ends while a peer may read its counts */
     return;
   }
 
@@ -376,7 +370,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
       if (p.page_map) p.page_map[src] = dst;
     }
     if (p.page_map)
-      for (int i = lo + tid; i < hi; i += kPlanThreads) {
+      for (int i = lo + tid; i < hi; i += threads) {
         const int v = __ldcg(p.claim + i);
         if (i < n_live || v == -1) p.page_map[i] = v; /* a mover's entry is written above */
       }
@@ -384,10 +378,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
       p.ctrl->n_copy = n_moves;
       p.ctrl->remap = 1 + stay; /* kv_move's list starts there */
     }
+    cluster_sync(); /* no CTA ends while a peer may read its counts */
   }
   if (OP == OP_FORK || OP == OP_RESIZE) {
     if (wanted > 0 && before < wanted) {
-      for (int i0 = lo; i0 < hi && before < wanted; i0 += kPlanThreads) {
+      for (int i0 = lo; i0 < hi && before < wanted; i0 += threads) {
         const int i = i0 + tid;
         const int v = i < hi && __ldcg(p.new_refs + i) == 0;
         int total;
@@ -401,8 +396,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
     }
     cluster_sync();
     for (int i = gtid; i < N; i += nthr) p.refs[i] = __ldcg(p.new_refs + i) & ~kSource;
-    for (long long it = gwarp; it < items; it += nwarp) {
-      const int i = (int)(it / nseg), seg = (int)(it - (long long)i * nseg);
+    for (unsigned it = gwarp; it < items; it += nwarp) {
+      const int i = (int)(it / nseg), seg = (int)(it - (unsigned)i * nseg);
       const int s = p.a[i], d = OP == OP_FORK ? p.b[i] : s;
       const int l0 = __ldcg(p.len0 + i), l1 = __ldcg(p.len1 + i);
       const int u0 = l0 / P + (l0 % P != 0), u1 = l1 / P + (l1 % P != 0);
@@ -442,33 +437,30 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads)
   }
 }
 
-struct Pools {
-  char *at[kMaxPools];
-};
-
-/* Copies the listed pages in every pool: reads and writes of HBM, nothing else.
- * One warp copies 4 KB at a time with all of its 16-byte loads in flight before
- * the first store. */
-__global__ void __launch_bounds__(kMoveThreads, 4)
-    kv_move(const __grid_constant__ Pools pools, const __grid_constant__ Params p, int n_pools,
-            long long page_bytes) {
-  wait_for_previous();
-  dependents_may_launch();
+/* Copies pages src[i] over dst[i] in every pool: reads and writes of HBM, nothing else.
+ * One warp copies 4 KB at a time with all of its 16-byte loads in flight before the first
+ * store. */
+__device__ __forceinline__ void move_pages(const Params &p, unsigned n, const int32_t *src,
+                                           const int32_t *dst) {
+  const long long page_bytes = p.page_bytes;
   const int lane = threadIdx.x & 31;
   const unsigned warp = (blockIdx.x * kMoveThreads + threadIdx.x) >> 5;
   const unsigned nwarp = gridDim.x * (kMoveThreads / 32);
-  const int remap = __ldcg(&p.ctrl->remap);
-  const unsigned n = __ldcg(&p.ctrl->n_copy), base = remap > 0 ? remap - 1 : 0;
   const unsigned per_page = (unsigned)((page_bytes + kMoveChunk - 1) / kMoveChunk);
-  const unsigned per_copy = per_page * n_pools;
-  const unsigned long long total = (unsigned long long)n * per_copy;
-  for (unsigned long long u = warp; u < total; u += nwarp) {
-    const unsigned c = (unsigned)(u / per_copy), r = (unsigned)(u - (unsigned long long)c * per_copy);
+  const unsigned per_copy = per_page * p.n_pools;
+  unsigned c = warp / per_copy, r = warp - c * per_copy; /* this warp's copy, its chunk among all pools' */
+  while (c < n) {
     const unsigned pool = r / per_page, chunk = r - pool * per_page;
-    const long long src = __ldcg(p.copy_src + base + c), dst = __ldcg(p.copy_dst + base + c);
+    const long long s = __ldcg(src + c), d = __ldcg(dst + c);
+    r += nwarp;
+    const unsigned q = r / per_copy;
+    c += q;
+    r -= q * per_copy;
+    if (s == d) continue;
     const long long off = (long long)chunk * kMoveChunk + lane * 16;
-    const char *from = pools.at[pool] + src * page_bytes + off;
-    char *to = pools.at[pool] + dst * page_bytes + off;
+    char *base = p.pools[pool];
+    const char *from = base + s * page_bytes + off;
+    char *to = base + d * page_bytes + off;
     const long long left = page_bytes - off;
     uint4 v[kMoveChunk / 512];
 #pragma unroll
@@ -478,12 +470,23 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
     for (int k = 0; k < kMoveChunk / 512; ++k)
       if (k * 512 < left) __stcs((uint4 *)(to + k * 512), v[k]);
   }
+}
+
+/* The plan's copies, and the tables through its map of pages. */
+__global__ void __launch_bounds__(kMoveThreads, 4)
+    kv_move(const __grid_constant__ Params p) {
+  wait_for_previous();
+  dependents_may_launch();
+  const int remap = __ldcg(&p.ctrl->remap), base = remap > 0 ? remap - 1 : 0;
+  move_pages(p, __ldcg(&p.ctrl->n_copy), p.copy_src + base, p.copy_dst + base);
   if (remap > 0) {
-    const unsigned nseg = (p.max_pages + 31) / 32;
-    const unsigned long long items = (unsigned long long)p.n_seqs * nseg;
-    for (unsigned long long it = warp; it < items; it += nwarp) {
-      const unsigned s = (unsigned)(it / nseg);
-      const long long j = (long long)(it - (unsigned long long)s * nseg) * 32 + lane;
+    const int lane = threadIdx.x & 31;
+    const unsigned warp = (blockIdx.x * kMoveThreads + threadIdx.x) >> 5;
+    const unsigned nwarp = gridDim.x * (kMoveThreads / 32);
+    const unsigned nseg = (p.max_pages + 31) / 32, items = p.n_seqs * nseg;
+    for (unsigned it = warp; it < items; it += nwarp) {
+      const unsigned s = it / nseg;
+      const long long j = (long long)(it - s * nseg) * 32 + lane;
       const int l = p.lens[s];
       if (j < l / p.page_size + (l % p.page_size != 0)) {
         int32_t *at = p.tables + (size_t)s * p.max_pages + j;
@@ -491,6 +494,46 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
       }
     }
   }
+}
+
+/* mk_kv_copy_pages for up to kFewPairs pairs and 32 KB of page bits, in one kernel: every
+ * block checks all pairs against its own bits, so that none waits for another. */
+constexpr int kFewPairs = 4096, kFewPages = 1 << 18;
+__global__ void __launch_bounds__(kMoveThreads, 4)
+    kv_copy_few(const __grid_constant__ Params p) {
+  extern __shared__ unsigned target[];
+  const int tid = threadIdx.x;
+  const unsigned N = p.num_pages;
+  for (unsigned i = tid; i < (N + 31) / 32; i += kMoveThreads) target[i] = 0;
+  wait_for_previous();
+  dependents_may_launch();
+  const int held_up = __ldcg(&p.ctrl->status); /* by an earlier refusal, or another block's of this call */
+  __syncthreads();
+  bool outside = false, twice = false;
+  for (int i = tid; i < p.n; i += kMoveThreads) {
+    const unsigned s = p.a[i], d = p.b[i];
+    if (s >= N || d >= N)
+      outside = true;
+    else if (s != d)
+      twice |= (atomicOr(target + d / 32, 1u << d % 32) >> d % 32) & 1;
+  }
+  outside = __syncthreads_or(outside);
+  for (int i = tid; i < p.n; i += kMoveThreads) {
+    const unsigned s = p.a[i];
+    twice |= s < N && s != (unsigned)p.b[i] && (target[s / 32] >> s % 32 & 1);
+  }
+  twice = __syncthreads_or(twice);
+  if (held_up) return;
+  if (outside || twice) {
+    if (blockIdx.x == 0 && tid == 0) {
+      const int err = outside ? MK_ERR_PAGE_OOB : MK_ERR_INVALID_ARG;
+      p.ctrl->status = err;
+      *(volatile int32_t *)p.err_host = err;
+      __threadfence_system();
+    }
+    return;
+  }
+  move_pages(p, p.n, p.a, p.b);
 }
 
 /* Makes `dev` current for a scope: a handle may be called with another device
@@ -514,10 +557,9 @@ struct OnDevice {
 
 struct mk_kv {
   mk_kv_desc d{};
-  Pools pools{};
   Params base{};
   cudaStream_t stream = nullptr;
-  int dev = 0, n_sm = 0;
+  int dev = 0, n_sm = 0, max_cluster = kMaxCluster;
   uint8_t *ws = nullptr;
   int32_t *err_host = nullptr;
 };
@@ -525,25 +567,53 @@ struct mk_kv {
 namespace {
 
 template <int OP>
-cudaError_t launch_plan(const Params &p, cudaStream_t st) {
+cudaError_t launch_plan(const mk_kv *kv, const Params &p) {
+  /* 8 CTAs of 512 threads, measured against one CTA (12 us for a small fork, one CTA 15) and
+   * against the largest cluster of 1024 threads, which takes the calls with more table
+   * entries than 512 warps hold 128 of (64 forks of 16384 tokens: 45 us, with it 29). */
+  const long long segs = (p.max_pages + kSeg - 1) / kSeg * (long long)(OP == OP_COMPACT ? p.n_seqs : p.n);
+  const bool large = segs > 256 || p.num_pages > 65536;
+  const int ctas = large ? kv->max_cluster : std::min(8, kv->max_cluster);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(kCluster);
-  cfg.blockDim = dim3(kPlanThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(large ? kPlanThreads : kPlanThreads / 2);
+  cfg.stream = kv->stream;
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {(unsigned)ctas, 1, 1};
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kv_plan<OP>, p);
 }
 
-/* max_copies bounds the pages kv_move can find listed. */
+/* The largest cluster of kv_plan that this device takes. */
 template <int OP>
-mk_status submit(mk_kv *kv, const Params &p, long long max_copies, long long extra_warps) {
-  OnDevice on(kv->dev);
-  if (!on.ok) return MK_ERR_CUDA;
-  if (launch_plan<OP>(p, kv->stream) != cudaSuccess) return MK_ERR_CUDA;
+cudaError_t allow_clusters(int *largest) {
+  cudaError_t e = cudaFuncSetAttribute(kv_plan<OP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.blockDim = dim3(kPlanThreads);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  for (; *largest > 1; *largest /= 2) {
+    int n = 0;
+    cfg.gridDim = dim3(*largest);
+    at[0].val.clusterDim = {(unsigned)*largest, 1, 1};
+    if (cudaOccupancyMaxActiveClusters(&n, kv_plan<OP>, &cfg) == cudaSuccess && n > 0) break;
+    cudaGetLastError(); /* a size too large is no error of the caller's */
+  }
+  return cudaSuccess;
+}
+
+typedef void (*MoveKernel)(Params);
+
+/* max_copies bounds the pages that are copied. */
+mk_status launch_move(mk_kv *kv, MoveKernel k, const Params &p, long long max_copies,
+                      long long extra_warps, size_t smem) {
   const long long per_copy =
       (kv->d.page_bytes + kMoveChunk - 1) / kMoveChunk * (long long)kv->d.n_pools;
   const long long warps = std::max(max_copies * per_copy, extra_warps);
@@ -551,16 +621,24 @@ mk_status submit(mk_kv *kv, const Params &p, long long max_copies, long long ext
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)std::max(1LL, std::min(want, (long long)kv->n_sm * 4)));
   cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = kv->stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv_move, kv->pools, p, (int)kv->d.n_pools,
-                         (long long)kv->d.page_bytes) != cudaSuccess)
-    return MK_ERR_CUDA;
-  return MK_OK;
+  return cudaLaunchKernelEx(&cfg, k, p) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}
+
+template <int OP>
+mk_status submit(mk_kv *kv, const Params &p, long long max_copies, long long extra_warps) {
+  OnDevice on(kv->dev);
+  if (!on.ok) return MK_ERR_CUDA;
+  if (OP == OP_COPY && p.n <= kFewPairs && p.num_pages <= kFewPages)
+    return launch_move(kv, kv_copy_few, p, max_copies, 0, ((size_t)p.num_pages + 31) / 32 * 4);
+  if (launch_plan<OP>(kv, p) != cudaSuccess) return MK_ERR_CUDA;
+  return launch_move(kv, kv_move, p, max_copies, extra_warps, 0);
 }
 
 bool aligned4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
@@ -574,9 +652,10 @@ mk_status mk_kv_create(const mk_kv_desc *d, void *stream, mk_kv **out) {
   if (d->n_pools < 1 || d->num_pages < 1 || d->page_size < 1 || d->n_seqs < 1 ||
       d->max_pages_per_seq < 1 || d->page_bytes < 16 || d->page_bytes % 16)
     return MK_ERR_INVALID_ARG;
-  if (d->n_pools > kMaxPools || d->num_pages > (1 << 21) || d->n_seqs > 65536 ||
+  if (d->n_pools > kMaxPools || d->num_pages > (1 << 20) || d->n_seqs > 65536 ||
       (int64_t)d->max_pages_per_seq * d->page_size > INT32_MAX ||
-      d->page_bytes > ((int64_t)1 << 32))
+      d->page_bytes > ((int64_t)1 << 32) ||
+      (int64_t)d->n_seqs * d->max_pages_per_seq > (int64_t)1 << 30)
     return MK_ERR_UNSUPPORTED;
   if (!d->pools || !d->page_tables || !d->seq_lens || !d->page_refs || !aligned4(d->page_tables) ||
       !aligned4(d->seq_lens) || !aligned4(d->page_refs))
@@ -592,7 +671,6 @@ mk_status mk_kv_create(const mk_kv_desc *d, void *stream, mk_kv **out) {
   mk_kv *kv = new (std::nothrow) mk_kv();
   if (!kv) return MK_ERR_CUDA;
   kv->d = *d;
-  std::memcpy(kv->pools.at, d->pools, sizeof(void *) * d->n_pools);
   kv->d.pools = nullptr;
   kv->stream = (cudaStream_t)stream;
   kv->dev = dev;
@@ -606,9 +684,16 @@ mk_status mk_kv_create(const mk_kv_desc *d, void *stream, mk_kv **out) {
   };
   const size_t o_ctrl = take(sizeof(Ctrl) / 4), o_refs = take(N), o_claim = take(std::max(N, S)),
                o_fresh = take(N), o_src = take(N), o_dst = take(N), o_need = take(S),
-               o_first = take(S), o_len0 = take(S), o_len1 = take(S), o_stage = take(S * M);
-  cudaError_t e = cudaMalloc(&kv->ws, off);
+               o_first = take(S), o_len0 = take(S), o_len1 = take(S), o_stage = take(S * M), o_pools = take(2 * (size_t)d->n_pools);
+  cudaError_t e = allow_clusters<OP_COPY>(&kv->max_cluster);
+  if (e == cudaSuccess) e = allow_clusters<OP_FORK>(&kv->max_cluster);
+  if (e == cudaSuccess) e = allow_clusters<OP_RESIZE>(&kv->max_cluster);
+  if (e == cudaSuccess) e = allow_clusters<OP_COMPACT>(&kv->max_cluster);
+  if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
   if (e == cudaSuccess) e = cudaMemsetAsync(kv->ws, 0, off, kv->stream);
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(kv->ws + o_pools, d->pools, sizeof(void *) * d->n_pools,
+                        cudaMemcpyHostToDevice, kv->stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize(kv->stream);
   if (e == cudaSuccess) e = cudaHostAlloc(&kv->err_host, 64, cudaHostAllocMapped);
   Params &p = kv->base;
@@ -624,6 +709,9 @@ mk_status mk_kv_create(const mk_kv_desc *d, void *stream, mk_kv **out) {
   p.page_size = d->page_size;
   p.n_seqs = d->n_seqs;
   p.max_pages = d->max_pages_per_seq;
+  p.n_pools = d->n_pools;
+  p.page_bytes = d->page_bytes;
+  p.pools = (char *const *)(kv->ws + o_pools);
   p.tables = d->page_tables;
   p.lens = d->seq_lens;
   p.refs = d->page_refs;
