@@ -72,6 +72,14 @@ __device__ __forceinline__ int peer_load(const int *mine, int rank) {
   return v;
 }
 
+/* Sum of the CTAs' variable, and *before: of those with a lower rank.  By whole warps. */
+__device__ __forceinline__ int peer_sum(const int *mine, int rank, int ctas, int *before) {
+  const int lane = threadIdx.x & 31;
+  const int v = lane < ctas ? peer_load(mine, lane) : 0;
+  *before = __reduce_add_sync(0xffffffffu, lane < rank ? v : 0);
+  return __reduce_add_sync(0xffffffffu, v);
+}
+
 /* Exclusive prefix sum over the block; *total is the block's sum. */
 __device__ int block_scan(int v, int *sums, int *total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -134,13 +142,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan(const Params p) {
 
   wait_for_previous();
   dependents_may_launch();
-  if (__ldcg(&p.ctrl->status) != 0) { /* the same for every thread: written at a call's end only */
-    if (gtid == 0) {
-      p.ctrl->n_copy = 0;
-      p.ctrl->remap = 0;
-    }
-    return;
-  }
+  const int held_up = __ldcg(&p.ctrl->status); /* looked at behind the first barrier */
 
   /* ---- 0: clear what the call counts in */
   if (OP == OP_FORK || OP == OP_RESIZE) {
@@ -155,6 +157,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan(const Params p) {
     p.ctrl->remap = 0;
   }
   cluster_sync();
+  if (held_up) return; /* the same for every thread: written at a call's end only */
 
   /* ---- 1: check the arguments and add up */
   if (OP == OP_COPY) {
@@ -277,13 +280,17 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan(const Params p) {
     }
   }
   if (OP == OP_FORK || OP == OP_RESIZE) {
+    /* the first turn's loads are under way together */
+    const int need0 = tid < p.n ? __ldcg(p.need + tid) : 0;
+    const int refs0 = lo + tid < hi ? __ldcg(p.new_refs + lo + tid) : 1;
     /* need[] is complete unless phase 1 refused.  One answer for the block: others
      * may refuse while this phase runs. */
     const bool sound = __syncthreads_or(__ldcg(&p.ctrl->call_err) != 0) == 0;
     if (sound) {
       for (int i0 = 0; i0 < p.n; i0 += threads) {
         const int i = i0 + tid;
-        const int v = i < p.n ? min(__ldcg(p.need + i), N + 1) : 0; /* 1024 * 2^20: no overflow */
+        const int raw = i0 == 0 ? need0 : i < p.n ? __ldcg(p.need + i) : 0;
+        const int v = min(raw, N + 1); /* 1024 * 2^20: no overflow */
         int total;
         const int at = block_scan(v, sums, &total);
         if (rank == 0 && i < p.n) p.first[i] = wanted + at;
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan(const Params p) {
     }
     int count = 0;
     for (int i = lo + tid; i < hi; i += threads) {
-      const int v = __ldcg(p.new_refs + i);
+      const int v = i == lo + tid ? refs0 : __ldcg(p.new_refs + i);
       count += v == 0;
       if (v < 0 || (v & ~kSource) > kMaxRefs) refuse(p, MK_ERR_INVALID_ARG);
     }
@@ -301,13 +308,8 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan(const Params p) {
     if (tid == 0) my_count = total;
   }
   if (OP == OP_COMPACT) {
-    int before = 0;
-    for (int r = 0; r < ctas; ++r) {
-      const int c = peer_load(&my_count, r);
-      if (r < rank) before += c;
-      n_live += c;
-    }
-    int base = before;
+    int base; /* live pages in the ranges before */
+    n_live = peer_sum(&my_count, rank, ctas, &base);
     for (int i0 = lo; i0 < hi; i0 += threads) {
       const int i = i0 + tid;
       const int v = i < hi && p.refs[i] > 0;
@@ -332,17 +334,15 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan(const Params p) {
   /* ---- 3: the last point where the call can be refused */
   int err = __ldcg(&p.ctrl->call_err);
   int before = 0, n_free = 0;
-  if ((OP == OP_FORK || OP == OP_RESIZE) && err == 0) {
-    for (int r = 0; r < ctas; ++r) {
-      const int c = peer_load(&my_count, r);
-      if (r < rank) before += c;
-      n_free += c;
-    }
-    if (wanted > n_free) err = MK_ERR_NO_PAGES;
-  }
   int n_moves = 0;
-  if (OP == OP_COMPACT)
-    for (int r = 0; r < ctas; ++r) n_moves += peer_load(&my_holes, r);
+  if (OP == OP_FORK || OP == OP_RESIZE) {
+    n_free = peer_sum(&my_count, rank, ctas, &before);
+    if (err == 0 && wanted > n_free) err = MK_ERR_NO_PAGES;
+  }
+  if (OP == OP_COMPACT) {
+    int holes_before;
+    n_moves = peer_sum(&my_holes, rank, ctas, &holes_before);
+  }
   if (err != 0) {
     if (gtid == 0) {
       p.ctrl->status = err;
