@@ -208,14 +208,18 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan(const Params p) {
 #pragma unroll
         for (int k = 0; k < kSeg / 32; ++k) {
           const int j = seg * kSeg + k * 32 + lane;
-          if (j < us && (v[k] = held_page(p, v[k])) >= 0) {
-            p.stage[(size_t)i * M + j] = v[k];
+          if (j < us) v[k] = held_page(p, v[k]);
+          if (j < ud) w[k] = held_page(p, w[k]);
+          if (j < us && v[k] >= 0) p.stage[(size_t)i * M + j] = v[k];
+          /* a beam that follows one of its own family keeps most of its pages */
+          if (j < full && v[k] == w[k]) continue;
+          if (j < us && v[k] >= 0) {
             if (j < full)
               atomicAdd(p.new_refs + v[k], 1);
             else
               atomicOr(p.new_refs + v[k], kSource);
           }
-          if (j < ud && (w[k] = held_page(p, w[k])) >= 0) atomicAdd(p.new_refs + w[k], -1);
+          if (j < ud && w[k] >= 0) atomicAdd(p.new_refs + w[k], -1);
         }
       } else {
         const int last = us - 1;
