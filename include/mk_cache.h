@@ -152,7 +152,9 @@ void mk_attn_destroy(mk_attn *attn);
  * prefix, as far as the shortest of them fills them.  Their rows have to name
  * the same pages there.  Softmax in fp32;
  * the probabilities are rounded to bf16 for the product with V, and so is the
- * result.  The same call gives the same bits.
+ * result.  The same call gives the same bits.  A call whose query tokens times
+ * table width are beyond what 32 bits of work items hold (2^20 tokens over
+ * millions of keys) is MK_ERR_UNSUPPORTED.
  *
  * A wrong DEVICE argument (offsets, lengths or starts that are out of order or
  * out of range: nothing is written; a page id out of range: that page's keys

@@ -29,6 +29,7 @@
 #include <cstdint>
 #include <cstring>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "mk_cache.h"
@@ -47,9 +48,9 @@ constexpr int kShare = 6; /* a CTA's share at least: each of its streams meets a
 constexpr int kQueue = 4;          /* pieces that a producer is ahead of its stream */
 constexpr int kMaxSeqs = 1024, kMaxGroups = 512; /* of a call: the cut's tables are in shared memory */
 constexpr uint64_t kWaitLimit = 2000000000ull; /* ns */
-/* The running maximum moves only when a score exceeds it by this much (in powers
- * of two): P then stays below 2^8, exact in its relative precision, and the
- * accumulator is rescaled a few times per row rather than in most tiles. */
+/* The reference that a row's P are taken against moves only when a score exceeds it by
+ * this much (in powers of two): P then stays below 2^8, its relative precision in bf16
+ * is the same, and the accumulator is rescaled a few times a row instead of in most tiles. */
 constexpr float kSlack = 8.0f;
 struct Args {
   int32_t Hq, Hkv, G, P, num_pages, max_pages, n_seqs, n_tokens, n_groups, box_rows;
@@ -57,6 +58,7 @@ struct Args {
   __nv_bfloat16 *out;
   float *lse;
   float scale_log2; /* scale * log2(e) */
+  int32_t few;      /* the call has few results: see keeps_rest */
   int32_t TB;       /* query tokens of a row tile: 128 / G */
   uint32_t inv_g;   /* ceil(2^16 / G): r * inv_g >> 16 is r / G for r < 128 */
   unsigned long long inv_p; /* ceil(2^38 / P): k * inv_p >> 38 is k / P for k < 2^30 */
@@ -515,6 +517,16 @@ __device__ bool take_cut(const Args &a, Smem *sm) {
   return true;
 }
 
+/* P is rounded to bf16 for the product with V, which moves a result by about as much as
+ * its own rounding does.  The smallest calls (up to 4096 results, rows of a piece in one
+ * warp) keep the rest of the rounding as well, for a product of its own, and P is good to
+ * 2^-17: they are bound by latency (16 rows over 480 shared keys: 15.1 us, with it 15.8)
+ * and their few results have no others to average with.  For all pieces of up to 32 rows it
+ * would cost 64 samples of one prompt a fifth (40 us, with it 48). */
+__device__ __forceinline__ bool keeps_rest(const Args &a, const Piece &p) {
+  return a.few && p.line == 1 && p.ntok * a.G <= 32;
+}
+
 /* The piece at place x of the pairs (line 0) or the singles (1), x < end; x moves
  * behind it.  A share that ends within an item's fixed cost has no tile of it: n is
  * 0.  By a whole warp. */
@@ -600,7 +612,8 @@ __device__ __forceinline__ void tell_merge(const Args &a, const Smem *sm, const 
 
 /* ---- the tiles ---------------------------------------------------------------- */
 
-/* S = Q K^T of a tile; half h of O (+)= P V: P's keys 64 h .. 64 h + 63. */
+/* S = Q K^T of a tile; half h of O (+)= P V: P's keys 64 h .. 64 h + 63, and the rest
+ * of their rounding 64 columns further on. */
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t s, uint64_t q, uint64_t k, uint32_t lead) {
   using C = Cfg<D>;
@@ -612,7 +625,7 @@ __device__ __forceinline__ void issue_qk(uint32_t s, uint64_t q, uint64_t k, uin
 }
 template <int D>
 __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, int h, bool acc,
-                                         uint32_t lead) {
+                                         bool rest, uint32_t lead) {
   using C = Cfg<D>;
   p += h * (kTile / 4);
   v += h * ((kTile / 2 * C::ROWB) >> 4);
@@ -620,6 +633,11 @@ __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, int
   for (int c = 0; c < kTile / 32; ++c)
     mma_ts(o, p + c * 8, v + ((c * 16 * C::ROWB) >> 4), inst_desc(D, true), acc || h > 0 || c > 0,
            lead);
+  if (rest) {
+#pragma unroll
+    for (int c = 0; c < kTile / 32; ++c)
+      mma_ts(o, p + kTile / 2 + c * 8, v + ((c * 16 * C::ROWB) >> 4), inst_desc(D, true), 1, lead);
+  }
 }
 
 /* Loads tile t of a piece, as far as its keys go: a box per page (or part of one) and
@@ -667,6 +685,15 @@ struct Loader {
   }
 };
 
+/* o_r = sum_j p_rj v_j, l_r = sum_j p_rj, p_rj = 2^(c q_r.k_j - m_r) over a piece's tiles of
+ * 128 keys.  Of one tile the tensor cores have 512 cycles for S = Q K^T and 512 for O += P V,
+ * a row tile's 4 warps 550 for the exponentials and 1800 in all, and 64 KB of K and V take
+ * an SM 2800 at its share of HBM.  So singles are bound by HBM where the cache is not in L2
+ * (16 sequences in two groups over 131072 and 32768 shared keys, 352 MB: 63 of 77 us in this
+ * kernel, 5.6 TB/s), pairs by the chain S, P, O of a stream, of which the other stream hides
+ * a part (4800 tokens of 32 heads over 32768 keys: 1.95 ms, 1.33 PFLOP/s, tensor cores 65 %
+ * active), and small calls by their first instructions: the cut, 2.6 us, the first tile 6 us
+ * after the start. */
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -836,6 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(&sm->qfull[s][qslot], (got / kQueue) & 1, abort);
         if (!ok) break;
         const int n = sm->queue[s][qslot].n, line = sm->queue[s][qslot].line;
+        const bool rest = keeps_rest(a, sm->queue[s][qslot]);
         __syncwarp();
         if (lane == 0) bar_arrive(&sm->qempty[s][qslot]);
         if (n == 0) break;
@@ -863,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; ok && h < 2; ++h) {
             ok = warp_wait(&sm->pready[s][h], p_par, abort);
             tc_fence_after();
-            if (ok) issue_pv<D>(at_o, at_s, v0 + o, h, t > 0, lead);
+            if (ok) issue_pv<D>(at_o, at_s, v0 + o, h, t > 0, rest, lead);
           }
           if (!ok) break;
           p_par ^= 1;
@@ -921,6 +949,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int limit = min(c.kend, sm->len[b] - (sm->off[b + 1] - tok) + 1);
       const int warp_limit = __reduce_min_sync(0xffffffffu, limit);
       float m = -INFINITY, l = 0.0f; /* m in score units */
+      auto tiles = [&](auto keeps_rest) {
+        constexpr bool REST = decltype(keeps_rest)::value;
 #pragma unroll 1
       for (int t = 0; t < c.n; ++t) {
         const int k0 = c.key0 + (c.t0 + t) * kTile;
@@ -1007,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, 1)
          * store lands while the next is computed. */
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
-          uint32_t w[16];
+          uint32_t w[16], rest[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             float2 e = fma2(make_float2(x[h * 32 + 2 * k], x[h * 32 + 2 * k + 1]),
@@ -1016,8 +1046,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             e.y = exp2_approx(e.y);
             sum[k & 1] = add2(sum[k & 1], e);
             w[k] = pack_bf16(e.x, e.y);
+            if (REST)
+              rest[k] = pack_bf16(e.x - __uint_as_float(w[k] << 16),
+                                           e.y - __uint_as_float(w[k] & 0xffff0000u));
           }
-          if (h != 2) tmem_st16(at_s + h * 16, w);
+          if (h != 2) {
+            tmem_st16(at_s + h * 16, w);
+            if (REST) tmem_st16(at_s + kTile / 2 + h * 16, rest);
+          }
           if (h >= 2) {
             tmem_wait_st();
             tc_fence_before();
@@ -1027,10 +1063,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (h == 3 && pair) bar_arrive(&sm->turn[1 - s]);
             }
           }
-          if (h == 2) tmem_st16(at_s + h * 16, w);
+          if (h == 2) {
+            tmem_st16(at_s + h * 16, w);
+            if (REST) tmem_st16(at_s + kTile / 2 + h * 16, rest);
+          }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
+      };
+      if (keeps_rest(a, c))
+        tiles(std::true_type{});
+      else
+        tiles(std::false_type{});
       if (!ok) break;
       ok = warp_wait(&sm->oready[s], o_par, abort);
       if (!ok) break;
@@ -1051,7 +1095,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int RL = W / 4, RI = 32 / RL;     /* lanes of a row, rows at a time */
         const int ch = ln % RL, mine = min(32, crows - w0); /* rows of this warp */
         float *to = a.part + (c.t0 ? extra : c.own * dense + row0) * D + ch * 4;
-        const float f = !whole ? 1.0f : l > 0.0f ? 1.0f / l : 0.0f;
+        const float f = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l; /* NaN stays NaN */
 #pragma unroll 1
         for (int i0 = 0; i0 < D; i0 += W) {
           float o[W];
@@ -1083,10 +1127,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const long long orow = row0 + (long long)rt * a.Hq + (r - rt * a.G);
         if (valid && whole) {
           if (a.lse)
-            a.lse[orow] = l > 0.0f ? (m * c2 + log2f(l)) * 0.69314718055994531f : -INFINITY;
+            a.lse[orow] = l == 0.0f ? -INFINITY : (m * c2 + log2f(l)) * 0.69314718055994531f;
         } else if (valid) {
           a.part_ml[c.t0 ? extra + r : c.own * dense + orow] =
-              make_float2(m == -INFINITY ? m : m * c2, l);
+              make_float2(l != l ? 0.0f : m == -INFINITY ? m : m * c2, l); /* NaN goes by l */
         }
       }
       tc_fence_before();
@@ -1196,7 +1240,7 @@ __global__ void __launch_bounds__(256, MANY ? 7 : 2) attn_merge(const __grid_con
       __syncthreads();
     }
     if (!mine || part) continue;
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l; /* NaN stays NaN */
     __nv_bfloat16 *dst = a.out + (size_t)orow * D + lane * N;
     if (N == 4) {
       *(uint2 *)dst =
@@ -1207,7 +1251,7 @@ __global__ void __launch_bounds__(256, MANY ? 7 : 2) attn_merge(const __grid_con
       *dst = __float2bfloat16_rn(o[0] * inv);
     }
     if (a.lse && lane == 0)
-      a.lse[orow] = l > 0.0f ? (M + log2f(l)) * 0.69314718055994531f : -INFINITY;
+      a.lse[orow] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
   }
 }
 
@@ -1373,7 +1417,13 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
     return MK_ERR_INVALID_ARG;
   if (b->n_seqs > d.max_seqs || b->n_tokens > d.max_tokens || b->n_groups > d.max_groups)
     return MK_ERR_BATCH;
-  if ((int64_t)b->max_pages_per_seq * d.page_size > (1 << 30)) return MK_ERR_UNSUPPORTED;
+  const int64_t cap = (int64_t)b->max_pages_per_seq * d.page_size;
+  if (cap > (1 << 30)) return MK_ERR_UNSUPPORTED;
+  /* the line of items is measured in 32 bits */
+  const int64_t block = 2 * (kTile / (d.n_q_heads / d.n_kv_heads));
+  if ((2 * (b->n_tokens / block) + b->n_seqs + b->n_groups) * d.n_kv_heads *
+          ((cap / kTile + 1) * kPairTile + kPairItem) > (1 << 30))
+    return MK_ERR_UNSUPPORTED;
   if (b->n_seqs == 0 || b->n_tokens == 0) return MK_OK;
   if (!b->page_tables || !b->seq_lens || !aligned(b->page_tables, 4) || !aligned(b->seq_lens, 4) ||
       !aligned(b->q_offsets, 4) || !aligned(b->group_starts, 4) || !aligned(b->prefix_lens, 4) ||
@@ -1404,6 +1454,7 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   a.out = (__nv_bfloat16 *)out;
   a.lse = lse;
   a.scale_log2 = at->scale_log2;
+  a.few = (int64_t)b->n_tokens * d.n_q_heads * d.head_dim <= 4096;
   a.TB = kTile / a.G;
   a.inv_g = (65536 + a.G - 1) / a.G;
   a.inv_p = ((1ull << 38) + a.P - 1) / a.P;

@@ -4,7 +4,8 @@ Tolerance, per element.  With u = 2^-8 (half a step of bf16 relative to the
 value) and A = sum_j p_j |v_j| / sum_j p_j:
 
 - the result is rounded to bf16: u |exact|;
-- each probability is rounded to bf16 before the product with V: u A;
+- each probability is rounded to bf16 before the product with V: u A (calls with few
+  results keep the rest of that rounding and are far better; the bound holds for all);
 - a score is a sum of D products in 32 bits, off by at most
   E = 2^-23 D scale max_j sum_d |q_d k_jd| (2^-23: a chopped sum), which moves
   each probability by the factor e^E and the result by at most 2 E A;
@@ -282,6 +283,19 @@ def test_rising_scores_move_the_maximum(scale, each):
             continue                       # shares its first pages with sequence 1
         c.k[r] = (ramp + 0.1 * c.k[r].float()).to(t.bfloat16)
     c.check()
+
+
+@gpu
+def test_nan_in_a_query_stays_in_its_row():
+    """One head of one token holds NaN: its row is NaN, the others are what they were."""
+    for each in (3, 40):                   # singles, and a pair
+        c = Case([(200, [(10 + i, 1) for i in range(each)])], (16, 2, 64))
+        want = c.exact()
+        c.q[1, 3, 5] = float("nan")
+        out, lse = c.run()
+        assert np.isnan(out[1, 3]).all() and np.isnan(lse[1, 3])
+        out[1, 3], lse[1, 3] = want[0][1, 3], want[1][1, 3]
+        c.check((out, lse), want)
 
 
 @gpu
