@@ -1158,10 +1158,11 @@ __global__ void __launch_bounds__(kThreads, 1)
  * share it) where there are too few for all SMs; its warps take the heads, several a head
  * where there are fewer than eight.  Reads L2: the partials were written just before.
  * What bounds it is its chain of three loads (where, maxima and sums, weighted sums), so
- * 32 pieces' maxima and eight pieces' sums are in flight together; where blocks are MANY,
- * more of them a SM instead. */
+ * 32 pieces' maxima and four pieces' sums are in flight together (with eight, and 80
+ * registers, fewer blocks fit an SM: 64 samples of one prompt 42 us, so 38); where blocks are
+ * MANY, more of them an SM instead. */
 template <int D, bool MANY>
-__global__ void __launch_bounds__(256, MANY ? 7 : 2) attn_merge(const __grid_constant__ Args a, int n_cta, int blocks) {
+__global__ void __launch_bounds__(256, MANY ? 7 : 4) attn_merge(const __grid_constant__ Args a, int n_cta, int blocks) {
   __shared__ float sums[8][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int unit = blockIdx.x / blocks, rank = blockIdx.x - unit * blocks, units = a.n_tokens * a.Hkv;
@@ -1211,7 +1212,7 @@ __global__ void __launch_bounds__(256, MANY ? 7 : 2) attn_merge(const __grid_con
           l += f * ml.y;
         }
         const int m = min(32, n - i0);
-#pragma unroll(MANY ? 2 : 8)
+#pragma unroll(MANY ? 2 : 4)
         for (int i = part; i < m; i += split) {
           const float w = __shfl_sync(0xffffffffu, f, i);
           const float *src = a.part + (size_t)__shfl_sync(0xffffffffu, row, i) * D + lane * N;
