@@ -1392,6 +1392,7 @@ mk_status mk_attn_create(const mk_attn_desc *d, void *stream, mk_attn **out) {
   }
   if (e != cudaSuccess) {
     mk_attn_destroy(at);
+    cudaGetLastError(); /* reported here: not to the caller's next launch as well */
     return MK_ERR_CUDA;
   }
   *out = at;

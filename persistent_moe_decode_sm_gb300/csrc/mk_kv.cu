@@ -710,6 +710,7 @@ mk_status mk_kv_create(const mk_kv_desc *d, void *stream, mk_kv **out) {
   }
   if (e != cudaSuccess) {
     mk_kv_destroy(kv);
+    cudaGetLastError(); /* reported here: not to the caller's next launch as well */
     return MK_ERR_CUDA;
   }
   p.num_pages = d->num_pages;

@@ -454,6 +454,18 @@ def test_host_arguments_are_checked():
         a.batch(d["tables"].long(), d["lens"])
 
 
+@gpu
+def test_a_refused_workspace_leaves_no_error_behind():
+    """2^20 tokens of 1024 heads want 1.1 TB: MK_ERR_CUDA, and torch's next launches, which
+    ask for the last error, work."""
+    import torch
+
+    pool = torch.zeros((1, 16, 16, 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(mk.MkError):
+        mk.PrefixAttention(1024, 16, 128, 16, [(pool, pool)], max_tokens=1 << 20)
+    assert int((pool + 1).sum().item()) == pool.numel()
+
+
 # ------------------------------------------------------------------------- without a GPU
 
 
