@@ -111,7 +111,7 @@ typedef struct {
   int32_t n_layers;
   const void *const *k_caches;               /* HOST arrays [n_layers] of DEVICE pools */
   const void *const *v_caches;
-  float scale;                               /* of the scores; 0: 1 / sqrt(head_dim) */
+  float scale;                               /* of the scores, below 2^127; 0: 1 / sqrt(head_dim) */
 } mk_attn_desc;
 
 /* A call's batch.  The arrays are DEVICE memory and are read by the call on the

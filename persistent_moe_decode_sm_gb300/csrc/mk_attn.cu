@@ -1334,8 +1334,12 @@ mk_status mk_attn_create(const mk_attn_desc *d, void *stream, mk_attn **out) {
   if (d->n_q_heads < 1 || d->n_kv_heads < 1 || d->head_dim < 1 || d->page_size < 1 ||
       d->num_pages < 1 || d->max_tokens < 1 || d->max_seqs < 1 ||
       d->max_groups < 0 || d->n_layers < 1 || d->n_q_heads % d->n_kv_heads ||
-      !(d->scale >= 0.0f) || !std::isfinite(d->scale))
+      !(d->scale >= 0.0f))
     return MK_ERR_INVALID_ARG;
+  /* of the scores, for powers of two */
+  const double scale = d->scale > 0.0f ? (double)d->scale : 1.0 / std::sqrt((double)d->head_dim);
+  const float scale_log2 = (float)(scale * 1.4426950408889634);
+  if (!std::isfinite(scale_log2)) return MK_ERR_INVALID_ARG;
   if ((d->head_dim != 32 && d->head_dim != 64 && d->head_dim != 128) || d->page_size % 16 ||
       d->page_size > 256 || d->n_q_heads / d->n_kv_heads > 64 || d->n_q_heads > 1024 ||
       d->max_tokens > (1 << 20) || d->max_seqs > kMaxSeqs || d->max_groups > kMaxGroups ||
@@ -1355,8 +1359,7 @@ mk_status mk_attn_create(const mk_attn_desc *d, void *stream, mk_attn **out) {
   if (!at) return MK_ERR_CUDA;
   at->d = *d;
   at->d.k_caches = at->d.v_caches = nullptr;
-  const double scale = d->scale > 0.0f ? (double)d->scale : 1.0 / std::sqrt((double)d->head_dim);
-  at->scale_log2 = (float)(scale * 1.4426950408889634);
+  at->scale_log2 = scale_log2;
   at->stream = (cudaStream_t)stream;
   at->dev = dev;
   at->n_sm = prop.multiProcessorCount;

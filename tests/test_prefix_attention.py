@@ -491,6 +491,14 @@ def test_create_refuses(over, code):
     assert not h.value
 
 
+@pytest.mark.parametrize("scale, code", [(3e38, 1), (2e38, 8)])
+def test_a_scale_beyond_32_bits_is_refused(scale, code):
+    """Scores are multiplied by scale / ln 2, which has to be finite in fp32 (at most 3.4e38);
+    a scale that passes gets as far as the head size, which is refused with another status."""
+    h, d = ctypes.c_void_p(), _desc(scale=scale, head_dim=96)
+    assert mk.lib().mk_attn_create(ctypes.byref(d), None, ctypes.byref(h)) == code
+
+
 def test_null_handles_are_refused():
     L = mk.lib()
     assert L.mk_attn_create(None, None, None) == mk.MK_ERR_INVALID_ARG
