@@ -151,8 +151,8 @@ void mk_attn_destroy(mk_attn *attn);
  * share is read through the first one's table row: the whole pages of the
  * prefix, as far as the shortest of them fills them.  Their rows have to name
  * the same pages there.  Softmax in fp32;
- * the probabilities are rounded to bf16 for the product with V, and so is the
- * result.  The same call gives the same bits.  A call whose query tokens times
+ * the probabilities enter the product with V as two bf16 parts, good to 2^-17,
+ * and the result is rounded to bf16.  The same call gives the same bits.  A call whose query tokens times
  * table width are beyond what 32 bits of work items hold (2^20 tokens over
  * millions of keys) is MK_ERR_UNSUPPORTED.
  *

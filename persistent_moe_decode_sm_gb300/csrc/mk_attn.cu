@@ -29,7 +29,6 @@
 #include <cstdint>
 #include <cstring>
 #include <new>
-#include <type_traits>
 #include <vector>
 
 #include "mk_cache.h"
@@ -58,7 +57,6 @@ struct Args {
   __nv_bfloat16 *out;
   float *lse;
   float scale_log2; /* scale * log2(e) */
-  int32_t few;      /* the call has few results: see keeps_rest */
   int32_t TB;       /* query tokens of a row tile: 128 / G */
   uint32_t inv_g;   /* ceil(2^16 / G): r * inv_g >> 16 is r / G for r < 128 */
   unsigned long long inv_p; /* ceil(2^38 / P): k * inv_p >> 38 is k / P for k < 2^30 */
@@ -301,6 +299,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+/* What the two bf16 of w leave of e (exact in fp32), rounded to bf16.  The products take the
+ * bf16 halves as they are: with two unpacking instructions a pair instead, 4800 tokens of 32
+ * heads over 32768 keys took 3.18 ms, so 2.89. */
+__device__ __forceinline__ uint32_t rest_bf16(uint32_t w, float2 e) {
+  float x, y;
+  asm("{\n .reg .b16 l, h, m;\n mov.b32 {l, h}, %2;\n mov.b16 m, 0xBF80;\n"
+      " fma.rn.f32.bf16 %0, l, m, %3;\n fma.rn.f32.bf16 %1, h, m, %4;\n}"
+      : "=f"(x), "=f"(y) : "r"(w), "f"(e.x), "f"(e.y));
+  return pack_bf16(x, y);
+}
 /* Shared-memory matrix descriptor: swizzled rows, `sbo` bytes from one group of
  * 8 rows to the next, `lbo` from one column block to the next (N-major only). */
 __device__ __forceinline__ uint64_t mat_desc(uint32_t at, uint32_t lbo, uint32_t sbo, uint64_t swz) {
@@ -517,16 +525,6 @@ __device__ bool take_cut(const Args &a, Smem *sm) {
   return true;
 }
 
-/* P is rounded to bf16 for the product with V, which moves a result by about as much as
- * its own rounding does.  The smallest calls (up to 4096 results, rows of a piece in one
- * warp) keep the rest of the rounding as well, for a product of its own, and P is good to
- * 2^-17: they are bound by latency (16 rows over 480 shared keys: 15.1 us, with it 15.8)
- * and their few results have no others to average with.  For all pieces of up to 32 rows it
- * would cost 64 samples of one prompt a fifth (40 us, with it 48). */
-__device__ __forceinline__ bool keeps_rest(const Args &a, const Piece &p) {
-  return a.few && p.line == 1 && p.ntok * a.G <= 32;
-}
-
 /* The piece at place x of the pairs (line 0) or the singles (1), x < end; x moves
  * behind it.  A share that ends within an item's fixed cost has no tile of it: n is
  * 0.  By a whole warp. */
@@ -612,8 +610,8 @@ __device__ __forceinline__ void tell_merge(const Args &a, const Smem *sm, const 
 
 /* ---- the tiles ---------------------------------------------------------------- */
 
-/* S = Q K^T of a tile; half h of O (+)= P V: P's keys 64 h .. 64 h + 63, and the rest
- * of their rounding 64 columns further on. */
+/* S = Q K^T of a tile; half h of O (+)= P V: P's keys 64 h .. 64 h + 63, and what their
+ * rounding left, 64 columns further on. */
 template <int D>
 __device__ __forceinline__ void issue_qk(uint32_t s, uint64_t q, uint64_t k, uint32_t lead) {
   using C = Cfg<D>;
@@ -625,7 +623,7 @@ __device__ __forceinline__ void issue_qk(uint32_t s, uint64_t q, uint64_t k, uin
 }
 template <int D>
 __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, int h, bool acc,
-                                         bool rest, uint32_t lead) {
+                                         uint32_t lead) {
   using C = Cfg<D>;
   p += h * (kTile / 4);
   v += h * ((kTile / 2 * C::ROWB) >> 4);
@@ -633,11 +631,9 @@ __device__ __forceinline__ void issue_pv(uint32_t o, uint32_t p, uint64_t v, int
   for (int c = 0; c < kTile / 32; ++c)
     mma_ts(o, p + c * 8, v + ((c * 16 * C::ROWB) >> 4), inst_desc(D, true), acc || h > 0 || c > 0,
            lead);
-  if (rest) {
 #pragma unroll
-    for (int c = 0; c < kTile / 32; ++c)
-      mma_ts(o, p + kTile / 2 + c * 8, v + ((c * 16 * C::ROWB) >> 4), inst_desc(D, true), 1, lead);
-  }
+  for (int c = 0; c < kTile / 32; ++c)
+    mma_ts(o, p + kTile / 2 + c * 8, v + ((c * 16 * C::ROWB) >> 4), inst_desc(D, true), 1, lead);
 }
 
 /* Loads tile t of a piece, as far as its keys go: a box per page (or part of one) and
@@ -863,7 +859,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(&sm->qfull[s][qslot], (got / kQueue) & 1, abort);
         if (!ok) break;
         const int n = sm->queue[s][qslot].n, line = sm->queue[s][qslot].line;
-        const bool rest = keeps_rest(a, sm->queue[s][qslot]);
         __syncwarp();
         if (lane == 0) bar_arrive(&sm->qempty[s][qslot]);
         if (n == 0) break;
@@ -891,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int h = 0; ok && h < 2; ++h) {
             ok = warp_wait(&sm->pready[s][h], p_par, abort);
             tc_fence_after();
-            if (ok) issue_pv<D>(at_o, at_s, v0 + o, h, t > 0, rest, lead);
+            if (ok) issue_pv<D>(at_o, at_s, v0 + o, h, t > 0, lead);
           }
           if (!ok) break;
           p_par ^= 1;
@@ -949,8 +944,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int limit = min(c.kend, sm->len[b] - (sm->off[b + 1] - tok) + 1);
       const int warp_limit = __reduce_min_sync(0xffffffffu, limit);
       float m = -INFINITY, l = 0.0f; /* m in score units */
-      auto tiles = [&](auto keeps_rest) {
-        constexpr bool REST = decltype(keeps_rest)::value;
 #pragma unroll 1
       for (int t = 0; t < c.n; ++t) {
         const int k0 = c.key0 + (c.t0 + t) * kTile;
@@ -1034,7 +1027,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float off = m == -INFINITY ? 0.0f : -m * c2;
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
         /* P in quarters; the product of the first half starts under the second.  A quarter's
-         * store lands while the next is computed. */
+         * store lands while the next is computed.  P goes into the product as a bf16 value and
+         * the bf16 rounding of what that leaves, so it is good to 2^-17, as in the decode step
+         * (bf16 alone moves a result by about as much as the result's own rounding does).  The
+         * second product and its operand cost 64 samples of one prompt a fifth (36 us, with
+         * them 44), 16 sequences over long prefixes 8 % (75, 80), 4800 tokens over 32768 keys
+         * a third (2.12 ms, 2.85). */
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           uint32_t w[16], rest[16];
@@ -1046,13 +1044,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             e.y = exp2_approx(e.y);
             sum[k & 1] = add2(sum[k & 1], e);
             w[k] = pack_bf16(e.x, e.y);
-            if (REST)
-              rest[k] = pack_bf16(e.x - __uint_as_float(w[k] << 16),
-                                           e.y - __uint_as_float(w[k] & 0xffff0000u));
+            rest[k] = rest_bf16(w[k], e);
           }
           if (h != 2) {
             tmem_st16(at_s + h * 16, w);
-            if (REST) tmem_st16(at_s + kTile / 2 + h * 16, rest);
+            tmem_st16(at_s + kTile / 2 + h * 16, rest);
           }
           if (h >= 2) {
             tmem_wait_st();
@@ -1060,21 +1056,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) {
               bar_arrive(&sm->pready[s][h - 2]);
-              if (h == 3 && pair) bar_arrive(&sm->turn[1 - s]);
+              if (h == 2 && pair) bar_arrive(&sm->turn[1 - s]); /* behind h 3: 2.89 ms for 2.85 */
             }
           }
           if (h == 2) {
             tmem_st16(at_s + h * 16, w);
-            if (REST) tmem_st16(at_s + kTile / 2 + h * 16, rest);
+            tmem_st16(at_s + kTile / 2 + h * 16, rest);
           }
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
-      };
-      if (keeps_rest(a, c))
-        tiles(std::true_type{});
-      else
-        tiles(std::false_type{});
       if (!ok) break;
       ok = warp_wait(&sm->oready[s], o_par, abort);
       if (!ok) break;
@@ -1459,7 +1450,6 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   a.out = (__nv_bfloat16 *)out;
   a.lse = lse;
   a.scale_log2 = at->scale_log2;
-  a.few = (int64_t)b->n_tokens * d.n_q_heads * d.head_dim <= 4096;
   a.TB = kTile / a.G;
   a.inv_g = (65536 + a.G - 1) / a.G;
   a.inv_p = ((1ull << 38) + a.P - 1) / a.P;
