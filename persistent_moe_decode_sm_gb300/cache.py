@@ -121,8 +121,10 @@ class KvCache:
 
     def read(self, seqs):
         """(lengths, table rows) of sequences as numpy arrays (synchronises)."""
-        self.sync()
         rows = [int(i) for i in seqs]
+        if any(not 0 <= i < self.n_seqs for i in rows):
+            raise ValueError(f"seqs are numbers of table rows, 0 to {self.n_seqs - 1}")
+        self.sync()
         return (self.seq_lens[rows].cpu().numpy(), self.page_tables[rows].cpu().numpy())
 
     def close(self):

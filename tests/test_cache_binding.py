@@ -1,0 +1,28 @@
+"""Checks of the cache classes that come before any call into the library (no GPU)."""
+import numpy as np
+import pytest
+import torch
+
+import persistent_moe_decode_sm_gb300 as mk
+
+
+def cache_of(lens, tables):
+    """A KvCache over host tensors whose calls into the library do nothing."""
+    c = mk.KvCache.__new__(mk.KvCache)
+    c.handle = None
+    c.seq_lens = torch.tensor(lens, dtype=torch.int32)
+    c.page_tables = torch.tensor(tables, dtype=torch.int32)
+    c.n_seqs, c.max_pages_per_seq = c.page_tables.shape
+    c.sync = lambda: None
+    return c
+
+
+@pytest.mark.parametrize("rows", [[3], [0, 3], [-1], [0, -3], [2 ** 31]])
+def test_read_refuses_rows_that_are_not_there(rows):
+    """On the device an index behind the table would be an assertion in a kernel, and a
+    negative one another sequence."""
+    c = cache_of([5, 6, 7], [[0], [1], [2]])
+    with pytest.raises(ValueError):
+        c.read(rows)
+    lens, tables = c.read([2, 0, 2])
+    assert lens.tolist() == [7, 5, 7] and np.array_equal(tables, [[2], [0], [2]])
