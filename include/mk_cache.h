@@ -142,7 +142,7 @@ void mk_attn_destroy(mk_attn *attn);
  * elements from a token to the next (a multiple of 8; heads are contiguous);
  * out: bf16 [n_tokens][n_q_heads][head_dim], contiguous; lse: fp32
  * [n_tokens][n_q_heads] or NULL, the natural logarithm of the softmax sum.  Both
- * q and out 16-byte aligned.  A token that sees no key (T > L) gets zeros and
+ * q and out 16-byte aligned; q, out and lse do not overlap.  A token that sees no key (T > L) gets zeros and
  * lse -inf; rows behind the last sequence's tokens are not written.
  *
  * Only positions below a sequence's length are read, and their K and V have to

@@ -1264,6 +1264,9 @@ struct OnDevice {
 };
 
 bool aligned(const void *p, unsigned n) { return ((uintptr_t)p & (n - 1)) == 0; }
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+  return (uintptr_t)a < (uintptr_t)b + (uint64_t)nb && (uintptr_t)b < (uintptr_t)a + (uint64_t)na;
+}
 
 }  // namespace
 
@@ -1427,7 +1430,15 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
       (b->n_groups > 0 && (!b->group_starts || !b->prefix_lens)))
     return MK_ERR_INVALID_ARG;
   if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
-      q_token_stride < (int64_t)d.n_q_heads * d.head_dim || q_token_stride % 8)
+      q_token_stride < (int64_t)d.n_q_heads * d.head_dim || q_token_stride % 8 ||
+      q_token_stride >= (int64_t)1 << 39 /* of a tensor map, in elements */)
+    return MK_ERR_INVALID_ARG;
+  /* a piece writes its rows while another still reads queries */
+  const int64_t row = (int64_t)d.n_q_heads * d.head_dim * 2;
+  const int64_t q_bytes = (b->n_tokens - 1) * q_token_stride * 2 + row;
+  const int64_t lse_bytes = (int64_t)b->n_tokens * d.n_q_heads * 4;
+  if (overlap(q, q_bytes, out, b->n_tokens * row) ||
+      (lse && (overlap(q, q_bytes, lse, lse_bytes) || overlap(out, b->n_tokens * row, lse, lse_bytes))))
     return MK_ERR_INVALID_ARG;
   OnDevice on(at->dev);
   if (!on.ok) return MK_ERR_CUDA;
