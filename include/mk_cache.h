@@ -164,8 +164,19 @@ mk_status mk_prefix_attention(mk_attn *attn, int32_t layer, const mk_attn_batch 
 
 /* Waits for the stream and returns the first device error since the last
  * mk_attn_sync (MK_OK if none); clears it.  MK_ERR_INVALID_ARG while the stream
- * is being captured. */
+ * is being captured.  Besides the errors of mk_prefix_attention there is
+ * MK_ERR_DEVICE_TIMEOUT: a wait inside a kernel ran out of time, and that call's
+ * results are undefined; later calls are not touched by it. */
 mk_status mk_attn_sync(mk_attn *attn);
+
+/* How long a wait inside a kernel lasts before the call is given up
+ * (MK_ERR_DEVICE_TIMEOUT), in nanoseconds; 2e9 unless set.  For the calls behind
+ * this one; a captured call keeps the limit that it was captured with. */
+mk_status mk_attn_set_wait_limit_ns(mk_attn *attn, uint64_t ns);
+
+/* Test only: in the next call every SM waits for something that never comes, so
+ * that the way out of such a wait can be tested without a hang. */
+mk_status mk_attn_debug_poison_wait(mk_attn *attn);
 
 #ifdef __cplusplus
 }

@@ -134,7 +134,8 @@ EXPORTS = ["mk_create", "mk_build_schedule", "mk_decode_step", "mk_sync", "mk_de
            "mk_set_trace", "mk_get_trace", "mk_set_stage_trace_cta",
            "mk_kv_create", "mk_kv_destroy", "mk_kv_copy_pages", "mk_kv_fork", "mk_kv_resize",
            "mk_kv_compact", "mk_kv_sync",
-           "mk_attn_create", "mk_attn_destroy", "mk_prefix_attention", "mk_attn_sync"]
+           "mk_attn_create", "mk_attn_destroy", "mk_prefix_attention", "mk_attn_sync",
+           "mk_attn_set_wait_limit_ns", "mk_attn_debug_poison_wait"]
 _NO_STATUS = ("mk_destroy", "mk_status_string", "mk_kv_destroy", "mk_attn_destroy")
 
 _lib = None
@@ -182,6 +183,8 @@ def lib():
         L.mk_attn_destroy.restype = None
         L.mk_prefix_attention.argtypes = [vp, i32, ctypes.POINTER(mk_attn_batch), vp, i64, vp, vp]
         L.mk_attn_sync.argtypes = [vp]
+        L.mk_attn_set_wait_limit_ns.argtypes = [vp, u64]
+        L.mk_attn_debug_poison_wait.argtypes = [vp]
         for n in EXPORTS:
             if n not in _NO_STATUS:
                 getattr(L, n).restype = i32

@@ -237,6 +237,11 @@ class PrefixAttention:
             q.stride(0) if rows[0] > 1 else self.heads * self.head_dim, out.data_ptr(),
             None if lse is None else lse.data_ptr()), "mk_prefix_attention")
 
+    def set_wait_limit_ns(self, ns: int):
+        """How long a wait inside a kernel of the calls behind this one lasts before the call
+        is given up, which sync() then raises; 2 seconds unless set."""
+        _check(self._lib.mk_attn_set_wait_limit_ns(self.handle, ns), "mk_attn_set_wait_limit_ns")
+
     def sync(self):
         """Waits for the stream; raises the MkError of the first device error."""
         _check(self._lib.mk_attn_sync(self.handle), "mk_attn_sync")

@@ -46,7 +46,7 @@ constexpr int kPairTile = 3, kSingleTile = 2, kPairItem = 11, kSingleItem = 4;
 constexpr int kShare = 6; /* a CTA's share at least: each of its streams meets a tile of a long item */
 constexpr int kQueue = 4;          /* pieces that a producer is ahead of its stream */
 constexpr int kMaxSeqs = 1024, kMaxGroups = 512; /* of a call: the cut's tables are in shared memory */
-constexpr uint64_t kWaitLimit = 2000000000ull; /* ns */
+constexpr unsigned long long kWaitLimit = 2000000000ull; /* ns: of a call unless set, and of the last waits */
 /* The reference that a row's P are taken against moves only when a score exceeds it by
  * this much (in powers of two): P then stays below 2^8, its relative precision in bf16
  * is the same, and the accumulator is rescaled a few times a row instead of in most tiles. */
@@ -61,6 +61,8 @@ struct Args {
   uint32_t inv_g;   /* ceil(2^16 / G): r * inv_g >> 16 is r / G for r < 128 */
   unsigned long long inv_p; /* ceil(2^38 / P): k * inv_p >> 38 is k / P for k < 2^30 */
   int32_t *err_host;
+  unsigned long long wait_limit; /* ns */
+  int32_t poison;    /* test hook: stream 0's issuer waits for what never comes */
   /* workspace */
   int32_t *bad;      /* the batch is not sound */
   int4 *where;       /* [2][n_tokens][Hkv], zero between calls: where a token's partials are, of
@@ -94,6 +96,12 @@ struct Piece {
   int begin;           /* the item's first place */
 };
 
+/* A wait that runs out of time ends the CTA's work: every role looks here while it waits. */
+struct Stop {
+  int abort;
+  unsigned long long limit; /* ns */
+};
+
 struct Smem { /* behind the tiles */
   uint64_t kfull[4], kempty[4], vfull[4], vempty[4];
   uint64_t sfull[2], pready[2][2], oready[2], drain[2];
@@ -102,7 +110,8 @@ struct Smem { /* behind the tiles */
   uint64_t qfull[2][kQueue], qempty[2][kQueue]; /* the queue's */
   Piece queue[2][kQueue];
   uint32_t tmem;
-  int abort;
+  Stop stop;
+  int fills[2][4], q_fills[2];                /* uses begun of each K and V slot, of each Q */
   unsigned long long sums[2][kThreads / 32];
   int total, pairs;   /* length of the line, of its pairs */
   int32_t off[kMaxSeqs + 1], len[kMaxSeqs];
@@ -142,22 +151,22 @@ __device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
   return ok != 0;
 }
 /* Waits for a phase; false when another role gave up or the limit ran out. */
-__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, Stop *stop) {
   uint64_t since = 0;
   for (int i = 0;; ++i) {
     if (__all_sync(0xffffffffu, bar_try(b, parity))) return true;
-    if (__any_sync(0xffffffffu, *abort != 0)) return false;
+    if (__any_sync(0xffffffffu, *(volatile int *)&stop->abort != 0)) return false;
     if ((i & 63) == 63) {
       const uint64_t t = now_ns();
       if (!since)
         since = t;
-      else if (t - since > kWaitLimit)
-        *abort = 1;
+      else if (t - since > stop->limit)
+        *(volatile int *)&stop->abort = 1;
     }
   }
 }
-__device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, volatile int *abort) {
-  return __all_sync(0xffffffffu, bar_try(b, parity)) || bar_wait(b, parity, abort);
+__device__ __forceinline__ bool warp_wait(uint64_t *b, uint32_t parity, Stop *stop) {
+  return __all_sync(0xffffffffu, bar_try(b, parity)) || bar_wait(b, parity, stop);
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
                                        uint64_t *bar, uint32_t lead) {
@@ -659,7 +668,7 @@ struct Loader {
       page = __ldg(a.tables + (size_t)p.seq * a.max_pages + page_of(k));
   }
   __device__ __forceinline__ void load(const Piece &p, int t, int pg, const CUtensorMap *map,
-                                       uint8_t *tile, uint64_t *full) {
+                                       uint8_t *tile, uint64_t *full, int *fills) {
     const int k0 = p.key0 + (p.t0 + t) * kTile;
     const int k = k0 + lane * a.box_rows;
     const bool mine = lane < boxes && k < p.kend;
@@ -668,7 +677,10 @@ struct Loader {
     const unsigned set = __ballot_sync(0xffffffffu, good);
     const int y = (pg * a.Hkv + p.kvh) * a.P + k - page_of(k) * a.P;
     const uint32_t bytes = a.box_rows * C::ROWB;
-    if (lead) bar_expect(full, __popc(set) * bytes * C::NH);
+    if (lead) {
+      atomicAdd(fills, 1);
+      bar_expect(full, __popc(set) * bytes * C::NH);
+    }
     __syncwarp();
     uint32_t dst = saddr(tile);
 #pragma unroll 4
@@ -724,7 +736,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_init(&sm->qempty[s][i], 5); /* the issuer, four softmax warps */
       }
     }
-    sm->abort = 0;
+    sm->stop.abort = 0;
+    sm->stop.limit = a.wait_limit;
+    for (int i = 0; i < 2; ++i) {
+      for (int k = 0; k < C::STAGES; ++k) sm->fills[i][k] = 0;
+      sm->q_fills[i] = 0;
+    }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 10) {
@@ -740,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool sound = take_cut(a, sm);
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
-  volatile int *abort = &sm->abort;
+  Stop *stop = &sm->stop;
   const long long n_cta = gridDim.x;
   const int TB = a.TB;
 
@@ -783,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const int qslot = put % kQueue;
-        ok = warp_wait(&sm->qempty[s][qslot], ((put / kQueue) & 1) ^ 1, abort);
+        ok = warp_wait(&sm->qempty[s][qslot], ((put / kQueue) & 1) ^ 1, stop);
         if (!ok) break;
         if (lane == 0) {
           sm->queue[s][qslot] = p;
@@ -801,18 +818,21 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int kv = line == 0 ? s : 0; kv <= (line == 0 ? s : 1); ++kv) {
             const uint32_t par = line == 0 ? it / C::STAGES : (kv ? armed_v : armed_k) >> slot;
-            ok = warp_wait(kv ? &sm->vempty[slot] : &sm->kempty[slot], (par & 1) ^ 1, abort);
+            ok = warp_wait(kv ? &sm->vempty[slot] : &sm->kempty[slot], (par & 1) ^ 1, stop);
             if (!ok) break;
             ld.load(p, t, page, kv ? &vmap : &kmap, (kv ? vs : ks) + slot * C::TILE,
-                    kv ? &sm->vfull[slot] : &sm->kfull[slot]);
+                    kv ? &sm->vfull[slot] : &sm->kfull[slot], &sm->fills[kv][slot]);
             if (line == 1) (kv ? armed_v : armed_k) ^= 1u << slot;
             if (t == 0 && (line == 0 || kv == 0)) {
               /* Q: [tokens][heads of the group][64 dims], the rows' order.  Rows behind the
                * last token are other rows of Q or zeros, and are not looked at. */
-              ok = warp_wait(&sm->q_free[s], (q_uses & 1) ^ 1, abort);
+              ok = warp_wait(&sm->q_free[s], (q_uses & 1) ^ 1, stop);
               if (!ok) break;
               ++q_uses;
-              if (ld.lead) bar_expect(&sm->q_full[s], C::NH * C::ROWB * TB * a.G);
+              if (ld.lead) {
+                ++sm->q_fills[s];
+                bar_expect(&sm->q_full[s], C::NH * C::ROWB * TB * a.G);
+              }
               __syncwarp();
 #pragma unroll
               for (int h = 0; h < C::NH; ++h)
@@ -820,27 +840,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                        &sm->q_full[s], ld.lead);
             }
           }
+          if (!ok) break;
           if (t == 0 && p.t0 == 0 && (line == 1 || s == 0)) tell_merge(a, sm, p);
           if (line == 0)
             ++it;
           else
             ring = ring + 1 == R ? 0 : ring + 1;
         }
-      }
-      if (!ok) {
-        /* gave up: let the copies in flight land (each wait has its limit; a slot that
-         * was not filled since passes at once or by its earlier phase) */
-        volatile int none = 0;
-        for (int i = 0; i < C::STAGES; ++i) {
-          const int last = it - 1 - (it - 1 - i + 2 * C::STAGES) % C::STAGES;
-          if (line == 0 && it > 0 && last >= 0)
-            warp_wait(s == 0 ? &sm->kfull[i] : &sm->vfull[i], (last / C::STAGES) & 1, &none);
-          if (line > 0 && i / R == s) {
-            warp_wait(&sm->kfull[i], ((armed_k >> i) & 1) ^ 1, &none);
-            warp_wait(&sm->vfull[i], ((armed_v >> i) & 1) ^ 1, &none);
-          }
-        }
-        if (q_uses) warp_wait(&sm->q_full[s], (q_uses - 1) & 1, &none);
       }
     } else {
       /* ---- issuer of stream s: S = Q K^T of a tile, then O += P V of its halves as P comes.
@@ -850,13 +856,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q0 = mat_desc(saddr(qs), 16, 8 * C::ROWB, C::SWIZZLE);
       const uint64_t k0 = mat_desc(saddr(ks), 16, 8 * C::ROWB, C::SWIZZLE);
       const uint64_t v0 = mat_desc(saddr(vs), C::BLOCK, 8 * C::ROWB, C::SWIZZLE);
-      bool ok = true;
+      bool ok = !(a.poison && s == 0) || warp_wait(&sm->drain[s], 0, stop);
       int it = 0, ring = 0;
       uint32_t par = 0, q_par = 0, p_par = 0; /* singles: parities of the stream's slots */
       bool singles = false;
-      for (int got = 0;; ++got) {
+      for (int got = 0; ok; ++got) {
         const int qslot = got % kQueue;
-        ok = warp_wait(&sm->qfull[s][qslot], (got / kQueue) & 1, abort);
+        ok = warp_wait(&sm->qfull[s][qslot], (got / kQueue) & 1, stop);
         if (!ok) break;
         const int n = sm->queue[s][qslot].n, line = sm->queue[s][qslot].line;
         __syncwarp();
@@ -867,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < C::STAGES; ++i)
             par |= (uint32_t)(((it + C::STAGES - 1 - i) / C::STAGES) & 1) << i;
         }
-        ok = warp_wait(&sm->q_full[s], q_par, abort);
+        ok = warp_wait(&sm->q_full[s], q_par, stop);
         if (!ok) break;
         q_par ^= 1;
 #pragma unroll 1
@@ -875,16 +881,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int slot = line == 0 ? it % C::STAGES : s * R + ring;
           const uint32_t parity = (line == 0 ? it / C::STAGES : par >> slot) & 1;
           const uint32_t o = (uint32_t)slot * (C::TILE >> 4);
-          ok = warp_wait(&sm->kfull[slot], parity, abort);
+          ok = warp_wait(&sm->kfull[slot], parity, stop);
           if (!ok) break;
           tc_fence_after();
           issue_qk<D>(at_s, q0 + (uint32_t)s * (C::TILE >> 4), k0 + o, lead);
           tc_commit(&sm->sfull[s], lead);
           tc_commit(&sm->kempty[slot], lead);
           if (line == 1) tc_commit(&sm->kempty[slot], lead); /* a pair's two readers count one each */
-          ok = warp_wait(&sm->vfull[slot], parity, abort);
+          ok = warp_wait(&sm->vfull[slot], parity, stop);
           for (int h = 0; ok && h < 2; ++h) {
-            ok = warp_wait(&sm->pready[s][h], p_par, abort);
+            ok = warp_wait(&sm->pready[s][h], p_par, stop);
             tc_fence_after();
             if (ok) issue_pv<D>(at_o, at_s, v0 + o, h, t > 0, lead);
           }
@@ -902,11 +908,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       }
-      if (!ok) { /* gave up: let the products in flight end */
-        volatile int none = 0;
-        tc_commit(&sm->drain[s], lead);
-        warp_wait(&sm->drain[s], 0, &none);
-      }
+      /* The products, and what their commits write into shared memory, end here in any case. */
+      Stop last{0, kWaitLimit};
+      tc_commit(&sm->drain[s], lead);
+      if (!warp_wait(&sm->drain[s], 0, &last)) *(volatile int *)&stop->abort = 1;
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -923,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (; ok; ++got) {
       const int qslot = got % kQueue;
-      ok = warp_wait(&sm->qfull[s][qslot], (got / kQueue) & 1, abort);
+      ok = warp_wait(&sm->qfull[s][qslot], (got / kQueue) & 1, stop);
       if (!ok) break;
       const Piece c = sm->queue[s][qslot];
       __syncwarp();
@@ -947,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int t = 0; t < c.n; ++t) {
         const int k0 = c.key0 + (c.t0 + t) * kTile;
-        ok = warp_wait(&sm->sfull[s], s_par, abort);
+        ok = warp_wait(&sm->sfull[s], s_par, stop);
         if (!ok) break;
         s_par ^= 1;
         tc_fence_after();
@@ -955,14 +960,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           /* The streams of a pair take turns, stream 0's tile before stream 1's: side by
            * side they would share the exponential unit and then leave it, and the tensor
            * cores, idle together. */
-          ok = warp_wait(&sm->turn[s], (it - 1 + s) & 1, abort);
+          ok = warp_wait(&sm->turn[s], (it - 1 + s) & 1, stop);
           if (!ok) break;
         }
         const int slot = pair ? it % C::STAGES : s * R + ring;
         if (k0 + kTile > c.kend) {
           /* zero the V rows behind the last key: what lies there may be NaN */
           ok = warp_wait(&sm->vfull[slot], pair ? (it / C::STAGES) & 1 : (v_par >> slot) & 1,
-                         abort);
+                         stop);
           if (!ok) break;
           if (k0 + r >= c.kend) {
             uint8_t *vr = vs + slot * C::TILE + r * C::ROWB;
@@ -1067,7 +1072,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
       if (!ok) break;
-      ok = warp_wait(&sm->oready[s], o_par, abort);
+      ok = warp_wait(&sm->oready[s], o_par, stop);
       if (!ok) break;
       o_par ^= 1;
       tc_fence_after();
@@ -1135,8 +1140,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!sound) *(volatile int32_t *)a.err_host = MK_ERR_INVALID_ARG;
   }
   __syncthreads();
-  if (tid == 0 && *abort) *(volatile int32_t *)a.err_host = MK_ERR_DEVICE_TIMEOUT;
   if (warp == 10) {
+    if (*(volatile int *)&stop->abort) {
+      /* Somebody gave up, so nobody may have waited for the last copy into each slot.  Shared
+       * memory stays until they have landed. */
+      if (lane == 0) *(volatile int32_t *)a.err_host = MK_ERR_DEVICE_TIMEOUT;
+      Stop last{0, kWaitLimit};
+      for (int i = 0; i < 2; ++i)
+        if (sm->q_fills[i]) warp_wait(&sm->q_full[i], (sm->q_fills[i] - 1) & 1, &last);
+      for (int i = 0; i < C::STAGES; ++i) {
+        if (sm->fills[0][i]) warp_wait(&sm->kfull[i], (sm->fills[0][i] - 1) & 1, &last);
+        if (sm->fills[1][i]) warp_wait(&sm->vfull[i], (sm->fills[1][i] - 1) & 1, &last);
+      }
+    }
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
   }
@@ -1277,6 +1293,8 @@ struct mk_attn {
   int box_rows = 0;
   cudaStream_t stream = nullptr;
   int dev = 0, n_sm = 0;
+  unsigned long long wait_limit = kWaitLimit;
+  bool poison = false; /* the next call */
   uint8_t *ws = nullptr;
   size_t o_where = 0, o_part = 0, o_ml = 0;
   int32_t *err_host = nullptr, *err_dev = nullptr;
@@ -1465,6 +1483,8 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   a.inv_g = (65536 + a.G - 1) / a.G;
   a.inv_p = ((1ull << 38) + a.P - 1) / a.P;
   a.err_host = at->err_dev;
+  a.wait_limit = at->wait_limit;
+  a.poison = at->poison;
   a.bad = (int32_t *)at->ws;
   a.where = (int4 *)(at->ws + at->o_where);
   a.part = (float *)(at->ws + at->o_part);
@@ -1475,7 +1495,21 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   const cudaError_t e = d.head_dim == 32   ? launch<32>(at, layer, qmap, a)
                         : d.head_dim == 64 ? launch<64>(at, layer, qmap, a)
                                            : launch<128>(at, layer, qmap, a);
-  return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  if (e != cudaSuccess) return MK_ERR_CUDA;
+  at->poison = false;
+  return MK_OK;
+}
+
+mk_status mk_attn_set_wait_limit_ns(mk_attn *at, uint64_t ns) {
+  if (!at || ns == 0) return MK_ERR_INVALID_ARG;
+  at->wait_limit = ns;
+  return MK_OK;
+}
+
+mk_status mk_attn_debug_poison_wait(mk_attn *at) {
+  if (!at) return MK_ERR_INVALID_ARG;
+  at->poison = true;
+  return MK_OK;
 }
 
 mk_status mk_attn_sync(mk_attn *at) {

@@ -1,4 +1,6 @@
 """mk_prefix_attention: calls that its documentation allows or refuses beside the plain ones."""
+import time
+
 import pytest
 
 import persistent_moe_decode_sm_gb300 as mk
@@ -29,3 +31,33 @@ def test_results_over_the_queries_are_refused():
     a.run(0, b, both[:3], both[3:6], lse)
     a.sync()
     c.check((both[3:6].double().cpu().numpy(), lse.double().cpu().numpy()))
+
+
+def test_wait_limits_are_checked():
+    L = mk.lib()
+    assert L.mk_attn_set_wait_limit_ns(None, 5) == mk.MK_ERR_INVALID_ARG
+    assert L.mk_attn_debug_poison_wait(None) == mk.MK_ERR_INVALID_ARG
+
+
+@gpu
+@pytest.mark.parametrize("each, heads", [(3, (4, 2, 64)), (40, (32, 4, 128)), (70, (6, 2, 32))])
+def test_a_wait_that_is_never_met_ends_the_call(each, heads):
+    """The call ends with a status after the limit; the next one is right, on the same handle."""
+    c = Case([(700, [(5 + i, 1) for i in range(each)])], heads)     # singles, and pairs
+    t, d = c.t, c.device()
+    a, b = c.attention(d)
+    out = t.full(d["q"].shape, 123.0, dtype=t.bfloat16, device="cuda")
+    lse = t.full(d["q"].shape[:2], 123.0, device="cuda")
+    with pytest.raises(mk.MkError):
+        a.set_wait_limit_ns(0)
+    a.set_wait_limit_ns(100_000_000)
+    assert mk.lib().mk_attn_debug_poison_wait(a.handle) == mk.MK_OK
+    start = time.time()
+    a.run(0, b, d["q"], out, lse)
+    with pytest.raises(mk.MkError) as e:
+        a.sync()
+    assert e.value.code == mk.MK_ERR_DEVICE_TIMEOUT
+    assert 0.1 <= time.time() - start < 10.0
+    a.run(0, b, d["q"], out, lse)
+    a.sync()
+    c.check((out.double().cpu().numpy(), lse.double().cpu().numpy()))
