@@ -65,6 +65,7 @@ struct Args {
   int32_t poison;    /* test hook: stream 0's issuer waits for what never comes */
   /* workspace */
   int32_t *bad;      /* the batch is not sound */
+  int32_t *error;    /* the first since mk_attn_sync took one, 0: none */
   int4 *where;       /* [2][n_tokens][Hkv], zero between calls: where a token's partials are, of
                       * the shared keys and of its own.  x: pieces + 1, 1: written already, 0:
                       * none; y: the first piece's worker; z: the token's first row in worker 0's
@@ -72,6 +73,10 @@ struct Args {
   float *part;       /* [2 * n_tokens * Hq + 4 * SMs * 128][D] weighted sums */
   float2 *part_ml;   /* the same rows: maximum (in powers of two), sum */
 };
+
+__device__ __forceinline__ void report(const Args &a, int code) {
+  if (atomicCAS(a.error, 0, code) == 0) *(volatile int32_t *)a.err_host = code;
+}
 
 template <int D>
 struct Cfg {
@@ -673,7 +678,7 @@ struct Loader {
     const int k = k0 + lane * a.box_rows;
     const bool mine = lane < boxes && k < p.kend;
     const bool good = mine && (unsigned)pg < (unsigned)a.num_pages;
-    if (mine && !good) *(volatile int32_t *)a.err_host = MK_ERR_PAGE_OOB;
+    if (mine && !good) report(a, MK_ERR_PAGE_OOB);
     const unsigned set = __ballot_sync(0xffffffffu, good);
     const int y = (pg * a.Hkv + p.kvh) * a.P + k - page_of(k) * a.P;
     const uint32_t bytes = a.box_rows * C::ROWB;
@@ -1137,14 +1142,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (blockIdx.x == 0 && tid == 0) {
     *a.bad = !sound;
-    if (!sound) *(volatile int32_t *)a.err_host = MK_ERR_INVALID_ARG;
+    if (!sound) report(a, MK_ERR_INVALID_ARG);
   }
   __syncthreads();
   if (warp == 10) {
     if (*(volatile int *)&stop->abort) {
       /* Somebody gave up, so nobody may have waited for the last copy into each slot.  Shared
        * memory stays until they have landed. */
-      if (lane == 0) *(volatile int32_t *)a.err_host = MK_ERR_DEVICE_TIMEOUT;
+      if (lane == 0) report(a, MK_ERR_DEVICE_TIMEOUT);
       Stop last{0, kWaitLimit};
       for (int i = 0; i < 2; ++i)
         if (sm->q_fills[i]) warp_wait(&sm->q_full[i], (sm->q_fills[i] - 1) & 1, &last);
@@ -1486,6 +1491,7 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   a.wait_limit = at->wait_limit;
   a.poison = at->poison;
   a.bad = (int32_t *)at->ws;
+  a.error = (int32_t *)at->ws + 1;
   a.where = (int4 *)(at->ws + at->o_where);
   a.part = (float *)(at->ws + at->o_part);
   a.part_ml = (float2 *)(at->ws + at->o_ml);
@@ -1521,7 +1527,10 @@ mk_status mk_attn_sync(mk_attn *at) {
   if (cap != cudaStreamCaptureStatusNone) return MK_ERR_INVALID_ARG;
   if (cudaStreamSynchronize(at->stream) != cudaSuccess) return MK_ERR_CUDA;
   const int32_t code = *(volatile int32_t *)at->err_host;
+  if (code == 0) return MK_OK;
   *(volatile int32_t *)at->err_host = 0;
+  if (cudaMemsetAsync((int32_t *)at->ws + 1, 0, sizeof(int32_t), at->stream) != cudaSuccess)
+    return MK_ERR_CUDA;
   return code;
 }
 

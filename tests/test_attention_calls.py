@@ -61,3 +61,30 @@ def test_a_wait_that_is_never_met_ends_the_call(each, heads):
     a.run(0, b, d["q"], out, lse)
     a.sync()
     c.check((out.double().cpu().numpy(), lse.double().cpu().numpy()))
+
+
+@gpu
+@pytest.mark.parametrize("order", [("page", "batch"), ("batch", "page"), ("time", "batch"),
+                                   ("time", "page"), ("page", "fine", "time", "batch")])
+def test_the_first_error_is_reported(order):
+    c = Case([(32, [(50, 1), (8, 1)])], (4, 2, 64))
+    t, d = c.t, c.device()
+    a, fine = c.attention(d)
+    wild = c.tables.copy()
+    wild[0, 3] = 10 ** 6
+    wild, wrong = t.from_numpy(wild).cuda(), t.tensor([-1, 40], dtype=t.int32).cuda()
+    calls = {"fine": fine, "time": fine, "page": a.batch(wild, d["lens"]),
+             "batch": a.batch(d["tables"], wrong)}
+    codes = {"time": mk.MK_ERR_DEVICE_TIMEOUT, "page": mk.MK_ERR_PAGE_OOB,
+             "batch": mk.MK_ERR_INVALID_ARG}
+    out = t.empty_like(d["q"])
+    a.set_wait_limit_ns(50_000_000)
+    for _ in range(2):                     # taken once, so the second turn starts anew
+        for name in order:
+            if name == "time":
+                mk.lib().mk_attn_debug_poison_wait(a.handle)
+            a.run(0, calls[name], d["q"], out)
+        with pytest.raises(mk.MkError) as e:
+            a.sync()
+        assert e.value.code == codes[order[0]]
+        a.sync()
