@@ -38,7 +38,9 @@ extern "C" {
  * or length out of range, the same destination twice, a used table entry that
  * names no held page) or that runs out of pages changes nothing; its status is
  * kept, the calls behind it change nothing either, and mk_kv_sync returns the
- * status and clears it. */
+ * status and clears it.  Where several arguments of a call are wrong, a page or
+ * length out of range (MK_ERR_PAGE_OOB) is reported before anything else
+ * (MK_ERR_INVALID_ARG), and both before MK_ERR_NO_PAGES. */
 
 typedef struct {
   int32_t n_pools;            /* K and V pools of every layer: 2 * n_layers (at most 512) */

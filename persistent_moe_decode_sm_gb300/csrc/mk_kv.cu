@@ -107,8 +107,9 @@ __device__ int block_scan(int v, int *sums, int *total) {
   return before + x - v;
 }
 
+/* Of several wrong arguments the largest status is kept, whichever is met first. */
 __device__ __forceinline__ void refuse(const Params &p, int code) {
-  atomicCAS(&p.ctrl->call_err, 0, code);
+  atomicMax(&p.ctrl->call_err, code);
 }
 
 /* A used table entry has to name a held page.  Returns it, or -1 (refused). */
