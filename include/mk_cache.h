@@ -79,10 +79,14 @@ mk_status mk_kv_copy_pages(mk_kv *kv, int32_t n, const int32_t *src_pages,
 mk_status mk_kv_fork(mk_kv *kv, int32_t n, const int32_t *src_seqs, const int32_t *dst_seqs);
 
 /* Sets the length of sequences seqs[i] (distinct) to new_lens[i] (DEVICE int32
- * [n], n <= n_seqs), the releases of all of them first.  Growing takes free
- * pages, and replaces a partly filled last page that has other holders by a
- * copy; their new positions hold whatever the pages held.  Shrinking releases
- * the pages behind the new length; 0 frees the sequence.  MK_ERR_NO_PAGES when
+ * [n], n <= n_seqs), the releases of all of them first: what shrinking rows hold
+ * alone, growing ones can take.  Growing takes free pages, and replaces a partly
+ * filled last page that had other holders before the call by a copy; the new
+ * positions hold whatever the pages held.  Every row that grows out of such a page
+ * takes a copy, also where the others leave the page in the same call, and the page
+ * is free behind the call if nobody is left: to keep it for the last one, resize the
+ * others in a call before.  Shrinking releases the pages behind the new length; 0
+ * frees the sequence.  MK_ERR_NO_PAGES when
  * there are too few, MK_ERR_PAGE_OOB for a length behind the table row. */
 mk_status mk_kv_resize(mk_kv *kv, int32_t n, const int32_t *seqs, const int32_t *new_lens);
 
