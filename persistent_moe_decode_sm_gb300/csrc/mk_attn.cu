@@ -670,7 +670,8 @@ struct Loader {
     const int k = p.key0 + (p.t0 + t) * kTile + lane * a.box_rows;
     page = -1;
     if (t < p.n && lane < boxes && k < p.kend)
-      page = __ldg(a.tables + (size_t)p.seq * a.max_pages + page_of(k));
+      /* through L2: the grid before this one may have written the tables while this one started */
+      page = __ldcg(a.tables + (size_t)p.seq * a.max_pages + page_of(k));
   }
   __device__ __forceinline__ void load(const Piece &p, int t, int pg, const CUtensorMap *map,
                                        uint8_t *tile, uint64_t *full, int *fills) {

@@ -1,6 +1,7 @@
 """mk_prefix_attention: calls that its documentation allows or refuses beside the plain ones."""
 import time
 
+import numpy as np
 import pytest
 
 import persistent_moe_decode_sm_gb300 as mk
@@ -88,3 +89,37 @@ def test_the_first_error_is_reported(order):
             a.sync()
         assert e.value.code == codes[order[0]]
         a.sync()
+
+
+@gpu
+def test_behind_page_calls_without_a_wait():
+    """Pages move and tables change right before the attention reads them, on one stream."""
+    c = Case([(300, [(40 + 7 * i, 1) for i in range(12)])], (8, 2, 64), P=16, spare=400)
+    t = c.t
+    n, want = c.k.shape[0], c.exact()
+    rng = np.random.default_rng(0)
+    i32 = dict(dtype=t.int32, device="cuda")
+    kept = t.from_numpy(c.tables).cuda(), c.k.cuda(), c.v.cuda()
+    refs = t.tensor(np.bincount(np.concatenate(c.rows), minlength=n), **i32)
+    tables, k, v, holders = (x.clone() for x in kept + (refs,))
+    lens = t.tensor(c.lens, **i32)
+    cache = mk.KvCache([k, v], tables, lens, holders, 16)
+    d = c.device(k=k, v=v, tables=tables, lens=lens)
+    a, b = c.attention(d)
+    outs = []
+    for turn in range(6):
+        tables.copy_(kept[0]), k.copy_(kept[1]), v.copy_(kept[2]), holders.copy_(refs)
+        order = t.from_numpy(rng.permutation(n)).cuda()          # page p lies at order[p]
+        k[order], v[order], holders[order] = kept[1], kept[2], refs
+        tables.copy_(t.where(kept[0] < 0, kept[0], order[kept[0].clamp(min=0).long()].int()))
+        out = t.empty_like(d["q"]), t.empty(d["q"].shape[:2], device="cuda")
+        a.run(0, b, d["q"], *out)
+        cache.compact()
+        again = t.empty_like(d["q"]), t.empty(d["q"].shape[:2], device="cuda")
+        a.run(0, b, d["q"], *again)
+        outs += [out, again]
+    a.sync()
+    cache.sync()
+    for out, lse in outs:
+        c.check((out.double().cpu().numpy(), lse.double().cpu().numpy()), want)
+    assert int((holders[:int((refs > 0).sum())] > 0).sum()) == int((refs > 0).sum())
