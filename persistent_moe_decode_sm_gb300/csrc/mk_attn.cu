@@ -31,19 +31,16 @@
 #include <new>
 #include <vector>
 
+#include "mk_attn_cut.h"
 #include "mk_cache.h"
 #include "mk_plan.h"
 
 namespace {
 
+using namespace mk_cut;
+
 constexpr int kThreads = 384;      /* two softmax warpgroups, two producers, two issuers */
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88; /* 256 * 208 + 128 * 88 = 384 * 168 */
-constexpr int kTile = 128;         /* keys per tile; rows per row tile */
-/* The line's unit is about 1100 cycles.  A tile takes 3300 of a CTA in a pair (its two
- * products and softmaxes, mostly hidden under one another) and 2300 in a single (64 KB at
- * the SM's share of HBM); an item's beginning and end take 12000 and 4000 on top. */
-constexpr int kPairTile = 3, kSingleTile = 2, kPairItem = 11, kSingleItem = 4;
-constexpr int kShare = 6; /* a CTA's share at least: each of its streams meets a tile of a long item */
 constexpr int kQueue = 4;          /* pieces that a producer is ahead of its stream */
 constexpr int kMaxSeqs = 1024, kMaxGroups = 512; /* of a call: the cut's tables are in shared memory */
 constexpr unsigned long long kWaitLimit = 2000000000ull; /* ns: of a call unless set, and of the last waits */
@@ -337,51 +334,6 @@ __host__ __device__ constexpr uint32_t inst_desc(int n, bool b_n_major) {
 
 /* ---- the cut ------------------------------------------------------------------ */
 
-/* Query tokens come in blocks of two row tiles.  T tokens: this many blocks have
- * more than one row tile (pairs); a last one may have one (a single). */
-__device__ __forceinline__ int pair_blocks(int T, int TB) {
-  if (T <= TB) return 0;
-  const int n = T / (2 * TB);
-  return n + (T - n * 2 * TB > TB);
-}
-__device__ __forceinline__ bool has_single(int T, int TB, int pairs) {
-  return T > pairs * 2 * TB; /* else the last pair holds the rest */
-}
-/* Keys that the last token of block j of a sequence sees. */
-__device__ __forceinline__ int block_end(int len, int T, int TB, int j) {
-  return min(len, len - T + min(T, (j + 1) * 2 * TB));
-}
-__device__ __forceinline__ int key_tiles(int begin, int end) {
-  return end > begin ? (end - begin + kTile - 1) / kTile : 0;
-}
-/* An item begins with its fixed cost; tile t then begins t tile costs further on, and
- * belongs to the worker that owns its first place. */
-__device__ __forceinline__ int fixed_cost(int line) { return line ? kSingleItem : kPairItem; }
-__device__ __forceinline__ int tile_cost(int line) { return line ? kSingleTile : kPairTile; }
-__device__ __forceinline__ int item_cost(int line, int tiles) {
-  return tiles ? tiles * tile_cost(line) + fixed_cost(line) : 0;
-}
-/* CTAs that take part.  With kShare places each, every worker whose share lies between an
- * item's first tile and its last has a tile of it: a CTA's 6 places hold one of a pair's
- * tiles, a stream's 3 one of a single's.  (The CTA whose share holds the last pairs may have
- * fewer singles, but those begin with an item's fixed cost: with up to 4 of them no tile, with
- * up to 8 the first tile in stream 1, with 9 or more tiles in both.) */
-__device__ __forceinline__ int active_ctas(int total, int n_cta) {
-  return max(1, min(n_cta, total / kShare));
-}
-/* Where CTA c's share of the line begins. */
-__device__ __forceinline__ int share_begin(int c, int total, int n) {
-  return (int)((unsigned long long)c * (unsigned)total / (unsigned)n);
-}
-/* The CTA that owns place x: the largest c with c total < (x + 1) n.  An estimate in
- * 32 bits is off by less than one. */
-__device__ __forceinline__ int cta_of(int x, int total, int n) {
-  const long long y = ((long long)x + 1) * n;
-  int c = (int)__fdividef((float)y, (float)total);
-  while ((long long)c * total >= y) --c;
-  while (((long long)c + 1) * total < y) ++c;
-  return c;
-}
 /* Last i in [0, n) with a[i] <= x (a not decreasing, a[0] <= x). */
 template <class T>
 __device__ __forceinline__ int find(const T *a, int n, int x) {
@@ -395,19 +347,25 @@ __device__ __forceinline__ int find(const T *a, int n, int x) {
   }
   return lo;
 }
-/* The same by a whole warp: 32 places a round, so one or two loads deep. */
-template <class T>
-__device__ __forceinline__ int warp_find(const T *a, int n, int x) {
+/* The last i in [0, n) that `holds` (it holds for 0 and up to some i), by a whole warp: 32
+ * places a round, so one or two rounds in most cases. */
+template <class F>
+__device__ __forceinline__ int warp_last(int n, F holds) {
   const int lane = threadIdx.x & 31;
-  int lo = 0, len = n; /* the answer is in [lo, lo + len) */
-  while (len > 1) {
-    const int step = (len + 31) >> 5, i = lane * step;
-    const unsigned le = __ballot_sync(0xffffffffu, i < len && (int)a[lo + i] <= x);
-    const int k = 31 - __clz(le | 1u);
+  int lo = 0;
+  while (n > 1) {
+    const int step = (n + 31) >> 5, i = lane * step;
+    const unsigned yes = __ballot_sync(0xffffffffu, i < n && holds(lo + i));
+    const int k = 31 - __clz(yes | 1u);
     lo += k * step;
-    len = min(step, len - k * step);
+    n = min(step, n - k * step);
   }
   return lo;
+}
+/* find by a whole warp. */
+template <class T>
+__device__ __forceinline__ int warp_find(const T *a, int n, int x) {
+  return warp_last(n, [&](int i) { return (int)a[i] <= x; });
 }
 
 /* A group's shared keys: whole pages that every one of its sequences with something
@@ -488,9 +446,8 @@ __device__ bool take_cut(const Args &a, Smem *sm) {
       const int T = sm->off[i + 1] - sm->off[i], len = sm->len[i];
       const int start = ng ? shared_keys(a, sm, find(sm->gs, ng + 1, i)) : 0;
       const int nb = pair_blocks(T, TB);
-      int pairs = 0, singles = 0;
-#pragma unroll 1
-      for (int j = 0; j < nb; ++j) pairs += item_cost(0, key_tiles(start, block_end(len, T, TB, j)));
+      const int pairs = nb ? pairs_before(start, len, T, TB, nb) : 0;
+      int singles = 0;
       if (has_single(T, TB, nb)) singles = item_cost(1, key_tiles(start, block_end(len, T, TB, nb)));
       vs = two(pairs * a.Hkv, singles * a.Hkv);
     }
@@ -574,23 +531,21 @@ __device__ __forceinline__ Piece next_piece(const Args &a, const Smem *sm, int l
     const int per = (sm->cum_s[line][b + 1] - sm->cum_s[line][b]) / a.Hkv;
     p.kvh = (x - begin) / per;
     begin += p.kvh * per;
-#pragma unroll 1
-    for (j = line == 0 ? 0 : pair_blocks(T, TB);; ++j) {
-      p.kend = block_end(len, T, TB, j);
-      p.nt = key_tiles(p.key0, p.kend);
-      const int cost = item_cost(line, p.nt);
-      if (x < begin + cost) break;
-      begin += cost;
+    const int nb = pair_blocks(T, TB);
+    j = nb;
+    if (line == 0) {
+      j = warp_last(nb, [&](int i) { return pairs_before(p.key0, len, T, TB, i) <= x - begin; });
+      begin += pairs_before(p.key0, len, T, TB, j);
     }
+    p.kend = block_end(len, T, TB, j);
+    p.nt = key_tiles(p.key0, p.kend);
   }
   p.tok0 = first + j * 2 * TB;
   p.ntok = min(2 * TB, T - j * 2 * TB);
-  const int tile = tile_cost(line), at = begin + fixed_cost(line);
-  p.t0 = line ? (max(0, x - at) + kSingleTile - 1) / kSingleTile : (max(0, x - at) + kPairTile - 1) / kPairTile;
-  const int t1 = line ? (max(0, end - at) + kSingleTile - 1) / kSingleTile
-                      : (max(0, end - at) + kPairTile - 1) / kPairTile;
-  p.n = max(0, min(p.nt, t1) - p.t0);
-  x = min(end, at + p.nt * tile);
+  const Range r = piece_range(line, begin, p.nt, x, end);
+  p.t0 = r.t0;
+  p.n = r.n;
+  x = r.next;
   p.begin = begin;
   return p;
 }
@@ -602,14 +557,8 @@ __device__ __forceinline__ void tell_merge(const Args &a, const Smem *sm, const 
   int w[2];
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) { /* the workers of the item's first tile and its last */
-    const int x = p.begin + fixed_cost(p.line) + (k ? (p.nt - 1) * tile_cost(p.line) : 0) +
-                  (p.line ? pairs : 0);
-    const int c = cta_of(x, total, n);
-    w[k] = c;
-    if (p.line) {
-      const int s0 = max(share_begin(c, total, n), pairs), s1 = share_begin(c + 1, total, n);
-      w[k] = 2 * c + (x - pairs >= ((s0 + s1 - 2 * pairs + 1) >> 1));
-    }
+    const int x = p.begin + fixed_cost(p.line) + (k ? (p.nt - 1) * tile_cost(p.line) : 0);
+    w[k] = worker_of(p.line, x, total, pairs, n);
   }
   const bool whole = p.own && p.key0 == 0 && p.n == p.nt;
   const int pieces = w[1] - w[0] + 1;
@@ -780,12 +729,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (sound) {
         const int total = sm->total, pairs = sm->pairs, n = active_ctas(total, gridDim.x);
         if ((int)blockIdx.x < n) {
-          const int lo = share_begin(blockIdx.x, total, n), hi = share_begin(blockIdx.x + 1, total, n);
-          x = min(lo, pairs);
-          end = min(hi, pairs);
-          const int s0 = max(lo, pairs) - pairs, s1 = max(hi, pairs) - pairs, mid = (s0 + s1 + 1) >> 1;
-          x1 = s ? mid : s0;
-          end1 = s ? s1 : mid;
+          const Share mine = share_of(blockIdx.x, s, total, pairs, n);
+          x = mine.x;
+          end = mine.end;
+          x1 = mine.x1;
+          end1 = mine.end1;
         }
       }
       uint32_t armed_k = 0, armed_v = 0; /* parities of each slot's next use */
