@@ -576,11 +576,14 @@ namespace {
 
 template <int OP>
 cudaError_t launch_plan(const mk_kv *kv, const Params &p) {
-  /* 8 CTAs of 512 threads, measured against one CTA (12 us for a small fork, one CTA 15) and
-   * against the largest cluster of 1024 threads, which takes the calls with more table
-   * entries than 512 warps hold 128 of (64 forks of 16384 tokens: 45 us, with it 29). */
+  /* 8 CTAs of 512 threads, or the largest cluster (16 CTAs) of 1024, which begins later and
+   * has four times the warps for the rows' segments and the pages.  Both times, a fork of n
+   * rows of 30 entries and their release: 128 rows over 4036 pages 20.9 and 26.3 us, 256 over
+   * 8004 27.3 and 26.2, 384 over 11972 34.5 and 27.2; 16 rows of 1000 over 18024 25.5 and
+   * 27.3, 32 over 34040 35.9 and 29.0; 4 rows of 8 over 16384 pages 23.0 and 24.4, over 32768
+   * 27.1 and 25.7, over 65536 35.1 and 27.7. */
   const long long segs = (p.max_pages + kSeg - 1) / kSeg * (long long)(OP == OP_COMPACT ? p.n_seqs : p.n);
-  const bool large = segs > 256 || p.num_pages > 65536;
+  const bool large = OP == OP_COPY || segs + p.num_pages / 128 > 288;
   const int ctas = large ? kv->max_cluster : std::min(8, kv->max_cluster);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas);
