@@ -152,6 +152,8 @@ class PrefixAttention:
                  scale: float = None, stream=None):
         import torch
 
+        if scale is not None and not ctypes.c_float(scale).value > 0.0:
+            raise ValueError("scale has to be positive, in 32 bits")
         layers = [tuple(kv) for kv in layers]
         if not layers:
             raise ValueError("no layers")
@@ -164,8 +166,6 @@ class PrefixAttention:
                                      f"[{head_dim}]")
         if dev.type != "cuda":
             raise ValueError("the caches have to be CUDA tensors")
-        if scale is not None and not scale > 0.0:
-            raise ValueError("scale has to be positive")
         self.handle = None
         self.device, self.layers, self.max_tokens = dev, layers, max_tokens
         self.heads, self.head_dim = n_q_heads, head_dim

@@ -26,3 +26,11 @@ def test_read_refuses_rows_that_are_not_there(rows):
         c.read(rows)
     lens, tables = c.read([2, 0, 2])
     assert lens.tolist() == [7, 5, 7] and np.array_equal(tables, [[2], [0], [2]])
+
+
+@pytest.mark.parametrize("scale", [1e-50, 0.0, -1.0, float("nan")])
+def test_scales_that_are_no_positive_float_are_refused(scale):
+    """1e-50 is 0 in 32 bits, which the library takes for 1 / sqrt(head_dim)."""
+    pool = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="scale"):
+        mk.PrefixAttention(1, 1, 64, 16, [(pool, pool)], max_tokens=1, scale=scale)
