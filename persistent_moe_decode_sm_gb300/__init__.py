@@ -381,6 +381,8 @@ class Decoder:
         the cache was grown by the token of the next step."""
         if cache.max_pages_per_seq != self.cdims.max_pages_per_seq:
             raise ValueError("the cache's table rows have another width than this decoder's")
+        if cache.page_size != self.cdims.page_size:
+            raise ValueError("the cache has another page size than this decoder")
         lens, tables = cache.read(seqs)
         self.build_schedule(lens - 1 if seq_lens is None else seq_lens, tables)
 

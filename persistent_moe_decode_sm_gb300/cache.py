@@ -69,6 +69,7 @@ class KvCache:
         self.pools, self.page_tables = pools, page_tables
         self.seq_lens, self.page_refs = seq_lens, page_refs
         self.n_seqs, self.max_pages_per_seq = page_tables.shape
+        self.page_size = page_size
         ptrs = (ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools])
         desc = mk_kv_desc(len(pools), shape[0], page_size, self.n_seqs, self.max_pages_per_seq,
                           page_bytes, ptrs, page_tables.data_ptr(), seq_lens.data_ptr(),

@@ -34,3 +34,17 @@ def test_scales_that_are_no_positive_float_are_refused(scale):
     pool = torch.zeros(2, 1, 16, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="scale"):
         mk.PrefixAttention(1, 1, 64, 16, [(pool, pool)], max_tokens=1, scale=scale)
+
+
+def test_a_schedule_over_another_page_size_is_refused():
+    """A decoder of 16 tokens a page would read the rows of pages of 32 as its own."""
+    dec = mk.Decoder.__new__(mk.Decoder)
+    dec.ctx = None
+    dec.cdims = mk.make_dims(2, 64, 4, 2, 64, 8, 2, 64, 64, 16, 4, 8, 1)
+    dec.build_schedule = lambda lens, tables: None
+    c = cache_of([5, 6, 7], [[0], [1], [2]])
+    c.page_size = 16
+    dec.schedule_cache(c, [0])
+    c.page_size = 32
+    with pytest.raises(ValueError, match="page size"):
+        dec.schedule_cache(c, [0])
