@@ -219,7 +219,7 @@ class PrefixAttention:
         have a token stride of its own (the q part of a fused projection)."""
         rows = (batch.n_tokens, self.heads, self.head_dim)
         if (q.shape != rows or q.dtype is not self._bf16 or q.get_device() != self._index
-                or q.stride(2) != 1 or q.stride(1) != self.head_dim):
+                or q.stride(2) != 1 or (self.heads > 1 and q.stride(1) != self.head_dim)):
             raise ValueError(f"q has to be bfloat16 {rows} with contiguous heads on {self.device}")
         # the quick look first: a call takes some tens of microseconds
         if not (out.dtype is self._bf16 and out.get_device() == self._index

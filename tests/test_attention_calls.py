@@ -123,3 +123,13 @@ def test_behind_page_calls_without_a_wait():
     for out, lse in outs:
         c.check((out.double().cpu().numpy(), lse.double().cpu().numpy()), want)
     assert int((holders[:int((refs > 0).sum())] > 0).sum()) == int((refs > 0).sum())
+
+
+@gpu
+def test_one_head_may_have_any_head_stride():
+    c = Case([(32, [(5, 1), (8, 1), (40, 1)])], (1, 1, 64))
+    t = c.t
+    wide = t.zeros(3, 200, dtype=t.bfloat16, device="cuda")
+    q = wide.as_strided((3, 1, 64), (200, 7, 1))
+    q.copy_(c.q)
+    c.check(c.run(c.device(q=q)))
