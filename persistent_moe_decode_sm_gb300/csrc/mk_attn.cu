@@ -649,14 +649,14 @@ struct Loader {
 };
 
 /* o_r = sum_j p_rj v_j, l_r = sum_j p_rj, p_rj = 2^(c q_r.k_j - m_r) over a piece's tiles of
- * 128 keys.  Of one tile the tensor cores have 512 cycles for S = Q K^T and 512 for O += P V,
- * a row tile's 4 warps 550 for the exponentials and 1800 in all, and 64 KB of K and V take
+ * 128 keys.  Of one tile the tensor cores have 512 cycles for S = Q K^T and 1024 for O += P V,
+ * a row tile's 4 warps 550 for the exponentials and 2000 in all, and 64 KB of K and V take
  * an SM 2800 at its share of HBM.  So singles are bound by HBM where the cache is not in L2
- * (16 sequences in two groups over 131072 and 32768 shared keys, 352 MB: 63 of 77 us in this
- * kernel, 5.6 TB/s), pairs by the chain S, P, O of a stream, of which the other stream hides
- * a part (4800 tokens of 32 heads over 32768 keys: 1.95 ms, 1.33 PFLOP/s, tensor cores 65 %
- * active), and small calls by their first instructions: the cut, 2.6 us, the first tile 6 us
- * after the start. */
+ * (16 sequences in two groups over 131072 and 32768 shared keys, 352 MB: 80 us with the join,
+ * 4.4 TB/s), pairs by the chain S, P, O of a stream, of which the other stream hides a part
+ * (4800 tokens of 32 heads over 32768 keys: 2.8 ms, 0.92 PFLOP/s and half as much again for
+ * the second product of P, tensor cores 76 % active), and small calls by their first
+ * instructions: the cut, 2.6 us, the first tile 6 us after the start. */
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -913,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (pair && it + s > 0) {
           /* The streams of a pair take turns, stream 0's tile before stream 1's: side by
            * side they would share the exponential unit and then leave it, and the tensor
-           * cores, idle together. */
+           * cores, idle together (4800 tokens over 32768 keys: 3.27 ms, so 2.89). */
           ok = warp_wait(&sm->turn[s], (it - 1 + s) & 1, stop);
           if (!ok) break;
         }
@@ -989,9 +989,9 @@ __global__ void __launch_bounds__(kThreads, 1)
          * store lands while the next is computed.  P goes into the product as a bf16 value and
          * the bf16 rounding of what that leaves, so it is good to 2^-17, as in the decode step
          * (bf16 alone moves a result by about as much as the result's own rounding does).  The
-         * second product and its operand cost 64 samples of one prompt a fifth (36 us, with
-         * them 44), 16 sequences over long prefixes 8 % (75, 80), 4800 tokens over 32768 keys
-         * a third (2.12 ms, 2.85). */
+         * second product and its operand cost 64 samples of one prompt 13 % (36 us, with them
+         * 41), 16 sequences over long prefixes 7 % (75, 80), 4800 tokens over 32768 keys a third
+         * (2.12 ms, 2.83). */
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           uint32_t w[16], rest[16];
