@@ -1,7 +1,8 @@
 /*
  * mk_cache.h -- C ABI for the paged KV cache around the decode step: who holds
- * which page (fork, resize, compact, copy) and attention that reads the pages
- * several sequences share once for all of them.
+ * which page (fork, resize, compact, copy), attention that reads the pages
+ * several sequences share once for all of them, and keys and values of many
+ * tokens (prompts, drafts) normed, rotated and appended to the pages.
  *
  * The pools, page tables and lengths are those of mk.h: per layer and for K
  * and V a pool [num_pages][n_kv_heads][page_size][head_dim] in bf16, one table
@@ -189,6 +190,69 @@ mk_status mk_attn_set_wait_limit_ns(mk_attn *attn, uint64_t ns);
 /* Test only: in the next call every SM waits for something that never comes, so
  * that the way out of such a wait can be tested without a hang. */
 mk_status mk_attn_debug_poison_wait(mk_attn *attn);
+
+/* ---- appending keys and values ----------------------------------------------
+ *
+ * What the decode step does for its own token, for any number of tokens of each
+ * sequence: heads of q and k are normed (optional) and turned to their position,
+ * and K and V written to the sequences' pages, in one pass. */
+
+typedef struct {
+  int32_t n_q_heads, n_kv_heads, head_dim;   /* n_q_heads 0: keys and values only */
+  int32_t page_size, num_pages;              /* head_dim 32, 64 or 128; page_size from 1 */
+  int32_t rotary_dim;                        /* the head's first dims turn: even, 0 to head_dim */
+  int32_t interleaved;                       /* pairs (2i, 2i + 1); 0: (i, i + rotary_dim / 2) */
+  int32_t n_layers;
+  void *const *k_caches, *const *v_caches;   /* HOST arrays [n_layers] of DEVICE pools */
+  const double *frequencies;                 /* HOST [rotary_dim / 2], radians a position (copied), or
+                                              * NULL: rope_base^(-2i / rotary_dim) */
+  float rope_base;                           /* above 0 where it is used */
+  float magnitude;                           /* of cos and sin, above 0; 0: 1 */
+  float norm_eps;                            /* 0 or above */
+} mk_append_desc;
+
+typedef struct mk_append mk_append;
+
+/* Allocates the workspace: 8 bytes for each pair of rotary dims and an error word.
+ * MK_ERR_INVALID_ARG / MK_ERR_UNSUPPORTED / MK_ERR_NO_DEVICE / MK_ERR_CUDA. */
+mk_status mk_append_create(const mk_append_desc *desc, void *stream, mk_append **out);
+void mk_append_destroy(mk_append *app);
+
+/* Rows of a call: bf16 [n_tokens][heads][head_dim] with heads contiguous and `stride`
+ * elements from a token to the next (a multiple of 8; q, k and v may lie side by side
+ * in one tensor), 16-byte aligned. */
+typedef struct {
+  const void *q;              /* or NULL, with q_out: keys and values only */
+  const void *k, *v;
+  void *q_out;                /* may be q itself with q's stride: in place */
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const void *q_norm, *k_norm; /* bf16 [head_dim] gains, or NULL: no norm */
+  const int32_t *positions;   /* DEVICE [n_tokens] that the heads turn to, 0 or above (drafted trees: by
+                               * depth), or NULL: each token's place in its sequence */
+} mk_append_rows;
+
+/* Appends the batch's tokens in layer `layer` (groups and prefix_lens are not looked at).
+ * With T tokens and length L (the tokens among them: resize first), token t of a
+ * sequence goes to place L - T + t of its table row; a token whose place is below 0
+ * (T > L: a padded row) is left out, and so are rows behind the last sequence's tokens:
+ * neither the cache nor q_out is written for them.
+ *   norm:  x_i <- gain_i x_i / sqrt(mean(x^2) + norm_eps), over the whole head
+ *   turn:  (a, b) <- magnitude (a cos - b sin, b cos + a sin), angle position * frequency
+ * in fp32, rounded to bf16 once; the angle is taken in 64-bit fixed point, good to 2^-24
+ * for every position.  v is copied.  Two tokens with the same place race: pages that
+ * tokens go to belong to one sequence (mk_kv_resize sees to it).  q_out overlaps nothing
+ * else, k and v do not overlap the pools; n_seqs at most 1024.
+ *
+ * A wrong DEVICE argument (offsets or lengths that are out of order or out of range:
+ * nothing is written; a page id out of range: that token's K and V are not written; a
+ * negative position: that token is left out) is reported by mk_append_sync, once. */
+mk_status mk_append_tokens(mk_append *app, int32_t layer, const mk_attn_batch *batch,
+                           const mk_append_rows *rows);
+
+/* Waits for the stream and returns the first device error since the last
+ * mk_append_sync (MK_OK if none); clears it.  MK_ERR_INVALID_ARG while the stream
+ * is being captured. */
+mk_status mk_append_sync(mk_append *app);
 
 #ifdef __cplusplus
 }

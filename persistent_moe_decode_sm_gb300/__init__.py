@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(BUILD, "libmk.so")
 
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 SOURCES = ["mk_kernel.cu", "mk_api.cpp", "mk_schedule.cpp", "mk_noalloc.cu", "mk_kv.cu",
-           "mk_attn.cu"]
+           "mk_attn.cu", "mk_append.cu"]
 
 MK_OK = 0
 STATUS_NAMES = {0: "MK_OK", 1: "MK_ERR_INVALID_ARG", 2: "MK_ERR_BATCH", 3: "MK_ERR_PAGE_OOB",
@@ -128,6 +128,22 @@ class mk_attn_batch(ctypes.Structure):
         ("page_tables", "seq_lens", "q_offsets", "group_starts", "prefix_lens")]
 
 
+class mk_append_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_q_heads", "n_kv_heads", "head_dim", "page_size", "num_pages", "rotary_dim",
+                 "interleaved", "n_layers")] + [
+                    ("k_caches", ctypes.POINTER(ctypes.c_void_p)),
+                    ("v_caches", ctypes.POINTER(ctypes.c_void_p)),
+                    ("frequencies", ctypes.POINTER(ctypes.c_double))] + [
+                        (n, ctypes.c_float) for n in ("rope_base", "magnitude", "norm_eps")]
+
+
+class mk_append_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k", "v", "q_out")] + [
+        (n, ctypes.c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")] + [
+            (n, ctypes.c_void_p) for n in ("q_norm", "k_norm", "positions")]
+
+
 EXPORTS = ["mk_create", "mk_build_schedule", "mk_decode_step", "mk_sync", "mk_destroy",
            "mk_status_string", "mk_set_wait_limit_ns", "mk_debug_routing", "mk_debug_dump",
            "mk_get_stats", "mk_debug_poison_wait", "mk_plan", "mk_decode_step_static",
@@ -135,8 +151,10 @@ EXPORTS = ["mk_create", "mk_build_schedule", "mk_decode_step", "mk_sync", "mk_de
            "mk_kv_create", "mk_kv_destroy", "mk_kv_copy_pages", "mk_kv_fork", "mk_kv_resize",
            "mk_kv_compact", "mk_kv_sync",
            "mk_attn_create", "mk_attn_destroy", "mk_prefix_attention", "mk_attn_sync",
-           "mk_attn_set_wait_limit_ns", "mk_attn_debug_poison_wait"]
-_NO_STATUS = ("mk_destroy", "mk_status_string", "mk_kv_destroy", "mk_attn_destroy")
+           "mk_attn_set_wait_limit_ns", "mk_attn_debug_poison_wait",
+           "mk_append_create", "mk_append_destroy", "mk_append_tokens", "mk_append_sync"]
+_NO_STATUS = ("mk_destroy", "mk_status_string", "mk_kv_destroy", "mk_attn_destroy",
+              "mk_append_destroy")
 
 _lib = None
 
@@ -185,6 +203,12 @@ def lib():
         L.mk_attn_sync.argtypes = [vp]
         L.mk_attn_set_wait_limit_ns.argtypes = [vp, u64]
         L.mk_attn_debug_poison_wait.argtypes = [vp]
+        L.mk_append_create.argtypes = [ctypes.POINTER(mk_append_desc), vp, ctypes.POINTER(vp)]
+        L.mk_append_destroy.argtypes = [vp]
+        L.mk_append_destroy.restype = None
+        L.mk_append_tokens.argtypes = [vp, i32, ctypes.POINTER(mk_attn_batch),
+                                       ctypes.POINTER(mk_append_rows)]
+        L.mk_append_sync.argtypes = [vp]
         for n in EXPORTS:
             if n not in _NO_STATUS:
                 getattr(L, n).restype = i32
@@ -434,4 +458,4 @@ class Decoder:
             pass
 
 
-from .cache import KvCache, PrefixAttention  # noqa: E402  (needs the functions above)
+from .cache import (KvAppend, KvCache, PrefixAttention, rope_frequencies)  # noqa: E402  (needs the functions above)

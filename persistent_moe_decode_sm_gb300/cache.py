@@ -8,8 +8,10 @@ two and keeps a call's tensors until the stream has passed it.
 from __future__ import annotations
 
 import ctypes
+import math
 
-from . import _addr, _check, lib, mk_attn_batch, mk_attn_desc, mk_kv_desc
+from . import (_addr, _check, lib, mk_append_desc, mk_append_rows, mk_attn_batch, mk_attn_desc,
+               mk_kv_desc)
 
 
 def _stream(stream, device):
@@ -34,6 +36,54 @@ def _want(t, what, dtype, device, ndim=None):
         raise ValueError(f"{what} has to be contiguous"
                          + (f" with {ndim} dimensions" if ndim is not None else ""))
     return t
+
+
+def _batch(device, page_tables, seq_lens, q_offsets, group_starts, prefix_lens, n_tokens):
+    _want(page_tables, "page_tables", "int32", device, 2)
+    _want(seq_lens, "seq_lens", "int32", device, 1)
+    n = seq_lens.numel()
+    if page_tables.shape[0] != n:
+        raise ValueError("seq_lens has an entry for each table row")
+    if (group_starts is None) != (prefix_lens is None):
+        raise ValueError("group_starts and prefix_lens come together")
+    groups = 0
+    if group_starts is not None:
+        _want(group_starts, "group_starts", "int32", device, 1)
+        _want(prefix_lens, "prefix_lens", "int32", device, 1)
+        groups = prefix_lens.numel()
+        if group_starts.numel() != groups + 1:
+            raise ValueError("group_starts has one entry more than prefix_lens")
+    if q_offsets is not None:
+        _want(q_offsets, "q_offsets", "int32", device, 1)
+        if q_offsets.numel() != n + 1:
+            raise ValueError("q_offsets has one entry more than there are sequences")
+    if n_tokens is None:
+        n_tokens = n
+    b = mk_attn_batch(n, n_tokens, groups, page_tables.shape[1], page_tables.data_ptr(), seq_lens.data_ptr(),
+                      _addr(q_offsets), _addr(group_starts), _addr(prefix_lens))
+    b.keep = (page_tables, seq_lens, q_offsets, group_starts, prefix_lens)
+    return b
+
+
+def _layers(layers, n_kv_heads, page_size, head_dim):
+    """(the (k_cache, v_cache) tensors of each layer, checked; device; pages)."""
+    layers = [tuple(kv) for kv in layers]
+    if not layers:
+        raise ValueError("no layers")
+    dev, pages = layers[0][0].device, layers[0][0].shape[0]
+    for k, v in layers:
+        for t, what in ((k, "k_cache"), (v, "v_cache")):
+            _want(t, what, "bfloat16", dev)
+            if t.numel() != pages * n_kv_heads * page_size * head_dim:
+                raise ValueError(f"{what} is not [{pages}][{n_kv_heads}][{page_size}]"
+                                 f"[{head_dim}]")
+    if dev.type != "cuda":
+        raise ValueError("the caches have to be CUDA tensors")
+    return layers, dev, pages
+
+
+def _pointers(tensors):
+    return (ctypes.c_void_p * len(tensors))(*[t.data_ptr() for t in tensors])
 
 
 class KvCache:
@@ -155,26 +205,14 @@ class PrefixAttention:
 
         if scale is not None and not ctypes.c_float(scale).value > 0.0:
             raise ValueError("scale has to be positive, in 32 bits")
-        layers = [tuple(kv) for kv in layers]
-        if not layers:
-            raise ValueError("no layers")
-        dev, pages = layers[0][0].device, layers[0][0].shape[0]
-        for k, v in layers:
-            for t, what in ((k, "k_cache"), (v, "v_cache")):
-                _want(t, what, "bfloat16", dev)
-                if t.numel() != pages * n_kv_heads * page_size * head_dim:
-                    raise ValueError(f"{what} is not [{pages}][{n_kv_heads}][{page_size}]"
-                                     f"[{head_dim}]")
-        if dev.type != "cuda":
-            raise ValueError("the caches have to be CUDA tensors")
+        layers, dev, pages = _layers(layers, n_kv_heads, page_size, head_dim)
         self.handle = None
         self.device, self.layers, self.max_tokens = dev, layers, max_tokens
         self.heads, self.head_dim = n_q_heads, head_dim
         self._index, self._bf16, self._f32 = layers[0][0].get_device(), torch.bfloat16, torch.float32
         self._lib = lib()
         n = len(layers)
-        ks = (ctypes.c_void_p * n)(*[k.data_ptr() for k, _ in layers])
-        vs = (ctypes.c_void_p * n)(*[v.data_ptr() for _, v in layers])
+        ks, vs = _pointers([k for k, _ in layers]), _pointers([v for _, v in layers])
         desc = mk_attn_desc(n_q_heads, n_kv_heads, head_dim, page_size, pages, max_tokens,
                             max_seqs, max_groups, n, ks, vs, scale or 0.0)
         h = ctypes.c_void_p()
@@ -188,30 +226,10 @@ class PrefixAttention:
         """The batch of a call, to be kept as long as its tensors stay in place (their
         contents may change between calls).  q_offsets None: one query token each.
         n_tokens: rows of q and out; None: with q_offsets max_tokens, else one each."""
-        _want(page_tables, "page_tables", "int32", self.device, 2)
-        _want(seq_lens, "seq_lens", "int32", self.device, 1)
-        n = seq_lens.numel()
-        if page_tables.shape[0] != n:
-            raise ValueError("seq_lens has an entry for each table row")
-        if (group_starts is None) != (prefix_lens is None):
-            raise ValueError("group_starts and prefix_lens come together")
-        groups = 0
-        if group_starts is not None:
-            _want(group_starts, "group_starts", "int32", self.device, 1)
-            _want(prefix_lens, "prefix_lens", "int32", self.device, 1)
-            groups = prefix_lens.numel()
-            if group_starts.numel() != groups + 1:
-                raise ValueError("group_starts has one entry more than prefix_lens")
-        if q_offsets is not None:
-            _want(q_offsets, "q_offsets", "int32", self.device, 1)
-            if q_offsets.numel() != n + 1:
-                raise ValueError("q_offsets has one entry more than there are sequences")
-        if n_tokens is None:
-            n_tokens = n if q_offsets is None else self.max_tokens
-        b = mk_attn_batch(n, n_tokens, groups, page_tables.shape[1], page_tables.data_ptr(), seq_lens.data_ptr(),
-                          _addr(q_offsets), _addr(group_starts), _addr(prefix_lens))
-        b.keep = (page_tables, seq_lens, q_offsets, group_starts, prefix_lens)
-        return b
+        if n_tokens is None and q_offsets is not None:
+            n_tokens = self.max_tokens
+        return _batch(self.device, page_tables, seq_lens, q_offsets, group_starts, prefix_lens,
+                      n_tokens)
 
     def run(self, layer: int, batch, q, out, lse=None):
         """out [n_tokens][n_q_heads][head_dim] = attention of q over the layer's pools;
@@ -250,6 +268,151 @@ class PrefixAttention:
     def close(self):
         if self.handle:
             self._lib.mk_attn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = None,
+                     factor: float = 1.0, old_context: int = None, low: float = 1.0,
+                     high: float = 4.0):
+    """Turning rates of rotary_dim / 2 pairs in radians a position, for KvAppend, of a context that
+    is `factor` times as long as the one a model was trained with.
+
+    scaling None: base ** (-2 i / rotary_dim).  "linear": those over factor.  "base": of a base
+    grown by factor ** (rotary_dim / (rotary_dim - 2)), so that the slowest pair turns 1 / factor
+    as fast and the fastest as before.  "parts": pairs that turn at least `high` times over
+    old_context keep their rate, those that turn at most `low` times take it over factor, those
+    between a blend that is linear in their turns."""
+    if rotary_dim < 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim has to be even")
+    if not (base > 0.0 and factor > 0.0):
+        raise ValueError("base and factor have to be positive")
+    if scaling == "base":
+        if rotary_dim < 4:
+            raise ValueError("scaling of the base takes two pairs at least")
+        base *= factor ** (rotary_dim / (rotary_dim - 2))
+    rates = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    if scaling in (None, "base"):
+        return rates
+    if scaling == "linear":
+        return [f / factor for f in rates]
+    if scaling != "parts":
+        raise ValueError(f"scaling is None, 'linear', 'base' or 'parts', not {scaling!r}")
+    if old_context is None or not low < high:
+        raise ValueError("scaling by parts takes old_context, and low below high")
+
+    def part(f):
+        kept = min(1.0, max(0.0, (old_context * f / (2.0 * math.pi) - low) / (high - low)))
+        return f * kept + f / factor * (1.0 - kept)
+
+    return [part(f) for f in rates]
+
+
+class KvAppend:
+    """Norms and rotates the heads of a batch's tokens and appends their keys and values to the
+    pages: prompts, drafted tokens, or single tokens.
+
+    layers: (k_cache, v_cache) of each layer as for PrefixAttention.  rotary_dim: the head's first
+    dims that turn (None: all).  interleaved: pairs are neighbours, else halves.  frequencies:
+    radians a position of each pair (see rope_frequencies), None: of rope_base.  magnitude: of
+    the cosines and sines."""
+
+    def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, layers,
+                 rotary_dim: int = None, interleaved: bool = False, rope_base: float = 10000.0,
+                 frequencies=None, magnitude: float = 1.0, norm_eps: float = 1e-6, stream=None):
+        import torch
+
+        rotary_dim = head_dim if rotary_dim is None else rotary_dim
+        if not ctypes.c_float(magnitude).value > 0.0:
+            raise ValueError("magnitude has to be positive, in 32 bits")
+        rates = None
+        if frequencies is not None:
+            rates = [float(f) for f in frequencies]
+            if len(rates) != rotary_dim // 2:
+                raise ValueError(f"frequencies has {len(rates)} entries for {rotary_dim // 2} pairs")
+            rates = (ctypes.c_double * max(1, len(rates)))(*rates)
+        layers, dev, pages = _layers(layers, n_kv_heads, page_size, head_dim)
+        self.handle = None
+        self.device, self.layers = dev, layers
+        self.heads, self.kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
+        self._index, self._bf16 = layers[0][0].get_device(), torch.bfloat16
+        self._int32 = torch.int32
+        self._lib, self._rows = lib(), mk_append_rows()
+        desc = mk_append_desc(n_q_heads, n_kv_heads, head_dim, page_size, pages, rotary_dim,
+                              int(bool(interleaved)), len(layers),
+                              _pointers([k for k, _ in layers]), _pointers([v for _, v in layers]),
+                              rates, rope_base, magnitude, norm_eps)
+        h = ctypes.c_void_p()
+        with torch.cuda.device(dev):
+            _check(self._lib.mk_append_create(ctypes.byref(desc), _stream(stream, dev),
+                                              ctypes.byref(h)), "mk_append_create")
+        self.handle = h.value
+
+    def batch(self, page_tables, seq_lens, q_offsets=None, n_tokens: int = None):
+        """The batch of a call, as PrefixAttention.batch makes it (whose batches run() takes
+        too).  n_tokens: rows of q, k and v; needed with q_offsets."""
+        if q_offsets is not None and n_tokens is None:
+            raise ValueError("n_tokens is needed with q_offsets")
+        return _batch(self.device, page_tables, seq_lens, q_offsets, None, None, n_tokens)
+
+    def _stride(self, t, what, shape):
+        if (t.shape != shape or t.dtype is not self._bf16 or t.get_device() != self._index
+                or t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != self.head_dim)):
+            raise ValueError(f"{what} has to be bfloat16 {tuple(shape)} with contiguous heads on "
+                             f"{self.device}")
+        return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+
+    def _gain(self, t, what):
+        if t is None:
+            return None
+        if not (t.dtype is self._bf16 and t.get_device() == self._index and t.is_contiguous()):
+            _want(t, what, "bfloat16", self.device, 1)
+        if t.shape != (self.head_dim,):
+            raise ValueError(f"{what} has an entry for each of the head's {self.head_dim} dims")
+        return t.data_ptr()
+
+    def run(self, layer: int, batch, k, v, q=None, q_out=None, positions=None, q_norm=None,
+            k_norm=None):
+        """k, v [n_tokens][n_kv_heads][head_dim] go to the layer's pages, q [n_tokens][n_q_heads]
+        [head_dim] to q_out (which may be q itself).  They may have token strides of their own,
+        as parts of a fused projection.  positions (int32 [n_tokens]): what the heads turn to,
+        None: the tokens' places.  q_norm, k_norm: gains of the norm, None: no norm."""
+        rows, n = self._rows, batch.n_tokens
+        if (q is None) != (q_out is None):
+            raise ValueError("q and q_out come together")
+        kv = (n, self.kv_heads, self.head_dim)
+        rows.k_stride, rows.v_stride = self._stride(k, "k", kv), self._stride(v, "v", kv)
+        rows.k, rows.v = k.data_ptr(), v.data_ptr()
+        rows.q = rows.q_out = None
+        if q is not None:
+            shape = (n, self.heads, self.head_dim)
+            rows.q_stride = self._stride(q, "q", shape)
+            rows.q_out_stride = self._stride(q_out, "q_out", shape)
+            rows.q, rows.q_out = q.data_ptr(), q_out.data_ptr()
+        rows.positions = None
+        if positions is not None:
+            if not (positions.dtype is self._int32 and positions.get_device() == self._index
+                    and positions.is_contiguous()):
+                _want(positions, "positions", "int32", self.device, 1)
+            if positions.shape != (n,):
+                raise ValueError("positions has an entry for each token")
+            rows.positions = positions.data_ptr()
+        rows.q_norm, rows.k_norm = self._gain(q_norm, "q_norm"), self._gain(k_norm, "k_norm")
+        _check(self._lib.mk_append_tokens(self.handle, layer, ctypes.byref(batch),
+                                          ctypes.byref(rows)), "mk_append_tokens")
+
+    def sync(self):
+        """Waits for the stream; raises the MkError of the first device error."""
+        _check(self._lib.mk_append_sync(self.handle), "mk_append_sync")
+
+    def close(self):
+        if self.handle:
+            self._lib.mk_append_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
