@@ -175,9 +175,20 @@ void mk_attn_destroy(mk_attn *attn);
 mk_status mk_prefix_attention(mk_attn *attn, int32_t layer, const mk_attn_batch *batch,
                               const void *q, int64_t q_token_stride, void *out, float *lse);
 
+/* The same for drafted trees: of its sequence's T query tokens (the drafted ones, which lie
+ * behind the context in the cache) token t sees those at places u <= t whose bit is set in
+ * its row, bit u % 32 of word u / 32 (itself among them only if its bit is set), and every
+ * key before them.  tree: DEVICE [n_tokens][tree_words], 4-byte aligned, not over out or lse;
+ * T is at most 32 * tree_words (longer: nothing is written, MK_ERR_INVALID_ARG from
+ * mk_attn_sync).  Parents come before their children, so a row is its parent's row and its own
+ * bit.  A token that sees no key at all gets zeros and lse -inf. */
+mk_status mk_tree_attention(mk_attn *attn, int32_t layer, const mk_attn_batch *batch,
+                            const uint32_t *tree, int32_t tree_words, const void *q,
+                            int64_t q_token_stride, void *out, float *lse);
+
 /* Waits for the stream and returns the first device error since the last
  * mk_attn_sync (MK_OK if none); clears it.  MK_ERR_INVALID_ARG while the stream
- * is being captured.  Besides the errors of mk_prefix_attention there is
+ * is being captured.  Besides the errors of the calls there is
  * MK_ERR_DEVICE_TIMEOUT: a wait inside a kernel ran out of time, and that call's
  * results are undefined; later calls are not touched by it. */
 mk_status mk_attn_sync(mk_attn *attn);

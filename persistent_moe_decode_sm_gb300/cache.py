@@ -210,6 +210,7 @@ class PrefixAttention:
         self.device, self.layers, self.max_tokens = dev, layers, max_tokens
         self.heads, self.head_dim = n_q_heads, head_dim
         self._index, self._bf16, self._f32 = layers[0][0].get_device(), torch.bfloat16, torch.float32
+        self._int32 = torch.int32
         self._lib = lib()
         n = len(layers)
         ks, vs = _pointers([k for k, _ in layers]), _pointers([v for _, v in layers])
@@ -231,10 +232,12 @@ class PrefixAttention:
         return _batch(self.device, page_tables, seq_lens, q_offsets, group_starts, prefix_lens,
                       n_tokens)
 
-    def run(self, layer: int, batch, q, out, lse=None):
+    def run(self, layer: int, batch, q, out, lse=None, tree=None):
         """out [n_tokens][n_q_heads][head_dim] = attention of q over the layer's pools;
         lse (fp32 [n_tokens][n_q_heads]) receives the logarithm of the softmax sums.  q may
-        have a token stride of its own (the q part of a fused projection)."""
+        have a token stride of its own (the q part of a fused projection).  tree (int32 [n_tokens]
+        [words], see tree_rows): which of its sequence's query tokens each one sees, a bit for
+        each; None: those before it and itself."""
         rows = (batch.n_tokens, self.heads, self.head_dim)
         if (q.shape != rows or q.dtype is not self._bf16 or q.get_device() != self._index
                 or q.stride(2) != 1 or (self.heads > 1 and q.stride(1) != self.head_dim)):
@@ -251,10 +254,21 @@ class PrefixAttention:
                 _want(lse, "lse", "float32", self.device)
             if lse.shape != rows[:2]:
                 raise ValueError(f"lse has to be {rows[:2]}")
-        _check(self._lib.mk_prefix_attention(
-            self.handle, layer, ctypes.byref(batch), q.data_ptr(),
-            q.stride(0) if rows[0] > 1 else self.heads * self.head_dim, out.data_ptr(),
-            None if lse is None else lse.data_ptr()), "mk_prefix_attention")
+        stride = q.stride(0) if rows[0] > 1 else self.heads * self.head_dim
+        to = None if lse is None else lse.data_ptr()
+        if tree is None:
+            _check(self._lib.mk_prefix_attention(self.handle, layer, ctypes.byref(batch),
+                                                 q.data_ptr(), stride, out.data_ptr(), to),
+                   "mk_prefix_attention")
+            return
+        if not (tree.dtype is self._int32 and tree.get_device() == self._index
+                and tree.dim() == 2 and tree.is_contiguous()):
+            _want(tree, "tree", "int32", self.device, 2)
+        if tree.shape[0] != rows[0]:
+            raise ValueError("tree has a row for each query token")
+        _check(self._lib.mk_tree_attention(self.handle, layer, ctypes.byref(batch),
+                                           tree.data_ptr(), tree.shape[1], q.data_ptr(), stride,
+                                           out.data_ptr(), to), "mk_tree_attention")
 
     def set_wait_limit_ns(self, ns: int):
         """How long a wait inside a kernel of the calls behind this one lasts before the call
@@ -275,6 +289,30 @@ class PrefixAttention:
             self.close()
         except Exception:
             pass
+
+
+def tree_rows(parents):
+    """(tree, depths) of drafted trees, on the host, for PrefixAttention.run and, added to the
+    context's length, for KvAppend's positions.  parents: for each sequence its tokens' parents,
+    numbers of earlier tokens of the same sequence, -1 for a token that follows the context.
+    tree: int32 [tokens][words], each token's ancestors and itself; depths: int32 [tokens]."""
+    import numpy as np
+    import torch
+
+    words = max([1] + [-(-len(p) // 32) for p in parents])
+    rows = np.zeros((sum(len(p) for p in parents), 4 * words), np.uint8)
+    depths = np.zeros(len(rows), np.int32)
+    first = 0
+    for tokens in parents:
+        for i, p in enumerate(tokens):
+            if not -1 <= p < i:
+                raise ValueError(f"token {i} has parent {p}: parents come before their children")
+            if p >= 0:
+                rows[first + i] = rows[first + p]
+                depths[first + i] = depths[first + p] + 1
+            rows[first + i, i // 8] |= 1 << i % 8
+        first += len(tokens)
+    return torch.from_numpy(rows.view("<i4")), torch.from_numpy(depths)
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = None,

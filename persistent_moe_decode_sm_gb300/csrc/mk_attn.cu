@@ -54,6 +54,8 @@ struct Args {
   __nv_bfloat16 *out;
   float *lse;
   float scale_log2; /* scale * log2(e) */
+  const uint32_t *tree; /* [n_tokens][tree_words] bits of the sequence's tokens that a token sees, or NULL */
+  int32_t tree_words, max_query; /* max_query: tokens of a sequence */
   int32_t TB;       /* query tokens of a row tile: 128 / G */
   uint32_t inv_g;   /* ceil(2^16 / G): r * inv_g >> 16 is r / G for r < 128 */
   unsigned long long inv_p; /* ceil(2^38 / P): k * inv_p >> 38 is k / P for k < 2^30 */
@@ -404,7 +406,7 @@ __device__ bool take_cut(const Args &a, Smem *sm) {
       }
     }
     if (i < ns) {
-      bad |= l < 0 || l > (long long)a.max_pages * a.P || o1 < o;
+      bad |= l < 0 || l > (long long)a.max_pages * a.P || o1 < o || o1 - o > a.max_query;
       sm->len[i] = l;
     }
     if (i <= ns) {
@@ -571,6 +573,19 @@ __device__ __forceinline__ void tell_merge(const Args &a, const Smem *sm, const 
   }
 }
 
+/* Word i of what query token `tok` of a tree sees of its sequence's tokens; of the keys before
+ * them (i < 0) it sees all. */
+__device__ __forceinline__ uint32_t tree_word(const Args &a, int tok, int i) {
+  if (i < 0) return 0xffffffffu;
+  return i < a.tree_words ? __ldcg(a.tree + (size_t)tok * a.tree_words + i) : 0;
+}
+/* The 32 keys from `key` on as bits, from the two words that hold them; none from `limit` on. */
+__device__ __forceinline__ uint32_t tree_keys(uint32_t lo, uint32_t hi, int key, int base, int limit) {
+  const uint32_t w = __funnelshift_r(lo, hi, (key - base) & 31);
+  const int d = limit - key;
+  return d >= 32 ? w : d <= 0 ? 0 : w & ((1u << d) - 1);
+}
+
 /* ---- the tiles ---------------------------------------------------------------- */
 
 /* S = Q K^T of a tile; half h of O (+)= P V: P's keys 64 h .. 64 h + 63, and what their
@@ -656,8 +671,10 @@ struct Loader {
  * 4.4 TB/s), pairs by the chain S, P, O of a stream, of which the other stream hides a part
  * (4800 tokens of 32 heads over 32768 keys: 2.8 ms, 0.92 PFLOP/s and half as much again for
  * the second product of P, tensor cores 76 % active), and small calls by their first
- * instructions: the cut, 2.6 us, the first tile 6 us after the start. */
-template <int D>
+ * instructions: the cut, 2.6 us, the first tile 6 us after the start.
+ * TREE: among its sequence's tokens a row sees those that its bits name (one at or before itself);
+ * only tiles with such keys look at them, and the words are fetched while S is under way. */
+template <int D, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                const __grid_constant__ CUtensorMap vmap, const __grid_constant__ Args a) {
@@ -901,11 +918,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int b = c.own ? c.seq : a.off ? find(sm->off, a.n_seqs + 1, tok) : tok;
       /* keys of the item that this row sees end here */
       const int limit = min(c.kend, sm->len[b] - (sm->off[b + 1] - tok) + 1);
-      const int warp_limit = __reduce_min_sync(0xffffffffu, limit);
+      const int base = TREE ? sm->len[b] - (sm->off[b + 1] - sm->off[b]) : 0; /* the tokens' first place */
+      /* below it every row of the warp sees all */
+      const int warp_limit = __reduce_min_sync(0xffffffffu, TREE ? min(limit, base) : limit);
       float m = -INFINITY, l = 0.0f; /* m in score units */
 #pragma unroll 1
       for (int t = 0; t < c.n; ++t) {
         const int k0 = c.key0 + (c.t0 + t) * kTile;
+        uint32_t seen[TREE ? kTile / 32 : 1];
+        if (TREE && busy && warp_limit < k0 + kTile) {
+          uint32_t lo = tree_word(a, tok, (k0 - base) >> 5);
+#pragma unroll
+          for (int i = 0; i < kTile / 32; ++i) {
+            const uint32_t hi = tree_word(a, tok, ((k0 - base) >> 5) + i + 1);
+            seen[TREE ? i : 0] = tree_keys(lo, hi, k0 + 32 * i, base, limit);
+            lo = hi;
+          }
+        }
         ok = warp_wait(&sm->sfull[s], s_par, stop);
         if (!ok) break;
         s_par ^= 1;
@@ -949,7 +978,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float x[kTile];
         tmem_ld128(at_s, x);
-        if (warp_limit < k0 + kTile) {
+        if (TREE && warp_limit < k0 + kTile) {
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) x[i] = seen[TREE ? i / 32 : 0] >> i % 32 & 1 ? x[i] : -INFINITY;
+        } else if (warp_limit < k0 + kTile) {
           const int d = limit - k0;
 #pragma unroll
           for (int i = 0; i < kTile; ++i) x[i] = i < d ? x[i] : -INFINITY;
@@ -1259,8 +1291,11 @@ namespace {
 template <int D>
 cudaError_t prepare() {
   static_assert(Cfg<D>::SMEM + sizeof(Smem) <= 232448, "shared memory of a CTA");
-  return cudaFuncSetAttribute(attn_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Cfg<D>::SMEM + (int)sizeof(Smem));
+  constexpr int smem = Cfg<D>::SMEM + (int)sizeof(Smem);
+  const cudaError_t e =
+      cudaFuncSetAttribute(attn_tiles<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(attn_tiles<D, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 template <int D>
@@ -1275,8 +1310,9 @@ cudaError_t launch(const mk_attn *at, int layer, const CUtensorMap &qmap, const 
   cfg.stream = at->stream;
   cfg.attrs = pdl;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, attn_tiles<D>, qmap, at->maps[2 * layer],
-                                     at->maps[2 * layer + 1], a);
+  const CUtensorMap &kmap = at->maps[2 * layer], &vmap = at->maps[2 * layer + 1];
+  const cudaError_t e = a.tree ? cudaLaunchKernelEx(&cfg, attn_tiles<D, true>, qmap, kmap, vmap, a)
+                               : cudaLaunchKernelEx(&cfg, attn_tiles<D, false>, qmap, kmap, vmap, a);
   if (e != cudaSuccess) return e;
   int blocks = 1;
   while (2 * blocks <= a.G && blocks < 8 && a.n_tokens * a.Hkv * blocks < 2 * at->n_sm) blocks *= 2;
@@ -1379,8 +1415,9 @@ void mk_attn_destroy(mk_attn *at) {
   delete at;
 }
 
-mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b, const void *q,
-                              int64_t q_token_stride, void *out, float *lse) {
+static mk_status attend(mk_attn *at, int32_t layer, const mk_attn_batch *b, const uint32_t *tree,
+                        int32_t tree_words, const void *q, int64_t q_token_stride, void *out,
+                        float *lse) {
   if (!at || !b) return MK_ERR_INVALID_ARG;
   const mk_attn_desc &d = at->d;
   if (layer < 0 || layer >= d.n_layers || b->n_seqs < 0 || b->n_tokens < 0 || b->n_groups < 0 ||
@@ -1412,6 +1449,10 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   if (overlap(q, q_bytes, out, b->n_tokens * row) ||
       (lse && (overlap(q, q_bytes, lse, lse_bytes) || overlap(out, b->n_tokens * row, lse, lse_bytes))))
     return MK_ERR_INVALID_ARG;
+  const int64_t tree_bytes = (int64_t)b->n_tokens * tree_words * 4;
+  if (tree && (overlap(tree, tree_bytes, out, b->n_tokens * row) ||
+               (lse && overlap(tree, tree_bytes, lse, lse_bytes))))
+    return MK_ERR_INVALID_ARG;
   OnDevice on(at->dev);
   if (!on.ok) return MK_ERR_CUDA;
   Args a{};
@@ -1433,6 +1474,9 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   a.out = (__nv_bfloat16 *)out;
   a.lse = lse;
   a.scale_log2 = at->scale_log2;
+  a.tree = tree;
+  a.tree_words = tree_words;
+  a.max_query = tree ? 32 * tree_words : INT32_MAX;
   a.TB = kTile / a.G;
   a.inv_g = (65536 + a.G - 1) / a.G;
   a.inv_p = ((1ull << 38) + a.P - 1) / a.P;
@@ -1453,6 +1497,19 @@ mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b
   if (e != cudaSuccess) return MK_ERR_CUDA;
   at->poison = false;
   return MK_OK;
+}
+
+mk_status mk_prefix_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b, const void *q,
+                              int64_t q_token_stride, void *out, float *lse) {
+  return attend(at, layer, b, nullptr, 0, q, q_token_stride, out, lse);
+}
+
+mk_status mk_tree_attention(mk_attn *at, int32_t layer, const mk_attn_batch *b,
+                            const uint32_t *tree, int32_t tree_words, const void *q,
+                            int64_t q_token_stride, void *out, float *lse) {
+  if (tree_words < 1 || tree_words > (1 << 20) / 32 || !aligned(tree, 4)) return MK_ERR_INVALID_ARG;
+  if (!tree && b && b->n_seqs > 0 && b->n_tokens > 0) return MK_ERR_INVALID_ARG;
+  return attend(at, layer, b, tree, tree_words, q, q_token_stride, out, lse);
 }
 
 mk_status mk_attn_set_wait_limit_ns(mk_attn *at, uint64_t ns) {
