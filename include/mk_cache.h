@@ -93,6 +93,20 @@ mk_status mk_kv_fork(mk_kv *kv, int32_t n, const int32_t *src_seqs, const int32_
  * there are too few, MK_ERR_PAGE_OOB for a length behind the table row. */
 mk_status mk_kv_resize(mk_kv *kv, int32_t n, const int32_t *seqs, const int32_t *new_lens);
 
+/* Keeps, of the tokens that were appended from place starts[i] of sequence seqs[i] on (DEVICE
+ * int32 [n], the sequences distinct, n <= n_seqs), the picked ones: the K and V rows, in every
+ * pool, of the tokens at starts[i] + picks[offsets[i] .. offsets[i + 1] - 1] move to starts[i],
+ * starts[i] + 1, ... in that order: the accepted path of a drafted tree.  A sequence's picks are
+ * 0 or above and rise; offsets: DEVICE int32 [n + 1] from 0, not decreasing, the last one <=
+ * n_picks; picks: DEVICE int32 [n_picks].  Lengths do not change: mk_kv_resize gives the rest
+ * back, or sets the length of the next draft.  A pool's page is [n_kv_heads][page_size][row] with
+ * rows of a multiple of 16 bytes.  MK_ERR_PAGE_OOB for a token behind its sequence's length or in
+ * a page that is not held; MK_ERR_INVALID_ARG where a token would go to a page that has other
+ * holders. */
+mk_status mk_kv_keep(mk_kv *kv, int32_t n, const int32_t *seqs, const int32_t *starts,
+                     const int32_t *offsets, int32_t n_picks, const int32_t *picks,
+                     int32_t n_kv_heads);
+
 /* Moves the held pages to the lowest ids: with H pages held, the k-th held page
  * with an id >= H goes to the k-th free id < H, in every pool; tables and
  * holders follow.  page_map: DEVICE int32 [num_pages] or NULL; receives each

@@ -149,7 +149,7 @@ EXPORTS = ["mk_create", "mk_build_schedule", "mk_decode_step", "mk_sync", "mk_de
            "mk_get_stats", "mk_debug_poison_wait", "mk_plan", "mk_decode_step_static",
            "mk_set_trace", "mk_get_trace", "mk_set_stage_trace_cta",
            "mk_kv_create", "mk_kv_destroy", "mk_kv_copy_pages", "mk_kv_fork", "mk_kv_resize",
-           "mk_kv_compact", "mk_kv_sync",
+           "mk_kv_keep", "mk_kv_compact", "mk_kv_sync",
            "mk_attn_create", "mk_attn_destroy", "mk_prefix_attention", "mk_tree_attention",
            "mk_attn_sync",
            "mk_attn_set_wait_limit_ns", "mk_attn_debug_poison_wait",
@@ -195,6 +195,7 @@ def lib():
         L.mk_kv_destroy.restype = None
         for n in ("mk_kv_copy_pages", "mk_kv_fork", "mk_kv_resize"):
             getattr(L, n).argtypes = [vp, i32, vp, vp]
+        L.mk_kv_keep.argtypes = [vp, i32, vp, vp, vp, i32, vp, i32]
         L.mk_kv_compact.argtypes = [vp, vp]
         L.mk_kv_sync.argtypes = [vp]
         L.mk_attn_create.argtypes = [ctypes.POINTER(mk_attn_desc), vp, ctypes.POINTER(vp)]

@@ -157,6 +157,25 @@ class KvCache:
         _check(self._lib.mk_kv_resize(*self._two(seqs, new_lens, "seqs", "new_lens")),
                "mk_kv_resize")
 
+    def keep(self, seqs, starts, offsets, picks, n_kv_heads: int = None):
+        """Moves, in every pool, the tokens at starts[i] + picks[j] of sequence seqs[i], j from
+        offsets[i] to offsets[i + 1], to starts[i], starts[i] + 1, ...: a drafted tree's accepted
+        path.  Lengths do not change.  n_kv_heads: of a page; None: the pools' second dimension
+        (pools [pages][heads][tokens][dims])."""
+        _, n, s, b = self._two(seqs, starts, "seqs", "starts")
+        for t, what in ((offsets, "offsets"), (picks, "picks")):
+            if not (getattr(t, "dtype", None) is self._int32 and t.get_device() == self._index
+                    and t.dim() == 1 and t.is_contiguous()):
+                _want(t, what, "int32", self.device, 1)
+        if offsets.numel() != n + 1:
+            raise ValueError("offsets has one entry more than there are sequences")
+        if n_kv_heads is None:
+            if self.pools[0].dim() != 4 or self.pools[0].shape[2] != self.page_size:
+                raise ValueError("n_kv_heads is needed: the pools are not [pages][heads][tokens][dims]")
+            n_kv_heads = self.pools[0].shape[1]
+        _check(self._lib.mk_kv_keep(self.handle, n, s, b, offsets.data_ptr(), picks.numel(),
+                                    picks.data_ptr(), n_kv_heads), "mk_kv_keep")
+
     def compact(self, page_map=None):
         """Moves the held pages to the lowest ids; page_map (int32 [num_pages]) receives
         each page's new id, -1 for free pages."""

@@ -546,6 +546,195 @@ __global__ void __launch_bounds__(kMoveThreads, 4)
   move_pages(p, p.n, p.a, p.b);
 }
 
+/* ---- keep: rows of a sequence's picked tokens move together ------------------- */
+
+struct Keep {
+  Params p; /* n sequences a[i] */
+  const int32_t *starts, *offsets, *picks;
+  int32_t n_picks, heads, row_chunks; /* kv heads of a page; 16-byte pieces of a token's row in one */
+  int32_t units;                      /* such pieces of a token in all pools */
+  unsigned warps;                     /* warps' shares of a sequence's pieces */
+};
+
+/* Whether the sequence and the range of picks of entry i can be looked at. */
+__device__ __forceinline__ bool keep_sound(const Keep &a, int i, int s, int lo, int hi) {
+  return (unsigned)s < (unsigned)a.p.n_seqs && lo >= 0 && hi >= lo && hi <= a.n_picks && (i > 0 || lo == 0);
+}
+/* Pick k, the j-th of entry i, in row s: x and y are the page and the place in it where its token
+ * lies, z and w where it goes.  Returns a status. */
+__device__ __forceinline__ int keep_pick(const Keep &a, int i, int s, int k, int j, int4 *rows) {
+  const Params &p = a.p;
+  const int pick = __ldcg(a.picks + k), before = j > 0 ? __ldcg(a.picks + k - 1) : -1;
+  const int start = __ldcg(a.starts + i), len = __ldcg(p.lens + s), P = p.page_size;
+  const long long from = (long long)start + pick;
+  if (pick <= before) return MK_ERR_INVALID_ARG;
+  if (start < 0 || len > (long long)p.max_pages * P || from >= len) return MK_ERR_PAGE_OOB;
+  if (pick < j) return MK_OK; /* one before it is wrong, which its own check reports */
+  const int32_t *row = p.tables + (size_t)s * p.max_pages;
+  const int to = start + j, src = __ldcg(row + (int)from / P), dst = __ldcg(row + to / P);
+  *rows = make_int4(src, (int)from % P, dst, to % P);
+  if ((unsigned)src >= (unsigned)p.num_pages || (unsigned)dst >= (unsigned)p.num_pages) return MK_ERR_PAGE_OOB;
+  const int holders = __ldcg(p.refs + dst);
+  if (holders < 1 || __ldcg(p.refs + src) < 1) return MK_ERR_PAGE_OOB;
+  return holders > 1 && pick != j ? MK_ERR_INVALID_ARG : MK_OK;
+}
+
+/* A warp's 32 pieces of every picked token of one sequence.  A lane has the same 16 bytes of each,
+ * and takes them in order, eight loads ahead of their stores: a token goes to a place at or before
+ * its own and the picks rise, so no store touches what is still to be loaded.  `rows_of` gives the
+ * rows of one pick to all lanes. */
+template <class F>
+__device__ __forceinline__ void keep_move(const Keep &a, unsigned share, int count, F rows_of) {
+  const Params &p = a.p;
+  const int unit = (int)share * 32 + (threadIdx.x & 31);
+  const bool mine = unit < a.units;
+  const int per_pool = a.heads * a.row_chunks, pool = mine ? unit / per_pool : 0;
+  const int rest = unit - pool * per_pool, head = rest / a.row_chunks;
+  const long long row_bytes = 16ll * a.row_chunks;
+  char *base = p.pools[pool] + (long long)head * p.page_size * row_bytes + (rest - head * a.row_chunks) * 16;
+  for (int j0 = 0; j0 < count; j0 += 8) {
+    uint4 v[8];
+    char *to[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      to[k] = nullptr;
+      if (j0 + k >= count) continue;
+      const int4 r = rows_of(j0 + k);
+      if (!mine || (r.x == r.z && r.y == r.w)) continue;
+      to[k] = base + r.z * p.page_bytes + r.w * row_bytes;
+      v[k] = __ldcg((const uint4 *)(base + r.x * p.page_bytes + r.y * row_bytes));
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (to[k]) __stcg((uint4 *)to[k], v[k]);
+  }
+}
+
+/* Checks all picks, one cluster, and lets kv_keep_rows go on or not. */
+__global__ void __launch_bounds__(kPlanThreads) kv_keep_plan(const __grid_constant__ Keep a) {
+  const Params &p = a.p;
+  const int lane = threadIdx.x & 31;
+  const int gtid = blockIdx.x * blockDim.x + threadIdx.x, nthr = gridDim.x * blockDim.x;
+  wait_for_previous();
+  dependents_may_launch();
+  const int held_up = __ldcg(&p.ctrl->status);
+  for (int i = gtid; i < p.n_seqs; i += nthr) p.claim[i] = 0;
+  if (gtid == 0) {
+    p.ctrl->call_err = 0;
+    p.ctrl->n_copy = 0;
+    p.ctrl->remap = 0;
+  }
+  cluster_sync();
+  if (held_up) return;
+  for (int i = gtid; i < p.n; i += nthr) {
+    const int s = __ldcg(p.a + i);
+    if (!keep_sound(a, i, s, __ldcg(a.offsets + i), __ldcg(a.offsets + i + 1)) ||
+        atomicExch(p.claim + s, 1) != 0)
+      refuse(p, MK_ERR_INVALID_ARG);
+  }
+  cluster_sync();
+  int err = __ldcg(&p.ctrl->call_err); /* the same for all: the next refusal comes behind a barrier */
+  cluster_sync();
+  if (err == 0) {
+    for (int i = gtid >> 5; i < p.n; i += nthr >> 5) {
+      const int s = __ldcg(p.a + i), lo = __ldcg(a.offsets + i), hi = __ldcg(a.offsets + i + 1);
+      for (int k = lo + lane; k < hi; k += 32) {
+        int4 rows;
+        const int e = keep_pick(a, i, s, k, k - lo, &rows);
+        if (e) refuse(p, e);
+      }
+    }
+    cluster_sync();
+    err = __ldcg(&p.ctrl->call_err);
+  }
+  if (gtid == 0) {
+    p.ctrl->n_copy = err == 0;
+    if (err) {
+      p.ctrl->status = err;
+      *(volatile int32_t *)p.err_host = err;
+      __threadfence_system();
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kMoveThreads, 4) kv_keep_rows(const __grid_constant__ Keep a) {
+  wait_for_previous();
+  dependents_may_launch();
+  if (__ldcg(&a.p.ctrl->n_copy) == 0) return;
+  const int lane = threadIdx.x & 31;
+  const unsigned long long nwarp = gridDim.x * (kMoveThreads / 32), all = (unsigned long long)a.warps * a.p.n;
+  for (unsigned long long w = (blockIdx.x * kMoveThreads + threadIdx.x) >> 5; w < all; w += nwarp) {
+    const int i = (int)(w / a.warps);
+    const int s = __ldcg(a.p.a + i), lo = __ldcg(a.offsets + i), n = __ldcg(a.offsets + i + 1) - lo;
+    int4 mine = make_int4(0, 0, 0, 0);
+    keep_move(a, (unsigned)(w - (unsigned long long)i * a.warps), n, [&](int j) {
+      if (j % 32 == 0 && j + lane < n) keep_pick(a, i, s, lo + j + lane, j + lane, &mine);
+      return make_int4(__shfl_sync(0xffffffffu, mine.x, j & 31), __shfl_sync(0xffffffffu, mine.y, j & 31),
+                       __shfl_sync(0xffffffffu, mine.z, j & 31), __shfl_sync(0xffffffffu, mine.w, j & 31));
+    });
+  }
+}
+
+/* Both in one kernel, for up to kFewKept sequences and kFewPicks picks: every block checks all of
+ * them, so that none waits for another, and finds their rows on the way. */
+constexpr int kFewKept = 1024, kFewPicks = 2048;
+__global__ void __launch_bounds__(kMoveThreads, 4) kv_keep_few(const __grid_constant__ Keep a) {
+  extern __shared__ int4 rows[]; /* [n_picks], then the offsets [n + 1], then a bit for each sequence */
+  int *off = (int *)(rows + a.n_picks);
+  unsigned *claim = (unsigned *)(off + a.p.n + 1);
+  const Params &p = a.p;
+  const int tid = threadIdx.x, n = p.n;
+  for (int i = tid; i < (p.n_seqs + 31) / 32; i += kMoveThreads) claim[i] = 0;
+  wait_for_previous();
+  dependents_may_launch();
+  const int held_up = __ldcg(&p.ctrl->status); /* by an earlier refusal, or another block's of this call */
+  for (int i = tid; i <= n; i += kMoveThreads) off[i] = __ldcg(a.offsets + i);
+  __syncthreads();
+  bool wrong = false;
+  for (int i = tid; i < n; i += kMoveThreads) {
+    const int s = __ldcg(p.a + i);
+    if (!keep_sound(a, i, s, off[i], off[i + 1]))
+      wrong = true;
+    else
+      wrong |= (atomicOr(claim + s / 32, 1u << s % 32) >> s % 32) & 1;
+  }
+  wrong = __syncthreads_or(wrong);
+  bool outside = false;
+  if (!wrong) {
+    for (int k = tid; k < off[n]; k += kMoveThreads) {
+      int lo = 0, hi = n - 1; /* the last entry that begins at or before it */
+      while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (off[m] <= k)
+          lo = m;
+        else
+          hi = m - 1;
+      }
+      const int e = keep_pick(a, lo, __ldcg(p.a + lo), k, k - off[lo], rows + k);
+      outside |= e == MK_ERR_PAGE_OOB;
+      wrong |= e == MK_ERR_INVALID_ARG;
+    }
+    outside = __syncthreads_or(outside);
+    wrong = __syncthreads_or(wrong);
+  }
+  if (held_up) return;
+  if (outside || wrong) {
+    if (blockIdx.x == 0 && tid == 0) {
+      const int err = outside ? MK_ERR_PAGE_OOB : MK_ERR_INVALID_ARG;
+      p.ctrl->status = err;
+      *(volatile int32_t *)p.err_host = err;
+      __threadfence_system();
+    }
+    return;
+  }
+  const unsigned nwarp = gridDim.x * (kMoveThreads / 32), all = a.warps * n;
+  for (unsigned w = (blockIdx.x * kMoveThreads + tid) >> 5; w < all; w += nwarp) {
+    const int i = (int)(w / a.warps);
+    const int4 *mine = rows + off[i];
+    keep_move(a, w - i * a.warps, off[i + 1] - off[i], [&](int j) { return mine[j]; });
+  }
+}
+
 /* Makes `dev` current for a scope: a handle may be called with another device
  * current. */
 struct OnDevice {
@@ -601,10 +790,10 @@ cudaError_t launch_plan(const mk_kv *kv, const Params &p) {
   return cudaLaunchKernelEx(&cfg, kv_plan<OP>, p);
 }
 
-/* The largest cluster of kv_plan that this device takes. */
-template <int OP>
-cudaError_t allow_clusters(int *largest) {
-  cudaError_t e = cudaFuncSetAttribute(kv_plan<OP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+/* The largest cluster of a plan that this device takes. */
+template <class Kernel>
+cudaError_t allow_clusters(Kernel plan, int *largest) {
+  cudaError_t e = cudaFuncSetAttribute(plan, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.blockDim = dim3(kPlanThreads);
@@ -616,7 +805,7 @@ cudaError_t allow_clusters(int *largest) {
     int n = 0;
     cfg.gridDim = dim3(*largest);
     at[0].val.clusterDim = {(unsigned)*largest, 1, 1};
-    if (cudaOccupancyMaxActiveClusters(&n, kv_plan<OP>, &cfg) == cudaSuccess && n > 0) break;
+    if (cudaOccupancyMaxActiveClusters(&n, plan, &cfg) == cudaSuccess && n > 0) break;
     cudaGetLastError(); /* a size too large is no error of the caller's */
   }
   return cudaSuccess;
@@ -698,10 +887,11 @@ mk_status mk_kv_create(const mk_kv_desc *d, void *stream, mk_kv **out) {
   const size_t o_ctrl = take(sizeof(Ctrl) / 4), o_refs = take(N), o_claim = take(std::max(N, S)),
                o_fresh = take(N), o_src = take(N), o_dst = take(N), o_need = take(S),
                o_first = take(S), o_len0 = take(S), o_len1 = take(S), o_stage = take(S * M), o_pools = take(2 * (size_t)d->n_pools);
-  cudaError_t e = allow_clusters<OP_COPY>(&kv->max_cluster);
-  if (e == cudaSuccess) e = allow_clusters<OP_FORK>(&kv->max_cluster);
-  if (e == cudaSuccess) e = allow_clusters<OP_RESIZE>(&kv->max_cluster);
-  if (e == cudaSuccess) e = allow_clusters<OP_COMPACT>(&kv->max_cluster);
+  cudaError_t e = allow_clusters(kv_plan<OP_COPY>, &kv->max_cluster);
+  if (e == cudaSuccess) e = allow_clusters(kv_plan<OP_FORK>, &kv->max_cluster);
+  if (e == cudaSuccess) e = allow_clusters(kv_plan<OP_RESIZE>, &kv->max_cluster);
+  if (e == cudaSuccess) e = allow_clusters(kv_plan<OP_COMPACT>, &kv->max_cluster);
+  if (e == cudaSuccess) e = allow_clusters(kv_keep_plan, &kv->max_cluster);
   if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
   if (e == cudaSuccess) e = cudaMemsetAsync(kv->ws, 0, off, kv->stream);
   if (e == cudaSuccess)
@@ -794,6 +984,59 @@ mk_status mk_kv_compact(mk_kv *kv, int32_t *page_map) {
   p.page_map = page_map;
   const long long rows = (long long)kv->d.n_seqs * ((kv->d.max_pages_per_seq + 31) / 32);
   return submit<OP_COMPACT>(kv, p, kv->d.num_pages / 2, rows);
+}
+
+mk_status mk_kv_keep(mk_kv *kv, int32_t n, const int32_t *seqs, const int32_t *starts,
+                     const int32_t *offsets, int32_t n_picks, const int32_t *picks,
+                     int32_t n_kv_heads) {
+  if (!kv || n < 0 || n > kv->d.n_seqs || n_picks < 0 || n_kv_heads < 1) return MK_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)n_kv_heads * kv->d.page_size; /* of a page: tokens times heads */
+  if (kv->d.page_bytes % rows || kv->d.page_bytes / rows % 16) return MK_ERR_INVALID_ARG;
+  if (n == 0) return MK_OK;
+  if (!seqs || !starts || !offsets || (n_picks && !picks) || !aligned4(seqs) || !aligned4(starts) ||
+      !aligned4(offsets) || !aligned4(picks))
+    return MK_ERR_INVALID_ARG;
+  Keep a{};
+  a.p = kv->base;
+  a.p.n = n;
+  a.p.a = seqs;
+  a.starts = starts;
+  a.offsets = offsets;
+  a.picks = picks;
+  a.n_picks = n_picks;
+  a.heads = n_kv_heads;
+  a.row_chunks = (int32_t)(kv->d.page_bytes / rows / 16);
+  const int64_t units = (int64_t)kv->d.n_pools * a.heads * a.row_chunks;
+  if (units > (1 << 24)) return MK_ERR_UNSUPPORTED; /* 256 MB a token */
+  a.units = (int32_t)units;
+  a.warps = (unsigned)((units + 31) / 32);
+  OnDevice on(kv->dev);
+  if (!on.ok) return MK_ERR_CUDA;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.stream = kv->stream;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const long long warps = (long long)a.warps * n;
+  const unsigned blocks = (unsigned)std::min((warps + kMoveThreads / 32 - 1) / (kMoveThreads / 32), (long long)kv->n_sm * 4);
+  if (n <= kFewKept && n_picks <= kFewPicks) {
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = (size_t)n_picks * 16 + (n + 1) * 4 + ((size_t)kv->d.n_seqs + 31) / 32 * 4;
+    return cudaLaunchKernelEx(&cfg, kv_keep_few, a) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  }
+  cfg.gridDim = dim3(kv->max_cluster);
+  cfg.blockDim = dim3(kPlanThreads);
+  cfg.numAttrs = 2;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {(unsigned)kv->max_cluster, 1, 1};
+  if (cudaLaunchKernelEx(&cfg, kv_keep_plan, a) != cudaSuccess) return MK_ERR_CUDA;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_keep_rows, a) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 
 mk_status mk_kv_sync(mk_kv *kv) {
