@@ -26,7 +26,7 @@ LIB_PATH = os.path.join(BUILD, "libmk.so")
 
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 SOURCES = ["mk_kernel.cu", "mk_api.cpp", "mk_schedule.cpp", "mk_noalloc.cu", "mk_kv.cu",
-           "mk_attn.cu", "mk_append.cu"]
+           "mk_attn.cu", "mk_append.cu", "mk_rules.cu"]
 
 MK_OK = 0
 STATUS_NAMES = {0: "MK_OK", 1: "MK_ERR_INVALID_ARG", 2: "MK_ERR_BATCH", 3: "MK_ERR_PAGE_OOB",
@@ -144,6 +144,15 @@ class mk_append_rows(ctypes.Structure):
             (n, ctypes.c_void_p) for n in ("q_norm", "k_norm", "positions")]
 
 
+class mk_rules_batch(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n_rows", "n_tokens", "n_path", "n_bias", "n_masks")] + [
+        (n, ctypes.c_void_p) for n in
+        ("tokens", "ranges", "prompt_lens", "path_offsets", "path_tokens", "repetition",
+         "presence", "frequency", "bias_offsets", "bias_tokens", "bias", "allowed",
+         "allowed_rows")]
+
+
 EXPORTS = ["mk_create", "mk_build_schedule", "mk_decode_step", "mk_sync", "mk_destroy",
            "mk_status_string", "mk_set_wait_limit_ns", "mk_debug_routing", "mk_debug_dump",
            "mk_get_stats", "mk_debug_poison_wait", "mk_plan", "mk_decode_step_static",
@@ -153,9 +162,10 @@ EXPORTS = ["mk_create", "mk_build_schedule", "mk_decode_step", "mk_sync", "mk_de
            "mk_attn_create", "mk_attn_destroy", "mk_prefix_attention", "mk_tree_attention",
            "mk_attn_sync",
            "mk_attn_set_wait_limit_ns", "mk_attn_debug_poison_wait",
-           "mk_append_create", "mk_append_destroy", "mk_append_tokens", "mk_append_sync"]
+           "mk_append_create", "mk_append_destroy", "mk_append_tokens", "mk_append_sync",
+           "mk_rules_create", "mk_rules_destroy", "mk_rules_apply", "mk_rules_sync"]
 _NO_STATUS = ("mk_destroy", "mk_status_string", "mk_kv_destroy", "mk_attn_destroy",
-              "mk_append_destroy")
+              "mk_append_destroy", "mk_rules_destroy")
 
 _lib = None
 
@@ -213,6 +223,11 @@ def lib():
         L.mk_append_tokens.argtypes = [vp, i32, ctypes.POINTER(mk_attn_batch),
                                        ctypes.POINTER(mk_append_rows)]
         L.mk_append_sync.argtypes = [vp]
+        L.mk_rules_create.argtypes = [i32, i32, vp, ctypes.POINTER(vp)]
+        L.mk_rules_destroy.argtypes = [vp]
+        L.mk_rules_destroy.restype = None
+        L.mk_rules_apply.argtypes = [vp, ctypes.POINTER(mk_rules_batch), vp, i32, i64, vp, vp]
+        L.mk_rules_sync.argtypes = [vp]
         for n in EXPORTS:
             if n not in _NO_STATUS:
                 getattr(L, n).restype = i32
@@ -396,6 +411,7 @@ class Decoder:
         self.weights = Weights(tensors["embed"], layers, tensors["final_norm"], tensors["lm_head"])
         self.ctx = None
         self.ctx = mk_create(self.cdims, self.weights, stream)
+        self.stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else (stream or 0)
         self.batch = 0
 
     def build_schedule(self, seq_lens, page_tables):
@@ -414,8 +430,16 @@ class Decoder:
         lens, tables = cache.read(seqs)
         self.build_schedule(lens - 1 if seq_lens is None else seq_lens, tables)
 
-    def decode_step(self, token_ids, out_logits, out_next_tokens):
+    def decode_step(self, token_ids, out_logits, out_next_tokens, rules=None):
+        """rules: (TokenRules, its batch) that are put on out_logits (a torch tensor) behind the
+        step, on the same stream; out_next_tokens are then the greedy tokens under them."""
+        if rules is not None and rules[0].stream != self.stream:
+            raise ValueError("the rules belong to another stream than the decoder")
+        if rules is not None and out_logits is None:
+            raise ValueError("rules need out_logits")
         mk_decode_step(self.ctx, token_ids, out_logits, out_next_tokens)
+        if rules is not None:
+            rules[0].run(rules[1], out_logits, out=out_logits, tokens=out_next_tokens)
 
     def sync(self):
         mk_sync(self.ctx)
@@ -464,3 +488,4 @@ class Decoder:
 
 from .cache import (KvAppend, KvCache, PrefixAttention, rope_frequencies,
                     tree_rows)  # noqa: E402  (needs the functions above)
+from .rules import TokenRules  # noqa: E402
