@@ -4,8 +4,8 @@
  *
  * A warp takes a token, or some of a token's heads where there are few tokens: 32 lanes of 8 dims
  * hold 256 / head_dim heads at a time, so a lane has the same dims of every head, and turns its
- * cosines and sines once for all of them.  The token's sequence, place, page and angle are looked
- * up while its first heads are on their way.
+ * cosines and sines once for all of them.  A token's sequence, place, page and position are looked
+ * up while the one before it is under way.
  */
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -25,16 +25,19 @@ using namespace mk_dev;
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxSeqs = 1024; /* of a call: offsets and lengths are in shared memory */
-constexpr int kBatch = 4;      /* 16-byte loads in flight a lane */
+constexpr int kBatch = 4;      /* steps whose loads are in flight together */
+constexpr int kBlocks = 3;     /* of an SM */
 
-/* How a dim finds its partner: in the same lane, in a lane some way on, or anywhere. */
-enum { PAIR_INSIDE = 0, PAIR_LANES = 1, PAIR_ANY = 2 };
+/* Which of a head's dims a lane holds, as four pairs (a, b): PAIR_HALVES 4 dims and the 4 half the
+ * rotary part further on (rotary_dim a multiple of 8), PAIR_NEIGHBOURS 8 dims in a row, PAIR_ANY
+ * halves one by one.  Either way no lane needs another's values, or turns an angle twice. */
+enum { PAIR_HALVES = 0, PAIR_NEIGHBOURS = 1, PAIR_ANY = 2 };
 
 struct Args {
   int32_t Hq, Hkv, P, M, num_pages, n_seqs, n_tokens, R;
-  int32_t rows, parts, steps; /* heads of a token (q, k, v); parts of a token; steps a part */
+  int32_t q_steps, kv_steps, parts, steps; /* warp's steps of a token's q, of k or v; parts of a token; steps a part */
   const int32_t *tables, *lens, *off, *positions;
-  const uint64_t *turns; /* [R / 2] turns a position, in 2^-64 */
+  const uint64_t *turns; /* [64] turns a position of each pair, in 2^-64; 0 behind the rotary part */
   const __nv_bfloat16 *q, *k, *v, *q_norm, *k_norm;
   __nv_bfloat16 *q_out, *k_pool, *v_pool;
   int64_t q_stride, k_stride, v_stride, q_out_stride;
@@ -42,13 +45,12 @@ struct Args {
   Errors err;
 };
 
-/* cos and sin of 2 pi position F / 2^64: the product mod 1 is exact, the nearest quarter turn is
- * taken off in integers, and the rest, within pi / 4, goes through the Taylor series (next terms:
- * x^11 / 11! below 2e-9, x^12 / 12! below 2e-10). */
+/* cos and sin of 2 pi position F / 2^64: the product mod 1 is exact; of its first 32 bits the
+ * nearest quarter turn is taken off in integers, and the rest, within pi / 4, goes through the Taylor
+ * series (next terms: x^11 / 11! below 2e-9, x^12 / 12! below 2e-10). */
 __device__ __forceinline__ void turn(uint32_t position, uint64_t F, float *c, float *s) {
-  const uint64_t u = F * position;
-  const uint64_t quarter = (u + (1ull << 61)) >> 62;
-  const float x = __ll2float_rn((long long)(u - (quarter << 62))) * 3.4061215800304e-19f; /* 2 pi / 2^64 */
+  const uint32_t u = (uint32_t)((F * position) >> 32), quarter = (u + (1u << 29)) >> 30;
+  const float x = (float)(int32_t)(u - (quarter << 30)) * 1.46291807927e-9f; /* 2 pi / 2^32 */
   const float y = x * x;
   float sn = fmaf(y, 2.755731922e-6f, -1.984126984e-4f); /* 1 / 9!, 1 / 7! */
   sn = fmaf(sn, y, 8.333333333e-3f);
@@ -65,29 +67,182 @@ __device__ __forceinline__ void turn(uint32_t position, uint64_t F, float *c, fl
   *s = (quarter & 2) ? -b : b;       /* quarters 2 and 3 */
 }
 
-__device__ __forceinline__ void unpack8(const uint4 &w, float *x) {
-  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(v[i] << 16);
-    x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float *x) {
-  uint32_t v[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(v[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
-  return make_uint4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ float low(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  uint32_t w;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+  return w;
 }
 
+/* A lane's 8 dims of a head of D. */
 template <int D, int PAIR>
-__global__ void __launch_bounds__(kThreads) append_tokens(const __grid_constant__ Args a) {
+struct Dims {
+  int l, half, oa, ob; /* lane of the head; first dims of the two pieces */
+  __device__ Dims(int lane, int R) : l(lane % (D / 8)), half(R >> 1) {
+    const bool turns = 8 * l < R;
+    oa = PAIR == PAIR_HALVES && turns ? 4 * l : 8 * l;
+    ob = PAIR == PAIR_HALVES && turns ? 4 * l + half : 8 * l + 4;
+  }
+  /* the dims of pair k; pairs behind the rotary part are neighbours */
+  __device__ __forceinline__ int a(int k) const {
+    const int p = 4 * l + k;
+    if (PAIR == PAIR_HALVES) return oa + k;
+    return PAIR == PAIR_ANY && p < half ? p : 2 * p;
+  }
+  __device__ __forceinline__ int b(int k) const {
+    const int p = 4 * l + k;
+    if (PAIR == PAIR_HALVES) return ob + k;
+    return PAIR == PAIR_ANY && p < half ? p + half : 2 * p + 1;
+  }
+  __device__ __forceinline__ bool turns(int k) const {
+    return PAIR == PAIR_HALVES ? 8 * l < 2 * half : 4 * l + k < half;
+  }
+  __device__ __forceinline__ uint4 load(const __nv_bfloat16 *head) const {
+    if constexpr (PAIR == PAIR_NEIGHBOURS) return __ldcg((const uint4 *)(head + oa));
+    if constexpr (PAIR == PAIR_HALVES) {
+      const uint2 x = __ldcg((const uint2 *)(head + oa)), y = __ldcg((const uint2 *)(head + ob));
+      return make_uint4(x.x, x.y, y.x, y.y);
+    }
+    if constexpr (PAIR == PAIR_ANY) {
+      uint32_t w[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[k] = __ldcg((const unsigned short *)head + a(k)) | (uint32_t)__ldcg((const unsigned short *)head + b(k)) << 16;
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16 *head, const uint4 &v) const {
+    if (PAIR == PAIR_NEIGHBOURS) {
+      *(uint4 *)(head + oa) = v;
+    } else if (PAIR == PAIR_HALVES) {
+      *(uint2 *)(head + oa) = make_uint2(v.x, v.y);
+      *(uint2 *)(head + ob) = make_uint2(v.z, v.w);
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        ((unsigned short *)head)[a(k)] = (unsigned short)w[k];
+        ((unsigned short *)head)[b(k)] = (unsigned short)(w[k] >> 16);
+      }
+    }
+  }
+  __device__ __forceinline__ void unpack(const uint4 &v, float *xa, float *xb) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (PAIR == PAIR_HALVES) {
+        xa[k] = k & 1 ? high(w[k / 2]) : low(w[k / 2]);
+        xb[k] = k & 1 ? high(w[2 + k / 2]) : low(w[2 + k / 2]);
+      } else {
+        xa[k] = low(w[k]);
+        xb[k] = high(w[k]);
+      }
+    }
+  }
+  __device__ __forceinline__ uint4 packed(const float *xa, const float *xb) const {
+    if (PAIR == PAIR_HALVES)
+      return make_uint4(pack(xa[0], xa[1]), pack(xa[2], xa[3]), pack(xb[0], xb[1]), pack(xb[2], xb[3]));
+    return make_uint4(pack(xa[0], xb[0]), pack(xa[1], xb[1]), pack(xa[2], xb[2]), pack(xa[3], xb[3]));
+  }
+};
+
+/* A lane's part of what is done to a head: a' = f (a ca + b sb), b' = f (b cb + a sa), with f the
+ * norm's factor, and the gains in the rest. */
+template <int D, int PAIR, bool NORM>
+struct Turn {
+  float ca[4], cb[4], sa[4], sb[4];
+  float eps;
+  bool normed;
+  __device__ __forceinline__ void set(const Dims<D, PAIR> &dims, const float *cs, const float *sn, const uint4 &gain,
+                                      bool normed_, float eps_) {
+    float ga[4] = {1.0f, 1.0f, 1.0f, 1.0f}, gb[4] = {1.0f, 1.0f, 1.0f, 1.0f};
+    if (NORM) dims.unpack(gain, ga, gb);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      ca[k] = cs[k] * ga[k];
+      cb[k] = cs[k] * gb[k];
+      sa[k] = sn[k] * ga[k];
+      sb[k] = -sn[k] * gb[k];
+    }
+    normed = normed_;
+    eps = eps_;
+  }
+  __device__ __forceinline__ uint4 operator()(const Dims<D, PAIR> &dims, const uint4 &v) const {
+    float xa[4], xb[4], f = 1.0f;
+    dims.unpack(v, xa, xb);
+    if (NORM && normed) {
+      float2 ss = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        ss = __ffma2_rn(make_float2(xa[j], xa[j + 1]), make_float2(xa[j], xa[j + 1]), ss);
+        ss = __ffma2_rn(make_float2(xb[j], xb[j + 1]), make_float2(xb[j], xb[j + 1]), ss);
+      }
+      f = ss.x + ss.y;
+#pragma unroll
+      for (int o = 1; o < D / 8; o *= 2) f += __shfl_xor_sync(0xffffffffu, f, o);
+      f = rsqrtf(f * (1.0f / D) + eps);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+      const float2 a = make_float2(xa[j], xa[j + 1]), b = make_float2(xb[j], xb[j + 1]);
+      float2 y0 = __fmul2_rn(a, make_float2(ca[j], ca[j + 1])), y1 = __fmul2_rn(b, make_float2(cb[j], cb[j + 1]));
+      /* an infinity beside a dim that does not turn stays there */
+      if (PAIR == PAIR_HALVES) {
+        if (dims.turns(0)) {
+          y0 = __ffma2_rn(b, make_float2(sb[j], sb[j + 1]), y0);
+          y1 = __ffma2_rn(a, make_float2(sa[j], sa[j + 1]), y1);
+        }
+      } else {
+        if (dims.turns(j)) y0.x = fmaf(b.x, sb[j], y0.x), y1.x = fmaf(a.x, sa[j], y1.x);
+        if (dims.turns(j + 1)) y0.y = fmaf(b.y, sb[j + 1], y0.y), y1.y = fmaf(a.y, sa[j + 1], y1.y);
+      }
+      if (NORM) {
+        y0 = __fmul2_rn(y0, make_float2(f, f));
+        y1 = __fmul2_rn(y1, make_float2(f, f));
+      }
+      xa[j] = y0.x, xa[j + 1] = y0.y;
+      xb[j] = y1.x, xb[j + 1] = y1.y;
+    }
+    return dims.packed(xa, xb);
+  }
+};
+
+/* n steps of a warp over heads that lie src_step and dst_step apart; this lane has a head in the
+ * first `mine` of them. */
+template <int D, int PAIR, class F>
+__device__ __forceinline__ void heads(const Dims<D, PAIR> &dims, int n, int mine, const __nv_bfloat16 *src, int src_step,
+                                      __nv_bfloat16 *dst, long long dst_step, F f) {
+#pragma unroll 1
+  for (; n > 0; n -= kBatch, mine -= kBatch) {
+    uint4 v[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (k < mine) v[k] = dims.load(src + k * src_step);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (k >= n) break;
+      v[k] = f(v[k]);
+      if (k < mine) dims.store(dst + k * dst_step, v[k]);
+    }
+    src += kBatch * src_step;
+    dst += kBatch * dst_step;
+  }
+}
+
+/* A token's place, position and page; the last two may be on their way. */
+struct Where {
+  int place, position, page;
+};
+
+template <int D, int PAIR, bool NORM>
+__global__ void __launch_bounds__(kThreads, kBlocks) append_tokens(const __grid_constant__ Args a) {
   constexpr int LPH = D / 8, HPW = 32 / LPH; /* lanes of a head, heads of a warp's step */
   __shared__ int s_off[kMaxSeqs + 1], s_len[kMaxSeqs];
-  __shared__ float s_any[PAIR == PAIR_ANY ? kWarps : 1][PAIR == PAIR_ANY ? 32 * 8 : 1];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int hl = lane / LPH, d0 = lane % LPH * 8, half = a.R >> 1;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hl = lane / LPH;
+  const Dims<D, PAIR> dims(lane, a.R);
 
   /* From here on what the grid before wrote is read, through L2: its blocks may have left older
    * lines in this SM's L1. */
@@ -104,29 +259,18 @@ __global__ void __launch_bounds__(kThreads) append_tokens(const __grid_constant_
       s_len[i] = l;
     }
   }
+  const uint4 ones = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+  const uint4 gq = NORM && a.q_norm ? dims.load(a.q_norm) : ones;
+  const uint4 gk = NORM && a.k_norm ? dims.load(a.k_norm) : ones;
   if (__syncthreads_or(bad)) {
     if (blockIdx.x == 0 && tid == 0) report(a.err, MK_ERR_INVALID_ARG);
     return;
   }
-  const int tokens = s_off[a.n_seqs];
-  const unsigned items = (unsigned)tokens * a.parts;
-  for (unsigned item = blockIdx.x * kWarps + warp; item < items; item += gridDim.x * kWarps) {
-    const int tok = (int)(item / a.parts), part = (int)(item - (unsigned)tok * a.parts);
-    const int row0 = part * a.steps * HPW, row1 = min(a.rows, row0 + a.steps * HPW);
-    auto source = [&](int r) -> const uint4 * {
-      const __nv_bfloat16 *p = r < a.Hq           ? a.q + tok * a.q_stride + r * D
-                               : r < a.Hq + a.Hkv ? a.k + tok * a.k_stride + (r - a.Hq) * D
-                                                  : a.v + tok * a.v_stride + (r - a.Hq - a.Hkv) * D;
-      return (const uint4 *)(p + d0);
-    };
-    uint4 raw[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int r = row0 + k * HPW + hl;
-      raw[k] = make_uint4(0, 0, 0, 0);
-      if (r < row1) raw[k] = __ldcg(source(r));
-    }
-    /* whose token it is, its place and page */
+  const unsigned items = (unsigned)s_off[a.n_seqs] * a.parts;
+  auto look_up = [&](unsigned item) {
+    Where w{-1, 0, -1};
+    if (item >= items) return w;
+    const int tok = (int)(item / a.parts);
     int lo = 0, hi = a.n_seqs - 1; /* the last sequence that begins at or before it */
     if (a.off) {
       while (lo < hi) {
@@ -139,108 +283,62 @@ __global__ void __launch_bounds__(kThreads) append_tokens(const __grid_constant_
     } else {
       lo = tok;
     }
-    const int place = s_len[lo] - (s_off[lo + 1] - tok);
-    const int position = a.positions ? __ldcg(a.positions + tok) : place;
-    if (place < 0) continue;
-    if (position < 0) {
+    w.place = s_len[lo] - (s_off[lo + 1] - tok);
+    w.position = a.positions ? __ldcg(a.positions + tok) : w.place;
+    if (w.place >= 0) w.page = __ldcg(a.tables + (size_t)lo * a.M + w.place / a.P);
+    return w;
+  };
+  unsigned item = blockIdx.x * kWarps + warp;
+  Where next = look_up(item);
+  for (; item < items; item += gridDim.x * kWarps) {
+    const int tok = (int)(item / a.parts), part = (int)(item - (unsigned)tok * a.parts);
+    const int first = part * a.steps, last = first + a.steps; /* of the steps of q, then k, then v */
+    const Where w = next;
+    next = look_up(item + gridDim.x * kWarps);
+    if (w.place < 0) continue;
+    if (w.position < 0) {
       if (lane == 0) report(a.err, MK_ERR_INVALID_ARG);
       continue;
     }
-    long long at = -1; /* first element of the token's first K or V head in the pools */
-    if (row1 > a.Hq) {
-      const int page = __ldcg(a.tables + (size_t)lo * a.M + place / a.P);
-      if ((unsigned)page < (unsigned)a.num_pages)
-        at = ((long long)page * a.Hkv * a.P + place % a.P) * D;
-      else if (lane == 0)
-        report(a.err, MK_ERR_PAGE_OOB);
+    Turn<D, PAIR, NORM> turned;
+    float cs[4], sn[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      turn((uint32_t)w.position, __ldg(a.turns + 4 * dims.l + k), &cs[k], &sn[k]);
+      cs[k] = dims.turns(k) ? cs[k] * a.magnitude : 1.0f;
+      sn[k] *= a.magnitude;
     }
-    /* this lane's cosines, and sines with the sign of their dim; 1 and 0 behind the rotary part */
-    constexpr int NP = PAIR == PAIR_INSIDE ? 4 : 8;
-    float cs[NP], sn[NP];
-    if (row0 < a.Hq + a.Hkv) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int d = PAIR == PAIR_INSIDE ? d0 + 2 * i : d0 + i;
-        cs[i] = 1.0f;
-        sn[i] = 0.0f;
-        if (d < a.R) {
-          const int pair = PAIR == PAIR_INSIDE ? d >> 1 : d < half ? d : d - half;
-          turn((uint32_t)position, a.turns[pair], &cs[i], &sn[i]);
-          cs[i] *= a.magnitude;
-          sn[i] *= PAIR != PAIR_INSIDE && d < half ? -a.magnitude : a.magnitude;
-        }
-      }
+    auto share = [&](int before, int all, int n_heads, int *i0, int *mine) { /* this item's of `all` steps */
+      *i0 = max(0, first - before);
+      *mine = (n_heads - hl + HPW - 1) / HPW - *i0;
+      return min(all, last - before) - *i0;
+    };
+    int i0, mine, n = share(0, a.q_steps, a.Hq, &i0, &mine);
+    if (n > 0) {
+      turned.set(dims, cs, sn, gq, NORM && a.q_norm, a.eps);
+      const int h = i0 * HPW + hl;
+      heads<D, PAIR>(dims, n, mine, a.q + tok * a.q_stride + h * D, HPW * D, a.q_out + tok * a.q_out_stride + h * D,
+                     HPW * D, [&](const uint4 &v) { return turned(dims, v); });
     }
-    for (int r0 = row0; r0 < row1; r0 += kBatch * HPW) {
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        const int r = r0 + k * HPW + hl;
-        if (r0 + k * HPW >= row1) break;
-        const bool is_q = r < a.Hq, turned = r < a.Hq + a.Hkv;
-        uint4 w = raw[k];
-        if (r0 + k * HPW < a.Hq + a.Hkv) { /* by whole warps: some of its heads are */
-          float x[8], y[8];
-          unpack8(w, x);
-          const __nv_bfloat16 *gain = is_q ? a.q_norm : a.k_norm;
-          if (a.q_norm || a.k_norm) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-            for (int o = 1; o < LPH; o *= 2) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (gain && turned) {
-              float g[8];
-              unpack8(*(const uint4 *)(gain + d0), g);
-              const float f = rsqrtf(ss * (1.0f / D) + a.eps);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) x[i] = x[i] * f * g[i];
-            }
-          }
-          if (PAIR == PAIR_INSIDE) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const bool on = d0 + 2 * i < a.R;
-              y[2 * i] = on ? __fmul_rn(x[2 * i], cs[i]) - __fmul_rn(x[2 * i + 1], sn[i]) : x[2 * i];
-              y[2 * i + 1] = on ? __fmul_rn(x[2 * i + 1], cs[i]) + __fmul_rn(x[2 * i], sn[i]) : x[2 * i + 1];
-            }
-          } else if (PAIR == PAIR_LANES) {
-            const int dist = half >> 3, l = lane % LPH;
-            const int from = lane + (l < dist ? dist : l < 2 * dist ? -dist : 0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float p = __shfl_sync(0xffffffffu, x[i], from);
-              y[i] = d0 < a.R ? __fmul_rn(x[i], cs[i]) + __fmul_rn(p, sn[i]) : x[i];
-            }
-          } else {
-            float *mine = s_any[warp] + hl * D;
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) mine[d0 + i] = x[i];
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int d = d0 + i;
-              y[i] = x[i];
-              if (d < a.R)
-                y[i] = __fmul_rn(x[i], cs[i]) + __fmul_rn(mine[d < half ? d + half : d - half], sn[i]);
-            }
-          }
-          if (turned) w = pack8(y);
-        }
-        if (r >= row1) continue;
-        if (is_q)
-          *(uint4 *)(a.q_out + tok * a.q_out_stride + r * D + d0) = w;
-        else if (at >= 0)
-          *(uint4 *)((turned ? a.k_pool : a.v_pool) + at +
-                     (long long)(turned ? r - a.Hq : r - a.Hq - a.Hkv) * a.P * D + d0) = w;
-      }
-      if (r0 + kBatch * HPW < row1) {
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-          const int r = r0 + (kBatch + k) * HPW + hl;
-          if (r < row1) raw[k] = __ldcg(source(r));
-        }
-      }
+    if (last <= a.q_steps) continue;
+    if ((unsigned)w.page >= (unsigned)a.num_pages) {
+      if (lane == 0) report(a.err, MK_ERR_PAGE_OOB);
+      continue;
+    }
+    const long long row = (long long)a.P * D; /* from a head of a page to the next */
+    const long long at = (long long)w.page * a.Hkv * row + (long long)(w.place % a.P) * D;
+    n = share(a.q_steps, a.kv_steps, a.Hkv, &i0, &mine);
+    if (n > 0) {
+      turned.set(dims, cs, sn, gk, NORM && a.k_norm, a.eps);
+      const int h = i0 * HPW + hl;
+      heads<D, PAIR>(dims, n, mine, a.k + tok * a.k_stride + h * D, HPW * D, a.k_pool + at + h * row, HPW * row,
+                     [&](const uint4 &v) { return turned(dims, v); });
+    }
+    n = share(a.q_steps + a.kv_steps, a.kv_steps, a.Hkv, &i0, &mine);
+    if (n > 0) {
+      const int h = i0 * HPW + hl;
+      heads<D, PAIR>(dims, n, mine, a.v + tok * a.v_stride + h * D, HPW * D, a.v_pool + at + h * row, HPW * row,
+                     [&](const uint4 &v) { return v; });
     }
   }
 }
@@ -259,11 +357,16 @@ struct mk_append {
 
 namespace {
 
+template <int D, int PAIR>
+cudaError_t launch(const cudaLaunchConfig_t &cfg, const Args &a) {
+  return a.q_norm || a.k_norm ? cudaLaunchKernelEx(&cfg, append_tokens<D, PAIR, true>, a)
+                              : cudaLaunchKernelEx(&cfg, append_tokens<D, PAIR, false>, a);
+}
 template <int D>
 cudaError_t launch(const mk_append *app, const cudaLaunchConfig_t &cfg, const Args &a) {
-  return app->pair == PAIR_INSIDE  ? cudaLaunchKernelEx(&cfg, append_tokens<D, PAIR_INSIDE>, a)
-         : app->pair == PAIR_LANES ? cudaLaunchKernelEx(&cfg, append_tokens<D, PAIR_LANES>, a)
-                                   : cudaLaunchKernelEx(&cfg, append_tokens<D, PAIR_ANY>, a);
+  return app->pair == PAIR_HALVES       ? launch<D, PAIR_HALVES>(cfg, a)
+         : app->pair == PAIR_NEIGHBOURS ? launch<D, PAIR_NEIGHBOURS>(cfg, a)
+                                        : launch<D, PAIR_ANY>(cfg, a);
 }
 
 }  // namespace
@@ -300,7 +403,7 @@ mk_status mk_append_create(const mk_append_desc *d, void *stream, mk_append **ou
   app->stream = (cudaStream_t)stream;
   app->dev = dev;
   app->n_sm = n_sm;
-  app->pair = d->interleaved || !d->rotary_dim ? PAIR_INSIDE : d->rotary_dim % 16 ? PAIR_ANY : PAIR_LANES;
+  app->pair = d->interleaved || !d->rotary_dim ? PAIR_NEIGHBOURS : d->rotary_dim % 8 ? PAIR_ANY : PAIR_HALVES;
   uint64_t turns[64] = {};
   try {
     app->k.assign(d->k_caches, d->k_caches + d->n_layers);
@@ -391,7 +494,6 @@ mk_status mk_append_tokens(mk_append *app, int32_t layer, const mk_attn_batch *b
   a.n_seqs = b->n_seqs;
   a.n_tokens = b->n_tokens;
   a.R = d.rotary_dim;
-  a.rows = a.Hq + 2 * a.Hkv;
   a.tables = b->page_tables;
   a.lens = b->seq_lens;
   a.off = b->q_offsets;
@@ -400,7 +502,7 @@ mk_status mk_append_tokens(mk_append *app, int32_t layer, const mk_attn_batch *b
   a.q = (const __nv_bfloat16 *)r->q;
   a.k = (const __nv_bfloat16 *)r->k;
   a.v = (const __nv_bfloat16 *)r->v;
-  a.q_norm = (const __nv_bfloat16 *)r->q_norm;
+  a.q_norm = with_q ? (const __nv_bfloat16 *)r->q_norm : nullptr;
   a.k_norm = (const __nv_bfloat16 *)r->k_norm;
   a.q_out = (__nv_bfloat16 *)r->q_out;
   a.k_pool = (__nv_bfloat16 *)app->k[layer];
@@ -413,7 +515,10 @@ mk_status mk_append_tokens(mk_append *app, int32_t layer, const mk_attn_batch *b
   a.eps = d.norm_eps;
   a.err = app->err;
   /* parts of a token: as many as make 8 warps an SM, each of one step at least */
-  const int steps = (a.rows + 256 / d.head_dim - 1) / (256 / d.head_dim);
+  const int heads = 256 / d.head_dim; /* of a step */
+  a.q_steps = (a.Hq + heads - 1) / heads;
+  a.kv_steps = (a.Hkv + heads - 1) / heads;
+  const int steps = a.q_steps + 2 * a.kv_steps;
   const int64_t want = ((int64_t)app->n_sm * 8 + b->n_tokens - 1) / b->n_tokens;
   a.steps = (int)std::max<int64_t>(1, steps / std::min<int64_t>(steps, want));
   a.parts = (steps + a.steps - 1) / a.steps;
@@ -422,7 +527,7 @@ mk_status mk_append_tokens(mk_append *app, int32_t layer, const mk_attn_batch *b
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(blocks, app->n_sm * 4));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(blocks, app->n_sm * kBlocks));
   cfg.blockDim = dim3(kThreads);
   cfg.stream = app->stream;
   cfg.attrs = at;
