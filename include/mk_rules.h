@@ -41,7 +41,7 @@ typedef struct {
 
 typedef struct mk_rules mk_rules;
 
-/* Allocates the workspace: 16 bytes a row.  vocab and max_rows from 1 to 2^24.
+/* Allocates the workspace: 8 bytes a row.  vocab and max_rows from 1 to 2^24.
  * MK_ERR_INVALID_ARG / MK_ERR_UNSUPPORTED / MK_ERR_NO_DEVICE / MK_ERR_CUDA. */
 mk_status mk_rules_create(int32_t vocab, int32_t max_rows, void *stream, mk_rules **out);
 void mk_rules_destroy(mk_rules *rules);

@@ -7,6 +7,12 @@
  * memory: how often the token was generated, whether the prompt has it, whether it has a bias.
  * The words of a history are counted once for all rows in a row that share it (the tokens of a
  * drafted tree); a row's path and biases are put in before its logits pass by, and taken out again.
+ *
+ * What bounds it: 384 bf16 rows of 152064 (350 MB) take 117 us, 3.0 TB/s, of which the copy with
+ * masks alone is 74 (about 100 instructions for 128 tokens, half of them a row's beginning and end)
+ * and the words and their rules the rest.  Rules in line, where a token's word is met, made most warps
+ * run them for one lane: 209 us.  A step of 8 rows, 15 us, and a single row of 32000, 7 us, are a
+ * chain of loads, each for the next: arguments, histories, listed tokens, the rows' best.
  */
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -23,9 +29,10 @@ namespace {
 
 using namespace mk_dev;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kSlice = 8192, kLeast = 1024; /* tokens of a slice: at most, at least */
 constexpr int kMost = 1 << 24;              /* vocabulary, rows */
+constexpr unsigned long long kWrong = 1; /* the key of a row that is not written: below that of any value */
 constexpr uint32_t kPrompt = 1u << 31, kBias = 1u << 30, kCount = kBias - 1;
 
 struct Args {
@@ -36,64 +43,80 @@ struct Args {
   float *out;
   int32_t *out_tokens;
   unsigned long long *best; /* [max_rows] of the slices so far, 0 between calls */
-  int32_t *done;            /* [max_rows] slices so far, 0 between calls */
+  int32_t *done;            /* blocks that are done, 0 between calls */
   Errors err;
 };
 
-__device__ __forceinline__ float4 load4(const float *p) { return __ldcg((const float4 *)p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-  const uint2 w = __ldcg((const uint2 *)p);
-  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                     __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-}
+/* Four tokens' logits as they lie in memory; none beyond `n` are looked at. */
+template <class T>
+struct Four;
+template <>
+struct Four<float> {
+  float4 v;
+  __device__ __forceinline__ void load(const float *p) { v = __ldcg((const float4 *)p); }
+  __device__ __forceinline__ void load(const float *p, int step, int n) {
+    v.x = n > 0 ? __ldcg(p) : 0.0f;
+    v.y = n > step ? __ldcg(p + step) : 0.0f;
+    v.z = n > 2 * step ? __ldcg(p + 2 * step) : 0.0f;
+    v.w = n > 3 * step ? __ldcg(p + 3 * step) : 0.0f;
+  }
+  __device__ __forceinline__ float4 get() const { return v; }
+};
+template <>
+struct Four<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldcg((const uint2 *)p); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *q, int step, int n) {
+    const unsigned short *p = (const unsigned short *)q;
+    const uint32_t a = n > 0 ? __ldcg(p) : 0, b = n > step ? __ldcg(p + step) : 0;
+    const uint32_t c = n > 2 * step ? __ldcg(p + 2 * step) : 0, d = n > 3 * step ? __ldcg(p + 3 * step) : 0;
+    v = make_uint2(a | b << 16, c | d << 16);
+  }
+  __device__ __forceinline__ float4 get() const {
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u),
+                       __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u));
+  }
+};
+
 __device__ __forceinline__ float load1(const float *p) { return __ldcg(p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16 *p) {
-  const unsigned short w = __ldcg((const unsigned short *)p);
-  return __uint_as_float((uint32_t)w << 16);
+  return __uint_as_float((uint32_t)__ldcg((const unsigned short *)p) << 16);
 }
 
-/* A row's arguments, the same in every thread. */
+/* A row's arguments.  A lane of one warp loads each. */
 struct Row {
   int begin, end, prompt, path0, path1, bias0, bias1, mask;
   float rep, pres, freq;
+  int pad;
 };
-__device__ __forceinline__ bool load_row(const mk_rules_batch &b, int row, Row *r) {
-  *r = Row{0, 0, 0, 0, 0, 0, 0, -1, 1.0f, 0.0f, 0.0f};
-  if (b.ranges) {
-    r->begin = __ldcg(b.ranges + 2 * (size_t)row);
-    r->end = __ldcg(b.ranges + 2 * (size_t)row + 1);
-    if (b.prompt_lens) r->prompt = __ldcg(b.prompt_lens + row);
-  }
-  if (b.path_offsets) {
-    r->path0 = __ldcg(b.path_offsets + row);
-    r->path1 = __ldcg(b.path_offsets + row + 1);
-  }
-  if (b.bias_offsets) {
-    r->bias0 = __ldcg(b.bias_offsets + row);
-    r->bias1 = __ldcg(b.bias_offsets + row + 1);
-  }
-  if (b.repetition) r->rep = __ldcg(b.repetition + row);
-  if (b.presence) r->pres = __ldcg(b.presence + row);
-  if (b.frequency) r->freq = __ldcg(b.frequency + row);
-  if (b.allowed) r->mask = b.allowed_rows ? __ldcg(b.allowed_rows + row) : row;
-  return r->begin >= 0 && r->end >= r->begin && r->end <= b.n_tokens && r->prompt >= 0 &&
-         r->path0 >= 0 && r->path1 >= r->path0 && r->path1 <= b.n_path && r->bias0 >= 0 &&
-         r->bias1 >= r->bias0 && r->bias1 <= b.n_bias && r->mask < b.n_masks && r->rep > 0.0f;
-}
-
-__device__ __forceinline__ float ruled(float x, uint32_t word, const float *bias, bool may, const Row &r) {
-  if (word) {
-    if (word & ~kBias) {
-      x = x > 0.0f ? __fdiv_rn(x, r.rep) : __fmul_rn(x, r.rep);
-      const uint32_t c = word & kCount;
-      if (c) {
-        x = __fsub_rn(x, __fmul_rn(r.freq, (float)c));
-        x = __fsub_rn(x, r.pres);
-      }
+constexpr int kRowWords = 11;
+struct RowLoader {
+  const int32_t *at;
+  int stride, otherwise;
+  __device__ RowLoader(const mk_rules_batch &b, int lane) : at(nullptr), stride(1), otherwise(0) {
+    switch (lane) {
+      case 0: at = b.ranges, stride = 2; break;
+      case 1: at = b.ranges ? b.ranges + 1 : nullptr, stride = 2; break;
+      case 2: at = b.prompt_lens; break;
+      case 3: at = b.path_offsets; break;
+      case 4: at = b.path_offsets ? b.path_offsets + 1 : nullptr; break;
+      case 5: at = b.bias_offsets; break;
+      case 6: at = b.bias_offsets ? b.bias_offsets + 1 : nullptr; break;
+      case 7: at = b.allowed ? b.allowed_rows : nullptr, otherwise = -1; break;
+      case 8: at = (const int32_t *)b.repetition, otherwise = 0x3f800000; break;
+      case 9: at = (const int32_t *)b.presence; break;
+      case 10: at = (const int32_t *)b.frequency; break;
     }
-    if (word & kBias) x = __fadd_rn(x, *bias);
+    if (lane == 7 && b.allowed && !b.allowed_rows) otherwise = -2; /* the row's own */
   }
-  return may ? x : -INFINITY;
+  __device__ __forceinline__ int operator()(int row) const {
+    return at ? __ldcg(at + (size_t)row * stride) : otherwise == -2 ? row : otherwise;
+  }
+};
+__device__ __forceinline__ bool sound(const mk_rules_batch &b, const Row &r) {
+  return r.begin >= 0 && r.end >= r.begin && r.end <= b.n_tokens && r.prompt >= 0 && r.path0 >= 0 &&
+         r.path1 >= r.path0 && r.path1 <= b.n_path && r.bias0 >= 0 && r.bias1 >= r.bias0 &&
+         r.bias1 <= b.n_bias && r.mask < b.n_masks && r.rep > 0.0f;
 }
 
 /* The row's best so far: x in an order that integers keep (-0 as 0), then the lowest id. */
@@ -102,132 +125,375 @@ __device__ __forceinline__ unsigned long long best_key(float x, int id) {
   return (unsigned long long)(u ^ (uint32_t)((int32_t)u >> 31 | 0x80000000)) << 32 | (uint32_t)~id;
 }
 
-template <class T, bool VEC>
-__global__ void __launch_bounds__(kThreads, 3) apply_rules(const __grid_constant__ Args a) {
+/* A row's penalties on one logit.  The quotient is x / r rounded once: r's rounded reciprocal, and
+ * the remainder of the first quotient in fused arithmetic (Markstein, "Computation of elementary
+ * functions on the IBM RISC System/6000 processor", 1990), which holds where nothing comes near
+ * the ends of the range; there the division itself is called. */
+struct Penalty {
+  float rep, inverse, pres, freq;
+  bool tame;
+  __device__ explicit Penalty(const Row &r) {
+    rep = r.rep;
+    inverse = __frcp_rn(r.rep);
+    pres = r.pres;
+    freq = r.freq;
+    tame = r.rep > 0x1p-30f && r.rep < 0x1p30f;
+  }
+  __device__ __forceinline__ float operator()(float x, uint32_t word) const {
+    const float q = x * inverse, d = fmaf(fmaf(-q, rep, x), inverse, q), size = fabsf(x);
+    float y = x > 0.0f ? d : __fmul_rn(x, rep);
+    if (x > 0.0f && !(tame && size > 0x1p-60f && size < 0x1p60f)) y = __fdiv_rn(x, rep);
+    const uint32_t c = word & kCount;
+    const float z = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)c)), pres);
+    y = c ? z : y;
+    return word & ~kBias ? y : x;
+  }
+};
+
+/* A block's slice: a word for each token, which tokens have one, and those tokens in no order. */
+struct Words {
+  uint32_t *word, *marked; /* [slice], [slice / 32] bits */
+  uint16_t *list;          /* [slice] */
+  __device__ Words(void *at, int slice)
+      : word((uint32_t *)at), marked(word + slice), list((uint16_t *)(marked + slice / 32)) {}
+  __device__ __forceinline__ void mark(int t, uint32_t before, int *length) const {
+    if (before) return;
+    list[atomicAdd(length, 1)] = (uint16_t)t;
+    atomicOr(marked + t / 32, 1u << t % 32);
+  }
+};
+static_assert(kSlice / 32 <= kThreads, "a thread lists one word of the bits");
+constexpr size_t words_bytes(int slice) { return (size_t)slice * 6 + slice / 8; }
+
+/* A thread's tokens of a slice, four to each chunk of 1024: in a row (VEC), or one of each 256.  They are
+ * masked and copied; those with a word, few as a rule, get their rules behind that, densely, from
+ * the list.  What a row needs next is loaded while the row before it is under way: its arguments and
+ * logits, then its path, biases and mask. */
+template <class T, bool VEC, int AHEAD>
+__global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant__ Args a) {
+  constexpr int STEP = VEC ? 1 : kThreads, CHUNK = 4 * kThreads; /* AHEAD chunks' logits are under way */
   extern __shared__ uint4 shared[];
   __shared__ unsigned long long s_best;
-  uint32_t *words = (uint32_t *)shared;
-  float *biases = (float *)(words + a.slice);
+  __shared__ int s_length, s_history; /* of the list, and of its part that rows share */
+  __shared__ __align__(16) Row s_row[2];
+  __shared__ int s_id[kThreads]; /* the row's first biases */
+  __shared__ float s_bias[kThreads];
+  const Words ws(shared, a.slice);
   const mk_rules_batch &b = a.b;
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, mine = VEC ? 4 * tid : tid;
   const bool counts = b.ranges || b.path_offsets || b.bias_offsets;
-  if (tid == 0) s_best = 0;
-  __syncthreads();
+  const RowLoader loader(b, warp == kWarps - 1 ? lane : 32);
+  if (tid == 0) {
+    s_best = 0;
+    s_length = 0;
+  }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const long long total = (long long)a.slices * b.n_rows;
-  const long long first = total * blockIdx.x / gridDim.x, last = total * (blockIdx.x + 1) / gridDim.x;
-  int at_slice = -1, at_begin = 0, at_end = 0, at_prompt = 0; /* whose words are there */
-  for (long long item = first; item < last; ++item) {
-    const int slice = (int)(item / b.n_rows), row = (int)(item - (long long)slice * b.n_rows);
-    const int v0 = slice * a.slice, nv = min(a.slice, a.vocab - v0);
-    Row r;
-    if (!load_row(b, row, &r)) {
-      if (tid == 0) report(a.err, MK_ERR_INVALID_ARG);
-      continue;
-    }
-    bool wrong = false;
-    if (counts) {
-      if (slice != at_slice || r.begin != at_begin || r.end != at_end || r.prompt != at_prompt) {
-        __syncthreads();
-        for (int i = tid; i < a.slice / 4; i += kThreads) shared[i] = make_uint4(0, 0, 0, 0);
-        __syncthreads();
-        for (int i = r.begin + tid; i < r.end; i += kThreads) {
-          const unsigned t = (unsigned)(__ldcg(b.tokens + i) - v0);
-          if (t < (unsigned)nv) {
-            if (i - r.begin < r.prompt)
-              atomicOr(words + t, kPrompt);
-            else
-              atomicAdd(words + t, 1u);
+  /* Two stretches of the items, slice by slice and row by row: text is made of few tokens, and those
+   * have low ids, so a block has as much of the first slices as of the last. */
+  const long long total = (long long)a.slices * b.n_rows, halves = 2ll * gridDim.x;
+  const long long lo = total * blockIdx.x / halves, lo_end = total * (blockIdx.x + 1) / halves;
+  const long long hi = total * (halves - 1 - blockIdx.x) / halves, hi_end = total * (halves - blockIdx.x) / halves;
+  const int n_lo = (int)(lo_end - lo), n_items = n_lo + (int)(hi_end - hi);
+  if (n_items) {
+    const long long first = n_lo ? lo : hi;
+    int slice = (int)(first / b.n_rows), row = (int)(first - (long long)slice * b.n_rows);
+    const int mask_words = (a.vocab + 31) / 32;
+    Four<T> raw[AHEAD];
+    const T *ahead; /* where the next chunks' logits lie, and how many tokens are left from there */
+    int ahead_left;
+    auto begin = [&](int slice, int row) {
+      const int i = slice * a.slice + mine;
+      ahead = (const T *)a.logits + row * a.row_stride + i;
+      ahead_left = min(a.slice, a.vocab - slice * a.slice) - mine;
+    };
+    auto fetch = [&](int k) {
+      if (!VEC)
+        raw[k].load(ahead + k * CHUNK, STEP, ahead_left - k * CHUNK);
+      else if (ahead_left > k * CHUNK)
+        raw[k].load(ahead + k * CHUNK);
+    };
+    auto go_on = [&] {
+      ahead += AHEAD * CHUNK;
+      ahead_left -= AHEAD * CHUNK;
+    };
+    if (warp == kWarps - 1 && lane < kRowWords) ((int *)&s_row[0])[lane] = loader(row);
+    begin(slice, row);
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) fetch(k);
+    go_on();
+    __syncthreads();
+    int path_id = -1, bias_id = -1, bias_before = -1;
+    float bias = 0.0f;
+    uint32_t may[AHEAD];
+    auto fetch_mask = [&](int k, const uint32_t *at, int left) {
+      may[k] = VEC && at && left > k * CHUNK ? __ldcg(at + k * (CHUNK / 32)) : 0xffffffffu;
+    };
+    const uint32_t *mask = nullptr; /* this thread's word of the row's next chunk */
+    auto fetch_own = [&](const Row &r, bool is_sound, int slice) {
+      mask = nullptr;
+      path_id = bias_id = bias_before = -1;
+      if (!is_sound) return;
+      if (r.path0 + tid < r.path1) path_id = __ldcg(b.path_tokens + r.path0 + tid);
+      if (r.bias0 + tid < r.bias1) {
+        bias_id = __ldcg(b.bias_tokens + r.bias0 + tid);
+        bias = __ldcg(b.bias + r.bias0 + tid);
+        if (tid) bias_before = __ldcg(b.bias_tokens + r.bias0 + tid - 1);
+      }
+      const int s0 = slice * a.slice;
+      if (r.mask >= 0) mask = b.allowed + (size_t)r.mask * mask_words + (s0 + mine) / 32;
+#pragma unroll
+      for (int k = 0; k < AHEAD; ++k) fetch_mask(k, mask, min(a.slice, a.vocab - s0) - mine);
+    };
+    Row r = s_row[0];
+    bool is_sound = sound(b, r);
+    fetch_own(r, is_sound, slice);
+    int at_slice = -1, at_begin = 0, at_end = 0, at_prompt = 0; /* whose words are there */
+#pragma unroll 1
+    for (int n = 0; n < n_items; ++n) {
+      const int v0 = slice * a.slice, nv = min(a.slice, a.vocab - v0);
+      const bool more = n + 1 < n_items;
+      int next_slice = slice, next_row = row + 1;
+      if (n + 1 == n_lo) {
+        next_slice = (int)(hi / b.n_rows);
+        next_row = (int)(hi - (long long)next_slice * b.n_rows);
+      } else if (next_row == b.n_rows) {
+        next_row = 0;
+        ++next_slice;
+      }
+      int next_word = 0;
+      if (more && warp == kWarps - 1 && lane < kRowWords) next_word = loader(next_row);
+      bool wrong = !is_sound;
+      const int n_bias = r.bias1 - r.bias0;
+      int own_path = -1, own_bias = -1; /* this thread's first words of the row's own */
+      if (counts && is_sound) {
+        if (slice != at_slice || r.begin != at_begin || r.end != at_end || r.prompt != at_prompt) {
+          for (int i = tid; i < a.slice / 4; i += kThreads) ((uint4 *)ws.word)[i] = make_uint4(0, 0, 0, 0);
+          for (int i = tid; i < a.slice / 32; i += kThreads) ws.marked[i] = 0;
+          __syncthreads();
+          for (int i0 = r.begin + tid; i0 < r.end; i0 += 8 * kThreads) {
+            int t[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) t[k] = i0 + k * kThreads < r.end ? __ldcg(b.tokens + i0 + k * kThreads) - v0 : -1;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if ((unsigned)t[k] >= (unsigned)nv) continue;
+              if (i0 + k * kThreads - r.begin < r.prompt)
+                atomicOr(ws.word + t[k], kPrompt);
+              else
+                atomicAdd(ws.word + t[k], 1u);
+              atomicOr(ws.marked + t[k] / 32, 1u << t[k] % 32);
+            }
+          }
+          __syncthreads();
+          /* the list, in order: a thread has one word of the bits */
+          uint32_t bits = tid < a.slice / 32 ? ws.marked[tid] : 0;
+          const int mine = __popc(bits);
+          int before = mine;
+#pragma unroll
+          for (int o = 1; o < 32; o *= 2) {
+            const int y = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += y;
+          }
+          if (lane == 31) s_id[warp] = before;
+          __syncthreads();
+          int to = before - mine, all = 0;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) to += s_id[w];
+            all += s_id[w];
+          }
+          for (; bits; bits &= bits - 1) ws.list[to++] = (uint16_t)(tid * 32 + __ffs(bits) - 1);
+          if (tid == 0) s_length = s_history = all;
+          __syncthreads();
+          at_slice = slice;
+          at_begin = r.begin;
+          at_end = r.end;
+          at_prompt = r.prompt;
+        }
+        if (path_id >= v0 && path_id - v0 < nv) {
+          own_path = path_id - v0;
+          ws.mark(own_path, atomicAdd(ws.word + own_path, 1u), &s_length);
+        }
+        if (tid < n_bias) {
+          wrong = (unsigned)bias_id >= (unsigned)a.vocab || bias_before >= bias_id;
+          s_id[tid] = bias_id;
+          s_bias[tid] = bias;
+          if (bias_id >= v0 && bias_id - v0 < nv) {
+            own_bias = bias_id - v0;
+            ws.mark(own_bias, atomicOr(ws.word + own_bias, kBias), &s_length);
           }
         }
-        at_slice = slice;
-        at_begin = r.begin;
-        at_end = r.end;
-        at_prompt = r.prompt;
-      }
-      for (int i = r.path0 + tid; i < r.path1; i += kThreads) {
-        const unsigned t = (unsigned)(__ldcg(b.path_tokens + i) - v0);
-        if (t < (unsigned)nv) atomicAdd(words + t, 1u);
-      }
-      for (int i = r.bias0 + tid; i < r.bias1; i += kThreads) {
-        const int id = __ldcg(b.bias_tokens + i);
-        wrong |= (unsigned)id >= (unsigned)a.vocab || (i > r.bias0 && __ldcg(b.bias_tokens + i - 1) >= id);
-        const unsigned t = (unsigned)(id - v0);
-        if (t < (unsigned)nv) {
-          atomicOr(words + t, kBias);
-          biases[t] = __ldcg(b.bias + i);
+        for (int i = r.path0 + tid + kThreads; i < r.path1; i += kThreads) {
+          const int t = __ldcg(b.path_tokens + i) - v0;
+          if ((unsigned)t < (unsigned)nv) ws.mark(t, atomicAdd(ws.word + t, 1u), &s_length);
         }
+        for (int i = r.bias0 + tid + kThreads; i < r.bias1; i += kThreads) {
+          const int id = __ldcg(b.bias_tokens + i), t = id - v0;
+          wrong |= (unsigned)id >= (unsigned)a.vocab || __ldcg(b.bias_tokens + i - 1) >= id;
+          if ((unsigned)t < (unsigned)nv) ws.mark(t, atomicOr(ws.word + t, kBias), &s_length);
+        }
+        wrong = __syncthreads_or(wrong);
       }
-      wrong = __syncthreads_or(wrong);
       if (wrong && tid == 0) report(a.err, MK_ERR_INVALID_ARG);
-    }
-    if (!wrong) {
+      const int length = counts && is_sound ? s_length : 0;
       const T *src = (const T *)a.logits + row * a.row_stride + v0;
       float *dst = a.out ? a.out + (long long)row * a.vocab + v0 : nullptr;
-      const uint32_t *mask =
-          r.mask >= 0 ? b.allowed + (size_t)r.mask * ((a.vocab + 31) / 32) + v0 / 32 : nullptr;
+      const uint32_t *masks = r.mask >= 0 && !wrong ? b.allowed + (size_t)r.mask * mask_words + v0 / 32 : nullptr;
       float top = -INFINITY;
       int at = -1;
-      if (VEC) {
-        for (int i = 4 * tid; i + 3 < nv; i += 4 * kThreads) {
-          const float4 x = load4(src + i);
-          const uint32_t may = mask ? __ldcg(mask + i / 32) >> (i & 31) : 15u;
-          const uint4 w = counts ? shared[i / 4] : make_uint4(0, 0, 0, 0);
-          float4 y;
-          y.x = ruled(x.x, w.x, biases + i, may & 1, r);
-          y.y = ruled(x.y, w.y, biases + i + 1, may & 2, r);
-          y.z = ruled(x.z, w.z, biases + i + 2, may & 4, r);
-          y.w = ruled(x.w, w.w, biases + i + 3, may & 8, r);
-          if (dst) __stcs((float4 *)(dst + i), y);
-          if (y.x > top) top = y.x, at = i;
-          if (y.y > top) top = y.y, at = i + 1;
-          if (y.z > top) top = y.z, at = i + 2;
-          if (y.w > top) top = y.w, at = i + 3;
+      const uint32_t *marked = ws.marked + mine / 32;
+      float *to = dst + mine;
+      int left = wrong ? 0 : nv - mine; /* of this thread's tokens */
+#pragma unroll 1
+      for (int c0 = 0; c0 < a.slice; c0 += AHEAD * CHUNK) {
+        const bool ends = c0 + AHEAD * CHUNK == a.slice;
+        if (ends) {
+          ahead_left = 0;
+          if (more) begin(next_slice, next_row);
+        }
+        if (mask) mask += AHEAD * (CHUNK / 32);
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+          const float4 x = raw[k].get();
+          uint32_t ok = may[k] >> (mine & 31), rest = 15; /* may follow; has no word */
+          fetch(k);
+          if (!ends) fetch_mask(k, mask, left - AHEAD * CHUNK);
+          if (left <= k * CHUNK) continue;
+          if (VEC) {
+            if (length) rest = ~marked[k * (CHUNK / 32)] >> (mine & 31);
+          } else {
+            ok = 15;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int w = (c0 + k * CHUNK + j * STEP + mine) / 32;
+              if (left <= k * CHUNK + j * STEP) {
+                rest &= ~(1u << j);
+              } else {
+                if (masks && !(__ldcg(masks + w) >> (mine & 31) & 1)) ok &= ~(1u << j);
+                if (length && ws.marked[w] >> (mine & 31) & 1) rest &= ~(1u << j);
+              }
+            }
+          }
+          float y[4] = {x.x, x.y, x.z, x.w}, z[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (!(ok >> j & 1)) y[j] = -INFINITY;
+            z[j] = rest >> j & 1 ? y[j] : -INFINITY;
+          }
+          if (dst) {
+            if (VEC) {
+              __stcs((float4 *)(to + k * CHUNK), make_float4(y[0], y[1], y[2], y[3]));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (left > k * CHUNK + j * STEP) __stcs(to + k * CHUNK + j * STEP, y[j]);
+            }
+          }
+          const float m = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])); /* NaN only if all are */
+          if (m > top) {
+            top = m;
+            at = c0 + k * CHUNK + mine + (z[0] == m ? 0 : z[1] == m ? STEP : z[2] == m ? 2 * STEP : 3 * STEP);
+          }
+        }
+        go_on();
+        marked += AHEAD * (CHUNK / 32);
+        to += AHEAD * CHUNK;
+        left -= AHEAD * CHUNK;
+      }
+      unsigned long long key = at >= 0 ? best_key(top, v0 + at) : 0;
+      if (more && warp == kWarps - 1 && lane < kRowWords) ((int *)&s_row[(n + 1) & 1])[lane] = next_word;
+      if (length) {
+        const Penalty penalty(r);
+#pragma unroll 1
+        for (int k0 = 0; k0 < length; k0 += 4 * kThreads) {
+          int t[4];
+          float x[4];
+          uint32_t may[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = k0 + j * kThreads + tid;
+            t[j] = k < length && !wrong ? ws.list[k] : -1;
+            if (t[j] >= 0) {
+              x[j] = load1(src + t[j]);
+              may[j] = masks ? __ldcg(masks + t[j] / 32) : 0xffffffffu;
+            }
+          }
+          /* over what was copied; in place it is the logit still, or masked for good */
+          if (k0 == 0) __syncthreads();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (t[j] < 0) continue;
+            const uint32_t word = ws.word[t[j]];
+            float y = penalty(x[j], word);
+            if (word & kBias) {
+              int at = 0, e = n_bias - 1; /* the last bias token at or below t: t itself */
+              while (at < e) {
+                const int m = (at + e + 1) >> 1;
+                if ((m < kThreads ? s_id[m] : __ldcg(b.bias_tokens + r.bias0 + m)) <= v0 + t[j])
+                  at = m;
+                else
+                  e = m - 1;
+              }
+              y = __fadd_rn(y, at < kThreads ? s_bias[at] : __ldcg(b.bias + r.bias0 + at));
+            }
+            if (!(may[j] >> t[j] % 32 & 1)) y = -INFINITY;
+            if (dst) __stcs(dst + t[j], y);
+            if (y > -INFINITY) key = max(key, best_key(y, v0 + t[j]));
+          }
         }
       }
-      for (int i = (VEC ? nv & ~3 : 0) + tid; i < nv; i += kThreads) {
-        const bool may = !mask || (__ldcg(mask + i / 32) >> (i & 31) & 1);
-        const float y = ruled(load1(src + i), counts ? words[i] : 0, biases + i, may, r);
-        if (dst) __stcs(dst + i, y);
-        if (y > top) top = y, at = i;
-      }
       if (a.out_tokens) {
-        unsigned long long key = at < 0 ? 0 : best_key(top, v0 + at);
 #pragma unroll
         for (int o = 16; o; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
         if (lane == 0 && key) atomicMax(&s_best, key);
       }
-    }
-    if (a.out_tokens || counts) __syncthreads();
-    if (!wrong && a.out_tokens && tid == 0) {
-      unsigned long long key = s_best;
-      s_best = 0;
-      bool mine = true; /* the row's last slice writes its token */
-      if (a.slices > 1) {
-        if (key) atomicMax(a.best + row, key);
-        __threadfence();
-        mine = atomicAdd(a.done + row, 1) == a.slices - 1;
-        if (mine) {
-          __threadfence();
-          key = atomicExch(a.best + row, 0ull);
-          a.done[row] = 0;
+      __syncthreads();
+      if (a.out_tokens && tid == 0) {
+        /* nothing waits for this: the last block takes the rows' best */
+        const unsigned long long best = wrong ? kWrong : s_best;
+        s_best = 0;
+        if (best) atomicMax(a.best + row, best);
+      }
+      if (length) { /* the row's own words out again */
+        if (own_path >= 0) atomicSub(ws.word + own_path, 1u);
+        if (own_bias >= 0) atomicAnd(ws.word + own_bias, ~kBias);
+        for (int i = r.path0 + tid + kThreads; i < r.path1; i += kThreads) {
+          const unsigned t = (unsigned)(__ldcg(b.path_tokens + i) - v0);
+          if (t < (unsigned)nv) atomicSub(ws.word + t, 1u);
         }
+        for (int i = r.bias0 + tid + kThreads; i < r.bias1; i += kThreads) {
+          const unsigned t = (unsigned)(__ldcg(b.bias_tokens + i) - v0);
+          if (t < (unsigned)nv) atomicAnd(ws.word + t, ~kBias);
+        }
+        for (int k = s_history + tid; k < length; k += kThreads)
+          atomicAnd(ws.marked + ws.list[k] / 32, ~(1u << ws.list[k] % 32));
+        if (tid == 0) s_length = s_history;
       }
-      if (mine) a.out_tokens[row] = key ? (int32_t)~(uint32_t)key : -1;
+      if (more) {
+        r = s_row[(n + 1) & 1];
+        is_sound = sound(b, r);
+        fetch_own(r, is_sound, next_slice);
+      }
+      __syncthreads();
+      slice = next_slice;
+      row = next_row;
     }
-    if (counts) { /* the row's own words out again */
-      for (int i = r.path0 + tid; i < r.path1; i += kThreads) {
-        const unsigned t = (unsigned)(__ldcg(b.path_tokens + i) - v0);
-        if (t < (unsigned)nv) atomicSub(words + t, 1u);
-      }
-      for (int i = r.bias0 + tid; i < r.bias1; i += kThreads) {
-        const unsigned t = (unsigned)(__ldcg(b.bias_tokens + i) - v0);
-        if (t < (unsigned)nv) atomicAnd(words + t, ~kBias);
-      }
-    }
-    if (a.out_tokens || counts) __syncthreads();
   }
+  if (!a.out_tokens) return;
+  if (tid == 0) {
+    __threadfence();
+    s_length = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!s_length) return;
+  __threadfence();
+  for (int i = tid; i < b.n_rows; i += kThreads) {
+    const unsigned long long key = __ldcg(a.best + i);
+    a.best[i] = 0;
+    if (key != kWrong) a.out_tokens[i] = key ? (int32_t)~(uint32_t)key : -1;
+  }
+  if (tid == 0) *a.done = 0;
 }
 
 }  // namespace
@@ -236,7 +502,7 @@ struct mk_rules {
   int32_t vocab = 0, max_rows = 0;
   cudaStream_t stream = nullptr;
   int dev = 0, n_sm = 0;
-  uint8_t *ws = nullptr; /* the error word; best and done of each row */
+  uint8_t *ws = nullptr; /* the error word, the blocks done; best of each row */
   Errors err{};
   int32_t *err_host = nullptr;
 };
@@ -244,8 +510,14 @@ struct mk_rules {
 namespace {
 
 typedef void (*Kernel)(Args);
-constexpr Kernel kKernels[2][2] = {{apply_rules<float, false>, apply_rules<float, true>},
-                                   {apply_rules<__nv_bfloat16, false>, apply_rules<__nv_bfloat16, true>}};
+template <class T, bool VEC>
+Kernel of_slice(int slice) { /* AHEAD divides a slice's chunks */
+  return slice >= 4 * kLeast ? apply_rules<T, VEC, 4> : slice == 2 * kLeast ? apply_rules<T, VEC, 2> : apply_rules<T, VEC, 1>;
+}
+Kernel kernel_of(bool bf16, bool vec, int slice) {
+  return bf16 ? vec ? of_slice<__nv_bfloat16, true>(slice) : of_slice<__nv_bfloat16, false>(slice)
+         : vec ? of_slice<float, true>(slice) : of_slice<float, false>(slice);
+}
 
 }  // namespace
 
@@ -263,10 +535,10 @@ mk_status mk_rules_create(int32_t vocab, int32_t max_rows, void *stream, mk_rule
   m->stream = (cudaStream_t)stream;
   m->dev = dev;
   m->n_sm = n_sm;
-  const size_t bytes = 64 + 16 * (size_t)max_rows;
+  const size_t bytes = 64 + 8 * (size_t)max_rows;
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-    e = cudaFuncSetAttribute(kKernels[i / 2][i % 2], cudaFuncAttributeMaxDynamicSharedMemorySize, kSlice * 8);
+    e = cudaFuncSetAttribute(kernel_of(i / 2, i % 2, kSlice), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)words_bytes(kSlice));
   if (e == cudaSuccess) e = cudaMalloc(&m->ws, bytes);
   if (e == cudaSuccess) e = cudaMemsetAsync(m->ws, 0, bytes, m->stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize(m->stream);
@@ -331,24 +603,24 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   a.out_tokens = out_tokens;
   a.err = m->err;
   a.best = (unsigned long long *)(m->ws + 64);
-  a.done = (int32_t *)(m->ws + 64 + 8 * (size_t)m->max_rows);
-  /* slices: as large as leaves every SM an item */
+  a.done = (int32_t *)(m->ws + 32);
+  /* slices: as large as leaves an SM two items (8 rows of 152064: 15.1 us, with one 17.2, with four
+   * 20.5; large slices cost a row less, 384 rows 117 us, with 4096 tokens a slice 158) */
   a.slice = kSlice;
-  while (a.slice > kLeast && (V + a.slice - 1) / a.slice * b->n_rows < m->n_sm) a.slice /= 2;
+  while (a.slice > kLeast && (V + a.slice - 1) / a.slice * b->n_rows < 2 * m->n_sm) a.slice /= 2;
   a.slices = (int32_t)((V + a.slice - 1) / a.slice);
-  const bool vec = row_stride % 4 == 0 && aligned(logits, 4 * (unsigned)size) &&
-                   (!out || (V % 4 == 0 && aligned(out, 16)));
+  const bool vec = V % 4 == 0 && row_stride % 4 == 0 && aligned(logits, 4 * (unsigned)size) && aligned(out, 16);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)a.slices * b->n_rows, m->n_sm * 3));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)a.slices * b->n_rows, m->n_sm * 4));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)a.slice * 8;
+  cfg.dynamicSmemBytes = words_bytes(a.slice);
   cfg.stream = m->stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kKernels[is_bf16 ? 1 : 0][vec], a) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel_of(is_bf16 != 0, vec, a.slice), a) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 
 mk_status mk_rules_sync(mk_rules *m) {
