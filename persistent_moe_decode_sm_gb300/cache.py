@@ -120,6 +120,7 @@ class KvCache:
         self.seq_lens, self.page_refs = seq_lens, page_refs
         self.n_seqs, self.max_pages_per_seq = page_tables.shape
         self.page_size = page_size
+        self._page_heads = shape[1] if len(shape) == 4 and shape[2] == page_size else None
         ptrs = (ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools])
         desc = mk_kv_desc(len(pools), shape[0], page_size, self.n_seqs, self.max_pages_per_seq,
                           page_bytes, ptrs, page_tables.data_ptr(), seq_lens.data_ptr(),
@@ -170,9 +171,9 @@ class KvCache:
         if offsets.numel() != n + 1:
             raise ValueError("offsets has one entry more than there are sequences")
         if n_kv_heads is None:
-            if self.pools[0].dim() != 4 or self.pools[0].shape[2] != self.page_size:
+            n_kv_heads = self._page_heads
+            if n_kv_heads is None:
                 raise ValueError("n_kv_heads is needed: the pools are not [pages][heads][tokens][dims]")
-            n_kv_heads = self.pools[0].shape[1]
         _check(self._lib.mk_kv_keep(self.handle, n, s, b, offsets.data_ptr(), picks.numel(),
                                     picks.data_ptr(), n_kv_heads), "mk_kv_keep")
 
@@ -399,7 +400,7 @@ class KvAppend:
         self.heads, self.kv_heads, self.head_dim = n_q_heads, n_kv_heads, head_dim
         self._index, self._bf16 = layers[0][0].get_device(), torch.bfloat16
         self._int32 = torch.int32
-        self._lib, self._rows = lib(), mk_append_rows()
+        self._lib = lib()
         desc = mk_append_desc(n_q_heads, n_kv_heads, head_dim, page_size, pages, rotary_dim,
                               int(bool(interleaved)), len(layers),
                               _pointers([k for k, _ in layers]), _pointers([v for _, v in layers]),
@@ -418,18 +419,17 @@ class KvAppend:
         return _batch(self.device, page_tables, seq_lens, q_offsets, None, None, n_tokens)
 
     def _stride(self, t, what, shape):
+        stride = t.stride()
         if (t.shape != shape or t.dtype is not self._bf16 or t.get_device() != self._index
-                or t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != self.head_dim)):
+                or stride[2] != 1 or (shape[1] > 1 and stride[1] != shape[2])):
             raise ValueError(f"{what} has to be bfloat16 {tuple(shape)} with contiguous heads on "
                              f"{self.device}")
-        return t.stride(0) if shape[0] > 1 else shape[1] * shape[2]
+        return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
     def _gain(self, t, what):
-        if t is None:
-            return None
         if not (t.dtype is self._bf16 and t.get_device() == self._index and t.is_contiguous()):
             _want(t, what, "bfloat16", self.device, 1)
-        if t.shape != (self.head_dim,):
+        if t.numel() != self.head_dim:
             raise ValueError(f"{what} has an entry for each of the head's {self.head_dim} dims")
         return t.data_ptr()
 
@@ -439,27 +439,28 @@ class KvAppend:
         [head_dim] to q_out (which may be q itself).  They may have token strides of their own,
         as parts of a fused projection.  positions (int32 [n_tokens]): what the heads turn to,
         None: the tokens' places.  q_norm, k_norm: gains of the norm, None: no norm."""
-        rows, n = self._rows, batch.n_tokens
+        n = batch.n_tokens
         if (q is None) != (q_out is None):
             raise ValueError("q and q_out come together")
         kv = (n, self.kv_heads, self.head_dim)
-        rows.k_stride, rows.v_stride = self._stride(k, "k", kv), self._stride(v, "v", kv)
-        rows.k, rows.v = k.data_ptr(), v.data_ptr()
-        rows.q = rows.q_out = None
+        k_stride, v_stride = self._stride(k, "k", kv), self._stride(v, "v", kv)
+        q_at = q_to = at = None
+        q_stride = q_out_stride = 0
         if q is not None:
             shape = (n, self.heads, self.head_dim)
-            rows.q_stride = self._stride(q, "q", shape)
-            rows.q_out_stride = self._stride(q_out, "q_out", shape)
-            rows.q, rows.q_out = q.data_ptr(), q_out.data_ptr()
-        rows.positions = None
+            q_stride, q_out_stride = self._stride(q, "q", shape), self._stride(q_out, "q_out", shape)
+            q_at, q_to = q.data_ptr(), q_out.data_ptr()
         if positions is not None:
             if not (positions.dtype is self._int32 and positions.get_device() == self._index
                     and positions.is_contiguous()):
                 _want(positions, "positions", "int32", self.device, 1)
             if positions.shape != (n,):
                 raise ValueError("positions has an entry for each token")
-            rows.positions = positions.data_ptr()
-        rows.q_norm, rows.k_norm = self._gain(q_norm, "q_norm"), self._gain(k_norm, "k_norm")
+            at = positions.data_ptr()
+        rows = mk_append_rows(
+            q_at, k.data_ptr(), v.data_ptr(), q_to, q_stride, k_stride, v_stride, q_out_stride,
+            None if q_norm is None else self._gain(q_norm, "q_norm"),
+            None if k_norm is None else self._gain(k_norm, "k_norm"), at)
         _check(self._lib.mk_append_tokens(self.handle, layer, ctypes.byref(batch),
                                           ctypes.byref(rows)), "mk_append_tokens")
 

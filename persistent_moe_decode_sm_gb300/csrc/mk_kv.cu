@@ -560,55 +560,71 @@ struct Keep {
 __device__ __forceinline__ bool keep_sound(const Keep &a, int i, int s, int lo, int hi) {
   return (unsigned)s < (unsigned)a.p.n_seqs && lo >= 0 && hi >= lo && hi <= a.n_picks && (i > 0 || lo == 0);
 }
-/* Pick k, the j-th of entry i, in row s: x and y are the page and the place in it where its token
- * lies, z and w where it goes.  Returns a status. */
-__device__ __forceinline__ int keep_pick(const Keep &a, int i, int s, int k, int j, int4 *rows) {
+/* The j-th pick of an entry that begins at place `start` in row s; `before` is the one before it.  x
+ * and y of rows are the page and the place in it where the token lies, z and w where it goes; x is -1
+ * where they cannot be told.  Returns a status, for all but the pages' holders. */
+__device__ __forceinline__ int keep_pick(const Keep &a, int s, int start, int pick, int before, int j, int4 *rows) {
   const Params &p = a.p;
-  const int pick = __ldcg(a.picks + k), before = j > 0 ? __ldcg(a.picks + k - 1) : -1;
-  const int start = __ldcg(a.starts + i), len = __ldcg(p.lens + s), P = p.page_size;
-  const long long from = (long long)start + pick;
+  const int P = p.page_size;
+  const long long from = (long long)start + pick, cap = (long long)p.max_pages * P;
+  *rows = make_int4(-1, 0, -1, 0);
   if (pick <= before) return MK_ERR_INVALID_ARG;
-  if (start < 0 || len > (long long)p.max_pages * P || from >= len) return MK_ERR_PAGE_OOB;
+  if (start < 0 || from >= cap) return MK_ERR_PAGE_OOB;
   if (pick < j) return MK_OK; /* one before it is wrong, which its own check reports */
   const int32_t *row = p.tables + (size_t)s * p.max_pages;
-  const int to = start + j, src = __ldcg(row + (int)from / P), dst = __ldcg(row + to / P);
+  const int to = start + j, len = __ldcg(p.lens + s);
+  const int src = __ldcg(row + (int)from / P), dst = __ldcg(row + to / P);
+  if (len > cap || from >= len || (unsigned)src >= (unsigned)p.num_pages || (unsigned)dst >= (unsigned)p.num_pages)
+    return MK_ERR_PAGE_OOB;
   *rows = make_int4(src, (int)from % P, dst, to % P);
-  if ((unsigned)src >= (unsigned)p.num_pages || (unsigned)dst >= (unsigned)p.num_pages) return MK_ERR_PAGE_OOB;
-  const int holders = __ldcg(p.refs + dst);
-  if (holders < 1 || __ldcg(p.refs + src) < 1) return MK_ERR_PAGE_OOB;
-  return holders > 1 && pick != j ? MK_ERR_INVALID_ARG : MK_OK;
+  return MK_OK;
+}
+/* Both pages have to be held, and the one that a token moves to by nobody else. */
+__device__ __forceinline__ int keep_holders(const Keep &a, const int4 &rows) {
+  if (rows.x < 0) return MK_OK; /* reported already */
+  const int to = __ldcg(a.p.refs + rows.z), from = __ldcg(a.p.refs + rows.x);
+  if (to < 1 || from < 1) return MK_ERR_PAGE_OOB;
+  return to > 1 && (rows.x != rows.z || rows.y != rows.w) ? MK_ERR_INVALID_ARG : MK_OK;
 }
 
 /* A warp's 32 pieces of every picked token of one sequence.  A lane has the same 16 bytes of each,
  * and takes them in order, eight loads ahead of their stores: a token goes to a place at or before
  * its own and the picks rise, so no store touches what is still to be loaded.  `rows_of` gives the
  * rows of one pick to all lanes. */
-template <class F>
-__device__ __forceinline__ void keep_move(const Keep &a, unsigned share, int count, F rows_of) {
-  const Params &p = a.p;
-  const int unit = (int)share * 32 + (threadIdx.x & 31);
-  const bool mine = unit < a.units;
-  const int per_pool = a.heads * a.row_chunks, pool = mine ? unit / per_pool : 0;
-  const int rest = unit - pool * per_pool, head = rest / a.row_chunks;
-  const long long row_bytes = 16ll * a.row_chunks;
-  char *base = p.pools[pool] + (long long)head * p.page_size * row_bytes + (rest - head * a.row_chunks) * 16;
-  for (int j0 = 0; j0 < count; j0 += 8) {
-    uint4 v[8];
-    char *to[8];
+struct Mover {
+  char *base;
+  long long row_bytes, page_bytes;
+  bool mine;
+  uint4 v[8];
+  char *to[8];
+  __device__ __forceinline__ Mover(const Keep &a, unsigned share) {
+    const Params &p = a.p;
+    const int unit = (int)share * 32 + (threadIdx.x & 31);
+    mine = unit < a.units;
+    const int per_pool = a.heads * a.row_chunks, pool = mine ? unit / per_pool : 0;
+    const int rest = unit - pool * per_pool, head = rest / a.row_chunks;
+    row_bytes = 16ll * a.row_chunks;
+    page_bytes = p.page_bytes;
+    base = p.pools[pool] + (long long)head * p.page_size * row_bytes + (rest - head * a.row_chunks) * 16;
+  }
+  template <class F>
+  __device__ __forceinline__ void load(int j0, int count, F rows_of) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       to[k] = nullptr;
       if (j0 + k >= count) continue;
       const int4 r = rows_of(j0 + k);
-      if (!mine || (r.x == r.z && r.y == r.w)) continue;
-      to[k] = base + r.z * p.page_bytes + r.w * row_bytes;
-      v[k] = __ldcg((const uint4 *)(base + r.x * p.page_bytes + r.y * row_bytes));
+      if (!mine || r.x < 0 || (r.x == r.z && r.y == r.w)) continue;
+      to[k] = base + r.z * page_bytes + r.w * row_bytes;
+      v[k] = __ldcg((const uint4 *)(base + r.x * page_bytes + r.y * row_bytes));
     }
+  }
+  __device__ __forceinline__ void store() const {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (to[k]) __stcg((uint4 *)to[k], v[k]);
   }
-}
+};
 
 /* Checks all picks, one cluster, and lets kv_keep_rows go on or not. */
 __global__ void __launch_bounds__(kPlanThreads) kv_keep_plan(const __grid_constant__ Keep a) {
@@ -638,9 +654,11 @@ __global__ void __launch_bounds__(kPlanThreads) kv_keep_plan(const __grid_consta
   if (err == 0) {
     for (int i = gtid >> 5; i < p.n; i += nthr >> 5) {
       const int s = __ldcg(p.a + i), lo = __ldcg(a.offsets + i), hi = __ldcg(a.offsets + i + 1);
+      const int start = __ldcg(a.starts + i);
       for (int k = lo + lane; k < hi; k += 32) {
         int4 rows;
-        const int e = keep_pick(a, i, s, k, k - lo, &rows);
+        int e = keep_pick(a, s, start, __ldcg(a.picks + k), k > lo ? __ldcg(a.picks + k - 1) : -1, k - lo, &rows);
+        if (!e) e = keep_holders(a, rows);
         if (e) refuse(p, e);
       }
     }
@@ -666,72 +684,117 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_keep_rows(const __grid_con
   for (unsigned long long w = (blockIdx.x * kMoveThreads + threadIdx.x) >> 5; w < all; w += nwarp) {
     const int i = (int)(w / a.warps);
     const int s = __ldcg(a.p.a + i), lo = __ldcg(a.offsets + i), n = __ldcg(a.offsets + i + 1) - lo;
-    int4 mine = make_int4(0, 0, 0, 0);
-    keep_move(a, (unsigned)(w - (unsigned long long)i * a.warps), n, [&](int j) {
-      if (j % 32 == 0 && j + lane < n) keep_pick(a, i, s, lo + j + lane, j + lane, &mine);
+    const int start = __ldcg(a.starts + i);
+    int4 mine;
+    auto rows_of = [&](int j) {
+      if (j % 32 == 0 && j + lane < n)
+        keep_pick(a, s, start, __ldcg(a.picks + lo + j + lane), -1, j + lane, &mine);
       return make_int4(__shfl_sync(0xffffffffu, mine.x, j & 31), __shfl_sync(0xffffffffu, mine.y, j & 31),
                        __shfl_sync(0xffffffffu, mine.z, j & 31), __shfl_sync(0xffffffffu, mine.w, j & 31));
-    });
+    };
+    Mover m(a, (unsigned)(w - (unsigned long long)i * a.warps));
+    for (int j0 = 0; j0 < n; j0 += 8) {
+      m.load(j0, n, rows_of);
+      m.store();
+    }
   }
 }
 
 /* Both in one kernel, for up to kFewKept sequences and kFewPicks picks: every block checks all of
- * them, so that none waits for another, and finds their rows on the way. */
-constexpr int kFewKept = 1024, kFewPicks = 2048;
-__global__ void __launch_bounds__(kMoveThreads, 4) kv_keep_few(const __grid_constant__ Keep a) {
-  extern __shared__ int4 rows[]; /* [n_picks], then the offsets [n + 1], then a bit for each sequence */
-  int *off = (int *)(rows + a.n_picks);
-  unsigned *claim = (unsigned *)(off + a.p.n + 1);
+ * them, so that none waits for another, and finds their rows on the way.  Three loads in a row
+ * (picks, tables, and holders with the first rows under way) and two barriers stand before the first
+ * store.  64 paths of up to 8 tokens in 96 pools, 44 MB read and written in rows of 256 bytes, take
+ * 14.4 us, 4 paths in 16 pools 3.6; in blocks of 256 threads, four an SM and each with the same checks
+ * to make, 17.2 and 3.3. */
+constexpr int kFewKept = 1024, kFewPicks = 2048, kKeepThreads = 512;
+constexpr int keep_few_bytes(int n, int n_picks, int n_seqs) {
+  return n_picks * 16 + (3 * n + 1) * 4 + (n_seqs + 31) / 32 * 4;
+}
+__global__ void __launch_bounds__(kKeepThreads, 2) kv_keep_few(const __grid_constant__ Keep a) {
+  extern __shared__ int4 rows[]; /* [n_picks], offsets [n + 1], sequences, starts [n], a bit a row */
   const Params &p = a.p;
   const int tid = threadIdx.x, n = p.n;
-  for (int i = tid; i < (p.n_seqs + 31) / 32; i += kMoveThreads) claim[i] = 0;
+  int *off = (int *)(rows + a.n_picks), *seq = off + n + 1, *start = seq + n;
+  unsigned *claim = (unsigned *)(start + n);
+  __shared__ int s_flags; /* 1: entries, 2: picks out of range, 4: picks wrong */
+  for (int i = tid; i < (p.n_seqs + 31) / 32; i += kKeepThreads) claim[i] = 0;
+  if (tid == 0) s_flags = 0;
   wait_for_previous();
   dependents_may_launch();
   const int held_up = __ldcg(&p.ctrl->status); /* by an earlier refusal, or another block's of this call */
-  for (int i = tid; i <= n; i += kMoveThreads) off[i] = __ldcg(a.offsets + i);
-  __syncthreads();
-  bool wrong = false;
-  for (int i = tid; i < n; i += kMoveThreads) {
-    const int s = __ldcg(p.a + i);
-    if (!keep_sound(a, i, s, off[i], off[i + 1]))
-      wrong = true;
-    else
-      wrong |= (atomicOr(claim + s / 32, 1u << s % 32) >> s % 32) & 1;
-  }
-  wrong = __syncthreads_or(wrong);
-  bool outside = false;
-  if (!wrong) {
-    for (int k = tid; k < off[n]; k += kMoveThreads) {
-      int lo = 0, hi = n - 1; /* the last entry that begins at or before it */
-      while (lo < hi) {
-        const int m = (lo + hi + 1) >> 1;
-        if (off[m] <= k)
-          lo = m;
-        else
-          hi = m - 1;
-      }
-      const int e = keep_pick(a, lo, __ldcg(p.a + lo), k, k - off[lo], rows + k);
-      outside |= e == MK_ERR_PAGE_OOB;
-      wrong |= e == MK_ERR_INVALID_ARG;
+  int pick = tid < a.n_picks ? __ldcg(a.picks + tid) : 0;
+  int before = tid && tid < a.n_picks ? __ldcg(a.picks + tid - 1) : -1;
+  for (int i = tid; i <= n; i += kKeepThreads) {
+    off[i] = __ldcg(a.offsets + i);
+    if (i < n) {
+      seq[i] = __ldcg(p.a + i);
+      start[i] = __ldcg(a.starts + i);
     }
-    outside = __syncthreads_or(outside);
-    wrong = __syncthreads_or(wrong);
   }
+  __syncthreads();
+  int flags = 0;
+  for (int i = tid; i < n; i += kKeepThreads) {
+    const int s = seq[i];
+    if (!keep_sound(a, i, s, off[i], off[i + 1]) || (atomicOr(claim + s / 32, 1u << s % 32) >> s % 32 & 1)) flags |= 1;
+  }
+  const int used = min(off[n], a.n_picks);
+  for (int k = tid; k < used; k += kKeepThreads) {
+    if (k != tid) {
+      pick = __ldcg(a.picks + k);
+      before = __ldcg(a.picks + k - 1);
+    }
+    int lo = 0, hi = n - 1; /* the last entry that begins at or before it, where offsets are in order */
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (off[m] <= k)
+        lo = m;
+      else
+        hi = m - 1;
+    }
+    const int j = k - off[lo], s = seq[lo];
+    rows[k] = make_int4(-1, 0, -1, 0);
+    if (j < 0 || (unsigned)s >= (unsigned)p.n_seqs) continue; /* an entry that is not sound */
+    const int e = keep_pick(a, s, start[lo], pick, j ? before : -1, j, rows + k);
+    flags |= e == MK_ERR_PAGE_OOB ? 2 : e ? 4 : 0;
+  }
+  if (flags) atomicOr(&s_flags, flags);
+  __syncthreads();
+  const unsigned nwarp = gridDim.x * (kKeepThreads / 32), all = a.warps * n;
+  unsigned w = (blockIdx.x * kKeepThreads + tid) >> 5;
+  const bool sound = !(s_flags & 1) && w < all; /* its entries: else their rows are not in order */
+  int i = sound ? (int)(w / a.warps) : 0, first = sound ? off[i] : 0, count = sound ? off[i + 1] - first : 0;
+  Mover m(a, w - i * a.warps);
+  auto rows_of = [&](int j) { return rows[first + j]; };
+  m.load(0, count, rows_of);
+  if (!(s_flags & 1))
+    for (int k = tid; k < used; k += kKeepThreads) {
+      const int e = keep_holders(a, rows[k]);
+      if (e) atomicOr(&s_flags, e == MK_ERR_PAGE_OOB ? 2 : 4);
+    }
+  __syncthreads();
   if (held_up) return;
-  if (outside || wrong) {
+  if (s_flags) {
     if (blockIdx.x == 0 && tid == 0) {
-      const int err = outside ? MK_ERR_PAGE_OOB : MK_ERR_INVALID_ARG;
+      const int err = s_flags & 1 ? MK_ERR_INVALID_ARG : s_flags & 2 ? MK_ERR_PAGE_OOB : MK_ERR_INVALID_ARG;
       p.ctrl->status = err;
       *(volatile int32_t *)p.err_host = err;
       __threadfence_system();
     }
     return;
   }
-  const unsigned nwarp = gridDim.x * (kMoveThreads / 32), all = a.warps * n;
-  for (unsigned w = (blockIdx.x * kMoveThreads + tid) >> 5; w < all; w += nwarp) {
-    const int i = (int)(w / a.warps);
-    const int4 *mine = rows + off[i];
-    keep_move(a, w - i * a.warps, off[i + 1] - off[i], [&](int j) { return mine[j]; });
+  while (true) {
+    m.store();
+    for (int j0 = 8; j0 < count; j0 += 8) {
+      m.load(j0, count, rows_of);
+      m.store();
+    }
+    w += nwarp;
+    if (w >= all) break;
+    i = (int)(w / a.warps);
+    first = off[i];
+    count = off[i + 1] - first;
+    m = Mover(a, w - i * a.warps);
+    m.load(0, count, rows_of);
   }
 }
 
@@ -892,6 +955,9 @@ mk_status mk_kv_create(const mk_kv_desc *d, void *stream, mk_kv **out) {
   if (e == cudaSuccess) e = allow_clusters(kv_plan<OP_RESIZE>, &kv->max_cluster);
   if (e == cudaSuccess) e = allow_clusters(kv_plan<OP_COMPACT>, &kv->max_cluster);
   if (e == cudaSuccess) e = allow_clusters(kv_keep_plan, &kv->max_cluster);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kv_keep_few, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             keep_few_bytes(kFewKept, kFewPicks, 65536));
   if (e == cudaSuccess) e = cudaMalloc(&kv->ws, off);
   if (e == cudaSuccess) e = cudaMemsetAsync(kv->ws, 0, off, kv->stream);
   if (e == cudaSuccess)
@@ -1022,9 +1088,9 @@ mk_status mk_kv_keep(mk_kv *kv, int32_t n, const int32_t *seqs, const int32_t *s
   const long long warps = (long long)a.warps * n;
   const unsigned blocks = (unsigned)std::min((warps + kMoveThreads / 32 - 1) / (kMoveThreads / 32), (long long)kv->n_sm * 4);
   if (n <= kFewKept && n_picks <= kFewPicks) {
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.dynamicSmemBytes = (size_t)n_picks * 16 + (n + 1) * 4 + ((size_t)kv->d.n_seqs + 31) / 32 * 4;
+    cfg.gridDim = dim3((unsigned)std::min((warps + kKeepThreads / 32 - 1) / (kKeepThreads / 32), (long long)kv->n_sm * 2));
+    cfg.blockDim = dim3(kKeepThreads);
+    cfg.dynamicSmemBytes = keep_few_bytes(n, n_picks, kv->d.n_seqs);
     return cudaLaunchKernelEx(&cfg, kv_keep_few, a) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
   }
   cfg.gridDim = dim3(kv->max_cluster);

@@ -169,7 +169,7 @@ constexpr size_t words_bytes(int slice) { return (size_t)slice * 6 + slice / 8; 
  * masked and copied; those with a word, few as a rule, get their rules behind that, densely, from
  * the list.  What a row needs next is loaded while the row before it is under way: its arguments and
  * logits, then its path, biases and mask. */
-template <class T, bool VEC, int AHEAD>
+template <class T, bool VEC, int AHEAD, bool LIST>
 __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant__ Args a) {
   constexpr int STEP = VEC ? 1 : kThreads, CHUNK = 4 * kThreads; /* AHEAD chunks' logits are under way */
   extern __shared__ uint4 shared[];
@@ -263,13 +263,19 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
       }
       int next_word = 0;
       if (more && warp == kWarps - 1 && lane < kRowWords) next_word = loader(next_row);
+      const bool readable = is_sound;
       bool wrong = !is_sound;
       const int n_bias = r.bias1 - r.bias0;
       int own_path = -1, own_bias = -1; /* this thread's first words of the row's own */
+      auto add = [&](int t, uint32_t count, uint32_t flag) {
+        const uint32_t before = flag ? atomicOr(ws.word + t, flag) : atomicAdd(ws.word + t, count);
+        if (LIST) ws.mark(t, before, &s_length);
+      };
       if (counts && is_sound) {
         if (slice != at_slice || r.begin != at_begin || r.end != at_end || r.prompt != at_prompt) {
           for (int i = tid; i < a.slice / 4; i += kThreads) ((uint4 *)ws.word)[i] = make_uint4(0, 0, 0, 0);
-          for (int i = tid; i < a.slice / 32; i += kThreads) ws.marked[i] = 0;
+          if (LIST)
+            for (int i = tid; i < a.slice / 32; i += kThreads) ws.marked[i] = 0;
           __syncthreads();
           for (int i0 = r.begin + tid; i0 < r.end; i0 += 8 * kThreads) {
             int t[8];
@@ -282,30 +288,32 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
                 atomicOr(ws.word + t[k], kPrompt);
               else
                 atomicAdd(ws.word + t[k], 1u);
-              atomicOr(ws.marked + t[k] / 32, 1u << t[k] % 32);
+              if (LIST) atomicOr(ws.marked + t[k] / 32, 1u << t[k] % 32);
             }
           }
-          __syncthreads();
-          /* the list, in order: a thread has one word of the bits */
-          uint32_t bits = tid < a.slice / 32 ? ws.marked[tid] : 0;
-          const int mine = __popc(bits);
-          int before = mine;
+          if (LIST) {
+            __syncthreads();
+            /* the list, in order: a thread has one word of the bits */
+            uint32_t bits = tid < a.slice / 32 ? ws.marked[tid] : 0;
+            const int mine = __popc(bits);
+            int before = mine;
 #pragma unroll
-          for (int o = 1; o < 32; o *= 2) {
-            const int y = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += y;
-          }
-          if (lane == 31) s_id[warp] = before;
-          __syncthreads();
-          int to = before - mine, all = 0;
+            for (int o = 1; o < 32; o *= 2) {
+              const int y = __shfl_up_sync(0xffffffffu, before, o);
+              if (lane >= o) before += y;
+            }
+            if (lane == 31) s_id[warp] = before;
+            __syncthreads();
+            int to = before - mine, all = 0;
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) to += s_id[w];
-            all += s_id[w];
+            for (int w = 0; w < kWarps; ++w) {
+              if (w < warp) to += s_id[w];
+              all += s_id[w];
+            }
+            for (; bits; bits &= bits - 1) ws.list[to++] = (uint16_t)(tid * 32 + __ffs(bits) - 1);
+            if (tid == 0) s_length = s_history = all;
+            __syncthreads();
           }
-          for (; bits; bits &= bits - 1) ws.list[to++] = (uint16_t)(tid * 32 + __ffs(bits) - 1);
-          if (tid == 0) s_length = s_history = all;
-          __syncthreads();
           at_slice = slice;
           at_begin = r.begin;
           at_end = r.end;
@@ -313,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
         }
         if (path_id >= v0 && path_id - v0 < nv) {
           own_path = path_id - v0;
-          ws.mark(own_path, atomicAdd(ws.word + own_path, 1u), &s_length);
+          add(own_path, 1, 0);
         }
         if (tid < n_bias) {
           wrong = (unsigned)bias_id >= (unsigned)a.vocab || bias_before >= bias_id;
@@ -321,22 +329,38 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
           s_bias[tid] = bias;
           if (bias_id >= v0 && bias_id - v0 < nv) {
             own_bias = bias_id - v0;
-            ws.mark(own_bias, atomicOr(ws.word + own_bias, kBias), &s_length);
+            add(own_bias, 0, kBias);
           }
         }
         for (int i = r.path0 + tid + kThreads; i < r.path1; i += kThreads) {
           const int t = __ldcg(b.path_tokens + i) - v0;
-          if ((unsigned)t < (unsigned)nv) ws.mark(t, atomicAdd(ws.word + t, 1u), &s_length);
+          if ((unsigned)t < (unsigned)nv) add(t, 1, 0);
         }
         for (int i = r.bias0 + tid + kThreads; i < r.bias1; i += kThreads) {
           const int id = __ldcg(b.bias_tokens + i), t = id - v0;
           wrong |= (unsigned)id >= (unsigned)a.vocab || __ldcg(b.bias_tokens + i - 1) >= id;
-          if ((unsigned)t < (unsigned)nv) ws.mark(t, atomicOr(ws.word + t, kBias), &s_length);
+          if ((unsigned)t < (unsigned)nv) add(t, 0, kBias);
         }
         wrong = __syncthreads_or(wrong);
       }
       if (wrong && tid == 0) report(a.err, MK_ERR_INVALID_ARG);
-      const int length = counts && is_sound ? s_length : 0;
+      const int length = LIST && counts && is_sound ? s_length : 0;
+      const Penalty penalty(r);
+      auto ruled = [&](float x, uint32_t word, int id) {
+        float y = penalty(x, word);
+        if (word & kBias) {
+          int at = 0, e = n_bias - 1; /* the last bias token at or below id: id itself */
+          while (at < e) {
+            const int m = (at + e + 1) >> 1;
+            if ((m < kThreads ? s_id[m] : __ldcg(b.bias_tokens + r.bias0 + m)) <= id)
+              at = m;
+            else
+              e = m - 1;
+          }
+          y = __fadd_rn(y, at < kThreads ? s_bias[at] : __ldcg(b.bias + r.bias0 + at));
+        }
+        return y;
+      };
       const T *src = (const T *)a.logits + row * a.row_stride + v0;
       float *dst = a.out ? a.out + (long long)row * a.vocab + v0 : nullptr;
       const uint32_t *masks = r.mask >= 0 && !wrong ? b.allowed + (size_t)r.mask * mask_words + v0 / 32 : nullptr;
@@ -376,6 +400,27 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
             }
           }
           float y[4] = {x.x, x.y, x.z, x.w}, z[4];
+          if (!LIST && counts) {
+            uint32_t w[4];
+            if (VEC) {
+              *(uint4 *)w = *(const uint4 *)(ws.word + c0 + k * CHUNK + mine);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] = rest >> j & 1 ? ws.word[c0 + k * CHUNK + mine + j * STEP] : 0;
+            }
+            uint32_t todo = (w[0] ? 1 : 0) | (w[1] ? 2 : 0) | (w[2] ? 4 : 0) | (w[3] ? 8 : 0);
+#pragma unroll 1
+            for (; todo; todo &= todo - 1) { /* one or two of the four, as a rule */
+              const int j = __ffs(todo) - 1;
+              const float z = ruled(j == 0 ? y[0] : j == 1 ? y[1] : j == 2 ? y[2] : y[3],
+                                    j == 0 ? w[0] : j == 1 ? w[1] : j == 2 ? w[2] : w[3],
+                                    v0 + c0 + k * CHUNK + mine + j * STEP);
+              y[0] = j == 0 ? z : y[0];
+              y[1] = j == 1 ? z : y[1];
+              y[2] = j == 2 ? z : y[2];
+              y[3] = j == 3 ? z : y[3];
+            }
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (!(ok >> j & 1)) y[j] = -INFINITY;
@@ -404,7 +449,6 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
       unsigned long long key = at >= 0 ? best_key(top, v0 + at) : 0;
       if (more && warp == kWarps - 1 && lane < kRowWords) ((int *)&s_row[(n + 1) & 1])[lane] = next_word;
       if (length) {
-        const Penalty penalty(r);
 #pragma unroll 1
         for (int k0 = 0; k0 < length; k0 += 4 * kThreads) {
           int t[4];
@@ -424,19 +468,7 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (t[j] < 0) continue;
-            const uint32_t word = ws.word[t[j]];
-            float y = penalty(x[j], word);
-            if (word & kBias) {
-              int at = 0, e = n_bias - 1; /* the last bias token at or below t: t itself */
-              while (at < e) {
-                const int m = (at + e + 1) >> 1;
-                if ((m < kThreads ? s_id[m] : __ldcg(b.bias_tokens + r.bias0 + m)) <= v0 + t[j])
-                  at = m;
-                else
-                  e = m - 1;
-              }
-              y = __fadd_rn(y, at < kThreads ? s_bias[at] : __ldcg(b.bias + r.bias0 + at));
-            }
+            float y = ruled(x[j], ws.word[t[j]], v0 + t[j]);
             if (!(may[j] >> t[j] % 32 & 1)) y = -INFINITY;
             if (dst) __stcs(dst + t[j], y);
             if (y > -INFINITY) key = max(key, best_key(y, v0 + t[j]));
@@ -455,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
         s_best = 0;
         if (best) atomicMax(a.best + row, best);
       }
-      if (length) { /* the row's own words out again */
+      if (counts && readable) { /* the row's own words out again */
         if (own_path >= 0) atomicSub(ws.word + own_path, 1u);
         if (own_bias >= 0) atomicAnd(ws.word + own_bias, ~kBias);
         for (int i = r.path0 + tid + kThreads; i < r.path1; i += kThreads) {
@@ -466,9 +498,11 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
           const unsigned t = (unsigned)(__ldcg(b.bias_tokens + i) - v0);
           if (t < (unsigned)nv) atomicAnd(ws.word + t, ~kBias);
         }
-        for (int k = s_history + tid; k < length; k += kThreads)
-          atomicAnd(ws.marked + ws.list[k] / 32, ~(1u << ws.list[k] % 32));
-        if (tid == 0) s_length = s_history;
+        if (LIST) {
+          for (int k = s_history + tid; k < length; k += kThreads)
+            atomicAnd(ws.marked + ws.list[k] / 32, ~(1u << ws.list[k] % 32));
+          if (tid == 0) s_length = s_history;
+        }
       }
       if (more) {
         r = s_row[(n + 1) & 1];
@@ -511,12 +545,15 @@ namespace {
 
 typedef void (*Kernel)(Args);
 template <class T, bool VEC>
-Kernel of_slice(int slice) { /* AHEAD divides a slice's chunks */
-  return slice >= 4 * kLeast ? apply_rules<T, VEC, 4> : slice == 2 * kLeast ? apply_rules<T, VEC, 2> : apply_rules<T, VEC, 1>;
+Kernel of_slice(int slice, bool list) { /* AHEAD divides a slice's chunks */
+  return list                    ? apply_rules<T, VEC, 4, true>
+         : slice >= 4 * kLeast   ? apply_rules<T, VEC, 4, false>
+         : slice == 2 * kLeast   ? apply_rules<T, VEC, 2, false>
+                                 : apply_rules<T, VEC, 1, false>;
 }
-Kernel kernel_of(bool bf16, bool vec, int slice) {
-  return bf16 ? vec ? of_slice<__nv_bfloat16, true>(slice) : of_slice<__nv_bfloat16, false>(slice)
-         : vec ? of_slice<float, true>(slice) : of_slice<float, false>(slice);
+Kernel kernel_of(bool bf16, bool vec, int slice, bool list) {
+  return bf16 ? vec ? of_slice<__nv_bfloat16, true>(slice, list) : of_slice<__nv_bfloat16, false>(slice, list)
+         : vec ? of_slice<float, true>(slice, list) : of_slice<float, false>(slice, list);
 }
 
 }  // namespace
@@ -538,7 +575,8 @@ mk_status mk_rules_create(int32_t vocab, int32_t max_rows, void *stream, mk_rule
   const size_t bytes = 64 + 8 * (size_t)max_rows;
   cudaError_t e = cudaSuccess;
   for (int i = 0; i < 4 && e == cudaSuccess; ++i)
-    e = cudaFuncSetAttribute(kernel_of(i / 2, i % 2, kSlice), cudaFuncAttributeMaxDynamicSharedMemorySize, (int)words_bytes(kSlice));
+    e = cudaFuncSetAttribute(kernel_of(i / 2, i % 2, kSlice, true), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)words_bytes(kSlice));
   if (e == cudaSuccess) e = cudaMalloc(&m->ws, bytes);
   if (e == cudaSuccess) e = cudaMemsetAsync(m->ws, 0, bytes, m->stream);
   if (e == cudaSuccess) e = cudaStreamSynchronize(m->stream);
@@ -608,6 +646,7 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
    * 20.5; large slices cost a row less, 384 rows 117 us, with 4096 tokens a slice 158) */
   a.slice = kSlice;
   while (a.slice > kLeast && (V + a.slice - 1) / a.slice * b->n_rows < 2 * m->n_sm) a.slice /= 2;
+  const bool list = a.slice == kSlice;
   a.slices = (int32_t)((V + a.slice - 1) / a.slice);
   const bool vec = V % 4 == 0 && row_stride % 4 == 0 && aligned(logits, 4 * (unsigned)size) && aligned(out, 16);
   cudaLaunchAttribute at[1];
@@ -616,11 +655,11 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)a.slices * b->n_rows, m->n_sm * 4));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = words_bytes(a.slice);
+  cfg.dynamicSmemBytes = list ? words_bytes(a.slice) : (size_t)a.slice * 4;
   cfg.stream = m->stream;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel_of(is_bf16 != 0, vec, a.slice), a) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel_of(is_bf16 != 0, vec, a.slice, list), a) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
 
 mk_status mk_rules_sync(mk_rules *m) {

@@ -24,6 +24,7 @@ class TokenRules:
             raise ValueError("the device has to be a CUDA device")
         if self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
+        self._index = self.device.index
         self.vocab, self.max_rows = vocab, max_rows
         self._f32, self._bf16, self._int32 = torch.float32, torch.bfloat16, torch.int32
         self._lib = lib()
@@ -95,18 +96,18 @@ class TokenRules:
         or bfloat16 with any row stride, under the batch's rules; tokens int32 [n_rows] (None: not
         wanted) the largest one's id in each row, -1 where none may follow."""
         n = batch.n_rows
-        if (logits.shape != (n, self.vocab) or logits.dtype not in (self._f32, self._bf16)
-                or logits.device != self.device or (self.vocab > 1 and logits.stride(1) != 1)):
+        stride, half = logits.stride(), logits.dtype is self._bf16
+        if (logits.shape != (n, self.vocab) or not (half or logits.dtype is self._f32)
+                or logits.get_device() != self._index or (self.vocab > 1 and stride[1] != 1)):
             raise ValueError(f"logits has to be float32 or bfloat16 {(n, self.vocab)} with contiguous "
                              f"rows on {self.device}")
         for t, what, dtype, shape in ((out, "out", self._f32, (n, self.vocab)), (tokens, "tokens", self._int32, (n,))):
-            if t is not None and (t.dtype is not dtype or t.shape != shape or t.device != self.device
+            if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != self._index
                                   or not t.is_contiguous()):
                 raise ValueError(f"{what} has to be contiguous {dtype} {shape} on {self.device}")
         _check(self._lib.mk_rules_apply(
-            self.handle, ctypes.byref(batch), logits.data_ptr(), int(logits.dtype is self._bf16),
-            logits.stride(0) if n > 1 else self.vocab, None if out is None else out.data_ptr(),
-            None if tokens is None else tokens.data_ptr()), "mk_rules_apply")
+            self.handle, ctypes.byref(batch), logits.data_ptr(), half, stride[0] if n > 1 else self.vocab,
+            None if out is None else out.data_ptr(), None if tokens is None else tokens.data_ptr()), "mk_rules_apply")
 
     def sync(self):
         """Waits for the stream; raises the MkError of the first device error."""
