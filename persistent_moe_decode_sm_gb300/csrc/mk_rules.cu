@@ -150,6 +150,9 @@ struct Penalty {
   }
 };
 
+/* An id's place in a slice that begins at v0; any id, so in unsigned numbers. */
+__device__ __forceinline__ int less(int id, int v0) { return (int)((unsigned)id - (unsigned)v0); }
+
 /* A block's slice: a word for each token, which tokens have one, and those tokens in no order. */
 struct Words {
   uint32_t *word, *marked; /* [slice], [slice / 32] bits */
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
           for (int i0 = r.begin + tid; i0 < r.end; i0 += 8 * kThreads) {
             int t[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) t[k] = i0 + k * kThreads < r.end ? __ldcg(b.tokens + i0 + k * kThreads) - v0 : -1;
+            for (int k = 0; k < 8; ++k) t[k] = i0 + k * kThreads < r.end ? less(__ldcg(b.tokens + i0 + k * kThreads), v0) : -1;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               if ((unsigned)t[k] >= (unsigned)nv) continue;
@@ -333,11 +336,11 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
           }
         }
         for (int i = r.path0 + tid + kThreads; i < r.path1; i += kThreads) {
-          const int t = __ldcg(b.path_tokens + i) - v0;
+          const int t = less(__ldcg(b.path_tokens + i), v0);
           if ((unsigned)t < (unsigned)nv) add(t, 1, 0);
         }
         for (int i = r.bias0 + tid + kThreads; i < r.bias1; i += kThreads) {
-          const int id = __ldcg(b.bias_tokens + i), t = id - v0;
+          const int id = __ldcg(b.bias_tokens + i), t = less(id, v0);
           wrong |= (unsigned)id >= (unsigned)a.vocab || __ldcg(b.bias_tokens + i - 1) >= id;
           if ((unsigned)t < (unsigned)nv) add(t, 0, kBias);
         }
@@ -491,11 +494,11 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
         if (own_path >= 0) atomicSub(ws.word + own_path, 1u);
         if (own_bias >= 0) atomicAnd(ws.word + own_bias, ~kBias);
         for (int i = r.path0 + tid + kThreads; i < r.path1; i += kThreads) {
-          const unsigned t = (unsigned)(__ldcg(b.path_tokens + i) - v0);
+          const unsigned t = less(__ldcg(b.path_tokens + i), v0);
           if (t < (unsigned)nv) atomicSub(ws.word + t, 1u);
         }
         for (int i = r.bias0 + tid + kThreads; i < r.bias1; i += kThreads) {
-          const unsigned t = (unsigned)(__ldcg(b.bias_tokens + i) - v0);
+          const unsigned t = less(__ldcg(b.bias_tokens + i), v0);
           if (t < (unsigned)nv) atomicAnd(ws.word + t, ~kBias);
         }
         if (LIST) {

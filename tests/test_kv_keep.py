@@ -281,6 +281,28 @@ def test_four_dimensional_pools_name_their_heads():
 
 
 @gpu
+def test_pages_behind_two_to_the_32():
+    import torch
+
+    pages = (1 << 32) // (2 * 16 * 128 * 2) + 900            # 8 KB a page
+    pool = torch.zeros(pages, 2, 16, 128, dtype=torch.bfloat16, device="cuda")
+    t = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    tables, lens = t([pages - 1, pages - 800]), t(30)
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+    refs[[pages - 1, pages - 800]] = 1
+    rows = torch.randn(30, 2, 128, device="cuda").to(torch.bfloat16)
+    for i in range(30):
+        pool[(pages - 1, pages - 800)[i // 16], :, i % 16] = rows[i]
+    c = mk.KvCache([pool], tables, lens, refs, 16)
+    c.keep(t(0), t(10), t(0, 4), t(1, 4, 9, 19))
+    c.sync()
+    want = rows.clone()
+    want[10:14] = rows[[11, 14, 19, 29]]
+    for i in range(30):
+        assert torch.equal(pool[(pages - 1, pages - 800)[i // 16], :, i % 16], want[i])
+
+
+@gpu
 def test_captured_calls_follow_their_tensors():
     import torch
 

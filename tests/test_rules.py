@@ -3,7 +3,9 @@
 The definition rounds each step to 32 bits by itself, so the results equal numpy's float32, step
 by step, bit for bit.  Against the formula in 64 bits: at most five steps round (division or
 product; frequency times count; two differences; bias), each by 2^-24 of a value no larger than
-the sum of the terms' magnitudes: 5 * 2^-24, taken as 2^-21, of that sum."""
+the sum of the terms' magnitudes: 5 * 2^-24, taken as 2^-21, of that sum.  A step whose result lies
+below 2^-126 rounds by half of the smallest step, 2^-150, instead: 5 * 2^-150 are below 2^-147.  Where
+the sum passes 2^127 a step may go to infinity, which the formula does not: there only the steps count."""
 import ctypes
 
 import numpy as np
@@ -103,8 +105,8 @@ class Case:
                 y = np.where(known, np.where(x64 > 0, x64 / r, x64 * r), x64)
                 size = np.abs(y) + np.where(c > 0, np.abs(f) * c + np.abs(p), 0) + np.abs(b)
                 y = y - np.where(c > 0, np.float64(f) * c + p, 0) + np.where(has, b, 0)
-                fine = np.isfinite(y)
-                assert (np.abs(x - y)[fine] <= 2.0 ** -21 * size[fine]).all()
+                fine = np.isfinite(y) & (size < 2.0 ** 127)
+                assert (np.abs(x - y)[fine] <= 2.0 ** -21 * size[fine] + 2.0 ** -147).all()
             x = np.where(may, x, f32(-np.inf)).astype(f32)
             rows.append(x)
             z = np.where(np.isnan(x), -np.inf, x)
@@ -203,6 +205,45 @@ def test_strides(vocab, stride, bf16):
 
 
 @gpu
+@pytest.mark.parametrize("vocab, bf16", [(9000, False), (9000, True), (9001, False), (9001, True)])
+@pytest.mark.parametrize("what", ["both", "out", "tokens", "in place"])
+def test_many_rows(vocab, bf16, what):
+    """Enough rows for the largest slices, whose tokens with a word are listed."""
+    if bf16 and what == "in place":
+        return
+    Case(vocab, 360, 40, bf16, history=400, share=5, path=4, bias=30, masks=6).check(what)
+    Case(vocab, 330, 41, bf16, history=None, bias=3).check(what)
+    Case(vocab, 330, 42, bf16, history=30, share=2).check(what)
+
+
+@gpu
+def test_dense_rows():
+    """More biases than a block's threads, paths longer than that, and a history that has most tokens."""
+    Case(3000, 3, 43, history=9000, path=700, bias=3000, masks=2).check()
+    Case(9000, 320, 44, history=9000, share=40, path=700, bias=1500, masks=2).check()
+
+
+@gpu
+def test_penalties_over_the_whole_range():
+    """The quotient is rounded once everywhere: near the ends, at zero, with and without a remainder."""
+    for seed in range(4):
+        c = Case(20000, 4, seed, history=60000, kinds="r")
+        rng = np.random.default_rng(seed)
+        e = rng.integers(-149, 128, (4, 20000)) if seed % 2 else rng.integers(-20, 20, (4, 20000))
+        c.x = c.t.from_numpy(np.ldexp(rng.uniform(-2, 2, (4, 20000)), e).astype(np.float32))
+        c.x[:, ::97] = 0.0
+        c.rep = np.float32([[1e-38, 1e38, 3.0, np.inf], [0.1, 7.0, 1e-3, 1.0 / 3], [1.2, 1.1, 1.7, 1.3],
+                            [2.0 ** -30, 2.0 ** 30, 2.0 ** -29, 1.0000001]][seed])
+        c.check()
+
+
+@gpu
+def test_the_largest_vocabulary():
+    c = Case(1 << 24, 1, 45, history=50, bias=10)
+    c.check()
+
+
+@gpu
 def test_padding_ids_and_masks_by_row():
     Case(700, 12, 6, history=50, share=2, pad=True, path=5).check()
     c = Case(700, 6, 7, masks=9)
@@ -290,10 +331,11 @@ WRONG = [("ranges", (1, 0), -1), ("ranges", (1, 1), 10 ** 6), ("ranges", (1, 0),
 
 
 @gpu
+@pytest.mark.parametrize("rows", [6, 340])
 @pytest.mark.parametrize("name, at, value", WRONG)
-def test_wrong_rows_are_not_written(name, at, value):
+def test_wrong_rows_are_not_written(name, at, value, rows):
     """The other rows are right; offsets belong to the rows on both their sides."""
-    c = Case(9000, 6, 13, path=4, bias=6, masks=3)
+    c = Case(9000, rows, 13, path=4, bias=6, masks=3)
     a = getattr(c, name)
     good = a.copy()
     a[at] = value
@@ -309,10 +351,11 @@ def test_wrong_rows_are_not_written(name, at, value):
 
 
 @gpu
+@pytest.mark.parametrize("rows", [4, 340])
 @pytest.mark.parametrize("ids", [[5, 5, 7], [7, 5, 9], [-1, 5, 7], [5, 7, 9000], [5, 2 ** 31 - 1, 7]])
-def test_bias_tokens_that_do_not_rise(ids):
-    c = Case(9000, 4, 14, history=20, masks=2)
-    c.boff = np.array([0, 2, 5, 5, 7], np.int32)
+def test_bias_tokens_that_do_not_rise(ids, rows):
+    c = Case(9000, rows, 14, history=20, masks=2)
+    c.boff = np.array([0, 2, 5, 5] + [7] * (rows - 3), np.int32)
     c.bids = np.array([1, 8999] + [3, 4, 5] + [0, 4000], np.int32)
     c.bias = np.arange(7).astype(np.float32)
     bad = c.bids.copy()
