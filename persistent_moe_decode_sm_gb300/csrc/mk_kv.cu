@@ -587,13 +587,21 @@ __device__ __forceinline__ int keep_holders(const Keep &a, const int4 &rows) {
   return to > 1 && (rows.x != rows.z || rows.y != rows.w) ? MK_ERR_INVALID_ARG : MK_OK;
 }
 
+/* Where a token's row begins in a pool's head 0, in bytes: now (x, -1 where that cannot be told) and
+ * afterwards (y). */
+__device__ __forceinline__ longlong2 keep_bytes(const Keep &a, const int4 &rows) {
+  const long long row_bytes = 16ll * a.row_chunks;
+  return rows.x < 0 ? make_longlong2(-1, -1)
+                    : make_longlong2(rows.x * a.p.page_bytes + rows.y * row_bytes,
+                                     rows.z * a.p.page_bytes + rows.w * row_bytes);
+}
+
 /* A warp's 32 pieces of every picked token of one sequence.  A lane has the same 16 bytes of each,
  * and takes them in order, eight loads ahead of their stores: a token goes to a place at or before
- * its own and the picks rise, so no store touches what is still to be loaded.  `rows_of` gives the
- * rows of one pick to all lanes. */
+ * its own and the picks rise, so no store touches what is still to be loaded.  `bytes_of` gives
+ * keep_bytes of one pick to all lanes. */
 struct Mover {
   char *base;
-  long long row_bytes, page_bytes;
   bool mine;
   uint4 v[8];
   char *to[8];
@@ -603,20 +611,18 @@ struct Mover {
     mine = unit < a.units;
     const int per_pool = a.heads * a.row_chunks, pool = mine ? unit / per_pool : 0;
     const int rest = unit - pool * per_pool, head = rest / a.row_chunks;
-    row_bytes = 16ll * a.row_chunks;
-    page_bytes = p.page_bytes;
-    base = p.pools[pool] + (long long)head * p.page_size * row_bytes + (rest - head * a.row_chunks) * 16;
+    base = p.pools[pool] + (long long)head * p.page_size * (16ll * a.row_chunks) + (rest - head * a.row_chunks) * 16;
   }
   template <class F>
-  __device__ __forceinline__ void load(int j0, int count, F rows_of) {
+  __device__ __forceinline__ void load(int j0, int count, F bytes_of) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       to[k] = nullptr;
       if (j0 + k >= count) continue;
-      const int4 r = rows_of(j0 + k);
-      if (!mine || r.x < 0 || (r.x == r.z && r.y == r.w)) continue;
-      to[k] = base + r.z * page_bytes + r.w * row_bytes;
-      v[k] = __ldcg((const uint4 *)(base + r.x * page_bytes + r.y * row_bytes));
+      const longlong2 at = bytes_of(j0 + k);
+      if (!mine || at.x < 0 || at.x == at.y) continue;
+      to[k] = base + at.y;
+      v[k] = __ldcg((const uint4 *)(base + at.x));
     }
   }
   __device__ __forceinline__ void store() const {
@@ -685,16 +691,18 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_keep_rows(const __grid_con
     const int i = (int)(w / a.warps);
     const int s = __ldcg(a.p.a + i), lo = __ldcg(a.offsets + i), n = __ldcg(a.offsets + i + 1) - lo;
     const int start = __ldcg(a.starts + i);
-    int4 mine;
-    auto rows_of = [&](int j) {
-      if (j % 32 == 0 && j + lane < n)
-        keep_pick(a, s, start, __ldcg(a.picks + lo + j + lane), -1, j + lane, &mine);
-      return make_int4(__shfl_sync(0xffffffffu, mine.x, j & 31), __shfl_sync(0xffffffffu, mine.y, j & 31),
-                       __shfl_sync(0xffffffffu, mine.z, j & 31), __shfl_sync(0xffffffffu, mine.w, j & 31));
+    longlong2 mine;
+    auto bytes_of = [&](int j) {
+      if (j % 32 == 0 && j + lane < n) {
+        int4 rows;
+        keep_pick(a, s, start, __ldcg(a.picks + lo + j + lane), -1, j + lane, &rows);
+        mine = keep_bytes(a, rows);
+      }
+      return make_longlong2(__shfl_sync(0xffffffffu, mine.x, j & 31), __shfl_sync(0xffffffffu, mine.y, j & 31));
     };
     Mover m(a, (unsigned)(w - (unsigned long long)i * a.warps));
     for (int j0 = 0; j0 < n; j0 += 8) {
-      m.load(j0, n, rows_of);
+      m.load(j0, n, bytes_of);
       m.store();
     }
   }
@@ -704,17 +712,17 @@ __global__ void __launch_bounds__(kMoveThreads, 4) kv_keep_rows(const __grid_con
  * them, so that none waits for another, and finds their rows on the way.  Three loads in a row
  * (picks, tables, and holders with the first rows under way) and two barriers stand before the first
  * store.  64 paths of up to 8 tokens in 96 pools, 44 MB read and written in rows of 256 bytes, take
- * 14.4 us, 4 paths in 16 pools 3.6; in blocks of 256 threads, four an SM and each with the same checks
- * to make, 17.2 and 3.3. */
+ * 13.0 us, 4 paths in 16 pools 3.3 (14.4 with pages and places in the list instead of bytes; 17.2 in
+ * blocks of 256 threads, four an SM and each with the same checks to make). */
 constexpr int kFewKept = 1024, kFewPicks = 2048, kKeepThreads = 512;
 constexpr int keep_few_bytes(int n, int n_picks, int n_seqs) {
   return n_picks * 16 + (3 * n + 1) * 4 + (n_seqs + 31) / 32 * 4;
 }
 __global__ void __launch_bounds__(kKeepThreads, 2) kv_keep_few(const __grid_constant__ Keep a) {
-  extern __shared__ int4 rows[]; /* [n_picks], offsets [n + 1], sequences, starts [n], a bit a row */
+  extern __shared__ longlong2 bytes[]; /* keep_bytes [n_picks], offsets [n + 1], sequences, starts [n], a bit a row */
   const Params &p = a.p;
   const int tid = threadIdx.x, n = p.n;
-  int *off = (int *)(rows + a.n_picks), *seq = off + n + 1, *start = seq + n;
+  int *off = (int *)(bytes + a.n_picks), *seq = off + n + 1, *start = seq + n;
   unsigned *claim = (unsigned *)(start + n);
   __shared__ int s_flags; /* 1: entries, 2: picks out of range, 4: picks wrong */
   for (int i = tid; i < (p.n_seqs + 31) / 32; i += kKeepThreads) claim[i] = 0;
@@ -738,6 +746,7 @@ __global__ void __launch_bounds__(kKeepThreads, 2) kv_keep_few(const __grid_cons
     if (!keep_sound(a, i, s, off[i], off[i + 1]) || (atomicOr(claim + s / 32, 1u << s % 32) >> s % 32 & 1)) flags |= 1;
   }
   const int used = min(off[n], a.n_picks);
+  int4 mine = make_int4(-1, 0, -1, 0); /* of this thread's first pick, whose holders are looked up below */
   for (int k = tid; k < used; k += kKeepThreads) {
     if (k != tid) {
       pick = __ldcg(a.picks + k);
@@ -752,9 +761,15 @@ __global__ void __launch_bounds__(kKeepThreads, 2) kv_keep_few(const __grid_cons
         hi = m - 1;
     }
     const int j = k - off[lo], s = seq[lo];
-    rows[k] = make_int4(-1, 0, -1, 0);
+    bytes[k] = make_longlong2(-1, -1);
     if (j < 0 || (unsigned)s >= (unsigned)p.n_seqs) continue; /* an entry that is not sound */
-    const int e = keep_pick(a, s, start[lo], pick, j ? before : -1, j, rows + k);
+    int4 rows;
+    int e = keep_pick(a, s, start[lo], pick, j ? before : -1, j, &rows);
+    bytes[k] = keep_bytes(a, rows);
+    if (k == tid)
+      mine = rows;
+    else if (!e)
+      e = keep_holders(a, rows);
     flags |= e == MK_ERR_PAGE_OOB ? 2 : e ? 4 : 0;
   }
   if (flags) atomicOr(&s_flags, flags);
@@ -764,13 +779,10 @@ __global__ void __launch_bounds__(kKeepThreads, 2) kv_keep_few(const __grid_cons
   const bool sound = !(s_flags & 1) && w < all; /* its entries: else their rows are not in order */
   int i = sound ? (int)(w / a.warps) : 0, first = sound ? off[i] : 0, count = sound ? off[i + 1] - first : 0;
   Mover m(a, w - i * a.warps);
-  auto rows_of = [&](int j) { return rows[first + j]; };
-  m.load(0, count, rows_of);
-  if (!(s_flags & 1))
-    for (int k = tid; k < used; k += kKeepThreads) {
-      const int e = keep_holders(a, rows[k]);
-      if (e) atomicOr(&s_flags, e == MK_ERR_PAGE_OOB ? 2 : 4);
-    }
+  auto bytes_of = [&](int j) { return bytes[first + j]; };
+  m.load(0, count, bytes_of);
+  const int e = keep_holders(a, mine);
+  if (e) atomicOr(&s_flags, e == MK_ERR_PAGE_OOB ? 2 : 4);
   __syncthreads();
   if (held_up) return;
   if (s_flags) {
@@ -785,7 +797,7 @@ __global__ void __launch_bounds__(kKeepThreads, 2) kv_keep_few(const __grid_cons
   while (true) {
     m.store();
     for (int j0 = 8; j0 < count; j0 += 8) {
-      m.load(j0, count, rows_of);
+      m.load(j0, count, bytes_of);
       m.store();
     }
     w += nwarp;
@@ -794,7 +806,7 @@ __global__ void __launch_bounds__(kKeepThreads, 2) kv_keep_few(const __grid_cons
     first = off[i];
     count = off[i + 1] - first;
     m = Mover(a, w - i * a.warps);
-    m.load(0, count, rows_of);
+    m.load(0, count, bytes_of);
   }
 }
 
