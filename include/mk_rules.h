@@ -54,7 +54,7 @@ void mk_rules_destroy(mk_rules *rules);
  *   t may not follow:               x <- -inf
  * logits: DEVICE [n_rows][vocab], fp32 or (is_bf16) bf16, row_stride elements from a row to
  * the next; out: fp32 [n_rows][vocab], contiguous, or NULL; it may be logits itself (fp32,
- * row_stride == vocab) and overlaps them in no other way.  out_tokens: int32 [n_rows] or NULL:
+ * row_stride == vocab) and overlaps them in no other way, nor anything else that the call reads.  out_tokens: int32 [n_rows] or NULL:
  * each row's largest x, ties to the lowest t, NaN never; -1 where none is above -inf.  One of
  * the two is given.  The same call gives the same bits.
  *

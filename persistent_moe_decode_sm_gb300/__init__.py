@@ -437,6 +437,10 @@ class Decoder:
             raise ValueError("the rules belong to another stream than the decoder")
         if rules is not None and out_logits is None:
             raise ValueError("rules need out_logits")
+        if rules is not None:  # refused before the step, which cannot be taken back
+            if rules[1].n_rows != self.batch:
+                raise ValueError(f"the rules are for {rules[1].n_rows} rows, the step has {self.batch}")
+            rules[0]._args(rules[1], out_logits, out_logits, out_next_tokens)
         mk_decode_step(self.ctx, token_ids, out_logits, out_next_tokens)
         if rules is not None:
             rules[0].run(rules[1], out_logits, out=out_logits, tokens=out_next_tokens)

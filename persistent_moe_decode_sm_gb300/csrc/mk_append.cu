@@ -237,6 +237,10 @@ struct Where {
   int place, position, page;
 };
 
+/* q' and k' = turn(norm(x)), v, each row read and written once.  25400 tokens of 32 + 2 x 4 heads of 128
+ * with norms, 520 MB, take 88 us, 5.9 TB/s, 87 % of a plain copy, with 24 warps an SM (102 with 16, 104
+ * with 32; copies to shared memory several steps ahead instead of loads to registers: 94).  Eight
+ * single tokens take 2.9 us, a chain of loads: offsets and lengths, tables and positions, rows. */
 template <int D, int PAIR, bool NORM>
 __global__ void __launch_bounds__(kThreads, kBlocks) append_tokens(const __grid_constant__ Args a) {
   constexpr int LPH = D / 8, HPW = 32 / LPH; /* lanes of a head, heads of a warp's step */

@@ -673,7 +673,8 @@ struct Loader {
  * the second product of P, tensor cores 76 % active), and small calls by their first
  * instructions: the cut, 2.6 us, the first tile 6 us after the start.
  * TREE: among its sequence's tokens a row sees those that its bits name (one at or before itself);
- * only tiles with such keys look at them, and the words are fetched while S is under way. */
+ * only tiles with such keys look at them, and the words are fetched while S is under way (8 trees of
+ * 33 to 62 tokens over 6700 to 8200 keys: 74.4 us, the same batch without bits 74.5). */
 template <int D, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,

@@ -8,11 +8,12 @@
  * The words of a history are counted once for all rows in a row that share it (the tokens of a
  * drafted tree); a row's path and biases are put in before its logits pass by, and taken out again.
  *
- * What bounds it: 384 bf16 rows of 152064 (350 MB) take 117 us, 3.0 TB/s, of which the copy with
- * masks alone is 74 (about 100 instructions for 128 tokens, half of them a row's beginning and end)
- * and the words and their rules the rest.  Rules in line, where a token's word is met, made most warps
- * run them for one lane: 209 us.  A step of 8 rows, 15 us, and a single row of 32000, 7 us, are a
- * chain of loads, each for the next: arguments, histories, listed tokens, the rows' best.
+ * What bounds it: 384 bf16 rows of 152064 (350 MB) take 118 us, 3.0 TB/s, of which the copy with
+ * masks and the greedy token is 74 (about 100 instructions for 128 tokens, half of them a row's
+ * beginning and end) and the words and their rules the rest.  With rules in line, where a token's word
+ * is met, most warps run them for one lane: 140 us; but a list takes its time to make, so where rows
+ * are few they are in line: 8 rows 14.4 us (15.7), one row of 32000 6.0 (8.0), both a chain of loads,
+ * each for the next: arguments, histories, the rows' best.
  */
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -153,7 +154,8 @@ struct Penalty {
 /* An id's place in a slice that begins at v0; any id, so in unsigned numbers. */
 __device__ __forceinline__ int less(int id, int v0) { return (int)((unsigned)id - (unsigned)v0); }
 
-/* A block's slice: a word for each token, which tokens have one, and those tokens in no order. */
+/* A block's slice: a word for each token, and (LIST) which tokens have one, and those tokens: the
+ * history's in order, then the row's own. */
 struct Words {
   uint32_t *word, *marked; /* [slice], [slice / 32] bits */
   uint16_t *list;          /* [slice] */
@@ -170,7 +172,7 @@ constexpr size_t words_bytes(int slice) { return (size_t)slice * 6 + slice / 8; 
 
 /* A thread's tokens of a slice, four to each chunk of 1024: in a row (VEC), or one of each 256.  They are
  * masked and copied; those with a word, few as a rule, get their rules behind that, densely, from
- * the list.  What a row needs next is loaded while the row before it is under way: its arguments and
+ * the list, or (not LIST) right there.  What a row needs next is loaded while the row before it is under way: its arguments and
  * logits, then its path, biases and mask. */
 template <class T, bool VEC, int AHEAD, bool LIST>
 __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant__ Args a) {
@@ -525,10 +527,19 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
   __syncthreads();
   if (!s_length) return;
   __threadfence();
-  for (int i = tid; i < b.n_rows; i += kThreads) {
-    const unsigned long long key = __ldcg(a.best + i);
-    a.best[i] = 0;
-    if (key != kWrong) a.out_tokens[i] = key ? (int32_t)~(uint32_t)key : -1;
+  for (int i0 = tid; i0 < b.n_rows; i0 += 8 * kThreads) {
+    unsigned long long key[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * kThreads;
+      key[k] = i < b.n_rows ? __ldcg(a.best + i) : kWrong;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = i0 + k * kThreads;
+      if (i < b.n_rows) a.best[i] = 0;
+      if (key[k] != kWrong) a.out_tokens[i] = key[k] ? (int32_t)~(uint32_t)key[k] : -1;
+    }
   }
   if (tid == 0) *a.done = 0;
 }
@@ -645,8 +656,8 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   a.err = m->err;
   a.best = (unsigned long long *)(m->ws + 64);
   a.done = (int32_t *)(m->ws + 32);
-  /* slices: as large as leaves an SM two items (8 rows of 152064: 15.1 us, with one 17.2, with four
-   * 20.5; large slices cost a row less, 384 rows 117 us, with 4096 tokens a slice 158) */
+  /* slices: as large as leaves an SM two items (8 rows of 152064: 14.4 us, with one 18.3, with four
+   * 16.6; large slices cost a row less, 384 rows 118 us, with 4096 tokens a slice 158) */
   a.slice = kSlice;
   while (a.slice > kLeast && (V + a.slice - 1) / a.slice * b->n_rows < 2 * m->n_sm) a.slice /= 2;
   const bool list = a.slice == kSlice;

@@ -95,6 +95,11 @@ class TokenRules:
         """out float32 [n_rows][vocab] (None: not wanted; logits itself: in place) = logits, float32
         or bfloat16 with any row stride, under the batch's rules; tokens int32 [n_rows] (None: not
         wanted) the largest one's id in each row, -1 where none may follow."""
+        _check(self._lib.mk_rules_apply(self.handle, ctypes.byref(batch),
+                                        *self._args(batch, logits, out, tokens)), "mk_rules_apply")
+
+    def _args(self, batch, logits, out, tokens):
+        """What mk_rules_apply takes behind the batch, checked."""
         n = batch.n_rows
         stride, half = logits.stride(), logits.dtype is self._bf16
         if (logits.shape != (n, self.vocab) or not (half or logits.dtype is self._f32)
@@ -105,9 +110,8 @@ class TokenRules:
             if t is not None and (t.dtype is not dtype or t.shape != shape or t.get_device() != self._index
                                   or not t.is_contiguous()):
                 raise ValueError(f"{what} has to be contiguous {dtype} {shape} on {self.device}")
-        _check(self._lib.mk_rules_apply(
-            self.handle, ctypes.byref(batch), logits.data_ptr(), half, stride[0] if n > 1 else self.vocab,
-            None if out is None else out.data_ptr(), None if tokens is None else tokens.data_ptr()), "mk_rules_apply")
+        return (logits.data_ptr(), half, stride[0] if n > 1 else self.vocab,
+                None if out is None else out.data_ptr(), None if tokens is None else tokens.data_ptr())
 
     def sync(self):
         """Waits for the stream; raises the MkError of the first device error."""

@@ -270,6 +270,14 @@ def test_a_step_with_rules_behind_it(batch):
     assert np.array_equal(nxt.cpu().numpy(), want.argmax(1))
     with pytest.raises(ValueError, match="out_logits"):
         dec.decode_step(i32(tokens), None, nxt, rules=(rules, b))
+    for bad in (rules.batch(batch + 1), rules.batch(batch - 1)):
+        with pytest.raises(ValueError, match="rows"):
+            dec.decode_step(i32(tokens), logits, nxt, rules=(rules, bad))
+    for out, to in ((logits.half(), nxt), (logits[:, :-1], nxt), (logits, nxt.long())):
+        with pytest.raises(ValueError):
+            dec.decode_step(i32(tokens), out, to, rules=(rules, b))
+    dec.sync()
+    assert dec.stats().steps == 1                               # refused before the step
     other = mk.TokenRules(V, batch, stream=torch.cuda.Stream())
     with pytest.raises(ValueError, match="stream"):
         dec.decode_step(i32(tokens), logits, nxt, rules=(other, b))
