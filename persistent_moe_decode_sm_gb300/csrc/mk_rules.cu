@@ -12,7 +12,7 @@
  * masks and the greedy token is 74 (about 100 instructions for 128 tokens, half of them a row's
  * beginning and end) and the words and their rules the rest.  With rules in line, where a token's word
  * is met, most warps run them for one lane: 140 us; but a list takes its time to make, so where rows
- * are few they are in line: 8 rows 14.4 us (15.7), one row of 32000 6.0 (8.0), both a chain of loads,
+ * are few they are in line: 8 rows 13.7 us (15.7), one row of 32000 5.6 (8.0), both a chain of loads,
  * each for the next: arguments, histories, the rows' best.
  */
 #include <cuda_bf16.h>
@@ -192,6 +192,12 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
     s_best = 0;
     s_length = 0;
   }
+  auto clear = [&] {
+    for (int i = tid; i < a.slice / 4; i += kThreads) ((uint4 *)ws.word)[i] = make_uint4(0, 0, 0, 0);
+    if (LIST)
+      for (int i = tid; i < a.slice / 32; i += kThreads) ws.marked[i] = 0;
+  };
+  if (counts) clear(); /* the grid before may still be running */
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   /* Two stretches of the items, slice by slice and row by row: text is made of few tokens, and those
@@ -278,10 +284,10 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
       };
       if (counts && is_sound) {
         if (slice != at_slice || r.begin != at_begin || r.end != at_end || r.prompt != at_prompt) {
-          for (int i = tid; i < a.slice / 4; i += kThreads) ((uint4 *)ws.word)[i] = make_uint4(0, 0, 0, 0);
-          if (LIST)
-            for (int i = tid; i < a.slice / 32; i += kThreads) ws.marked[i] = 0;
-          __syncthreads();
+          if (at_slice >= 0) {
+            clear();
+            __syncthreads();
+          }
           for (int i0 = r.begin + tid; i0 < r.end; i0 += 8 * kThreads) {
             int t[8];
 #pragma unroll
@@ -520,13 +526,13 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
     }
   }
   if (!a.out_tokens) return;
-  if (tid == 0) {
-    __threadfence();
-    s_length = atomicAdd(a.done, 1) == (int)gridDim.x - 1;
+  if (tid == 0) { /* behind this thread's best, and before the others' are read */
+    int before;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.done) : "memory");
+    s_length = before == (int)gridDim.x - 1;
   }
   __syncthreads();
   if (!s_length) return;
-  __threadfence();
   for (int i0 = tid; i0 < b.n_rows; i0 += 8 * kThreads) {
     unsigned long long key[8];
 #pragma unroll
@@ -656,7 +662,7 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   a.err = m->err;
   a.best = (unsigned long long *)(m->ws + 64);
   a.done = (int32_t *)(m->ws + 32);
-  /* slices: as large as leaves an SM two items (8 rows of 152064: 14.4 us, with one 18.3, with four
+  /* slices: as large as leaves an SM two items (8 rows of 152064: 13.7 us, with one 18.3, with four
    * 16.6; large slices cost a row less, 384 rows 118 us, with 4096 tokens a slice 158) */
   a.slice = kSlice;
   while (a.slice > kLeast && (V + a.slice - 1) / a.slice * b->n_rows < 2 * m->n_sm) a.slice /= 2;
