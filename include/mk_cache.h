@@ -263,7 +263,7 @@ typedef struct {
  * neither the cache nor q_out is written for them.
  *   norm:  x_i <- gain_i x_i / sqrt(mean(x^2) + norm_eps), over the whole head
  *   turn:  (a, b) <- magnitude (a cos - b sin, b cos + a sin), angle position * frequency
- * in fp32, rounded to bf16 once; the angle is taken in 64-bit fixed point, good to 2^-24
+ * in fp32, rounded to bf16 once; the angle is taken in 64-bit fixed point, good to 2^-22
  * for every position.  v is copied.  Two tokens with the same place race: pages that
  * tokens go to belong to one sequence (mk_kv_resize sees to it).  q_out overlaps nothing
  * else, k and v do not overlap the pools; n_seqs at most 1024.
