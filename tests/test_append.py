@@ -187,6 +187,28 @@ def test_single_tokens(heads):
 
 
 @gpu
+def test_single_tokens_at_other_positions():
+    Case([(40, 1), (0, 1), (8000, 1), (16, 1)], (6, 2, 32), norm="q", single=True, rotary=20,
+         positions=lambda r, n: r.integers(0, 100000, n)).check()
+
+
+@gpu
+def test_batches_of_the_attention_are_taken_with_their_groups():
+    import torch
+
+    c = Case([(40, 3), (33, 1)])
+    d = c.device()
+    attn = mk.PrefixAttention(4, 2, 64, 16, [(d["k"], d["v"])], max_tokens=c.n)
+    t = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    batch = attn.batch(d["tables"], d["lens"], q_offsets=d["off"], group_starts=t(0, 2), prefix_lens=t(32))
+    a = c.handle(d)
+    q, k, v = c.parts(d["qkv"])
+    a.run(0, batch, k, v, q=q, q_out=d["q_out"])
+    a.sync()
+    c.check(d, run=False)
+
+
+@gpu
 def test_tokens_without_a_place_are_left_out():
     Case([(3, 7), (40, 2), (0, 4), (5, 5)], extra=2).check()
 

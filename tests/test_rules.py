@@ -293,6 +293,20 @@ def test_infinite_logits_under_penalties():
 
 
 @gpu
+def test_empty_arrays_and_rows():
+    """No token anywhere, though ranges, paths and biases are given; a bias of -inf forbids."""
+    c = Case(3000, 4, 46, history=0, masks=2)
+    c.tokens = np.zeros(0, np.int32)
+    c.off, c.path = np.zeros(5, np.int32), np.zeros(0, np.int32)
+    c.boff, c.bids, c.bias = np.zeros(5, np.int32), np.zeros(0, np.int32), np.zeros(0, np.float32)
+    c.check()
+    c = Case(3000, 2, 47, history=9, bias=40)
+    c.bias[:] = -np.inf
+    rows, tokens = c.check()
+    assert np.isneginf(rows).sum() >= 1 and (tokens >= 0).all()
+
+
+@gpu
 def test_counts_of_one_token():
     """A history of one token over and over: 30000 atomics on one word."""
     c = Case(2000, 3, 11, history=30000)
