@@ -33,6 +33,8 @@ using namespace mk_dev;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kSlice = 8192, kLeast = 1024; /* tokens of a slice: at most, at least */
 constexpr int kMost = 1 << 24;              /* vocabulary, rows */
+/* Blocks an SM: without vectors the registers of four spill (256 rows of 50257: 47 us, with four 68). */
+constexpr int blocks_of(bool vec) { return vec ? 4 : 3; }
 constexpr unsigned long long kWrong = 1; /* the key of a row that is not written: below that of any value */
 constexpr uint32_t kPrompt = 1u << 31, kBias = 1u << 30, kCount = kBias - 1;
 
@@ -170,13 +172,14 @@ struct Words {
 static_assert(kSlice / 32 <= kThreads, "a thread lists one word of the bits");
 constexpr size_t words_bytes(int slice) { return (size_t)slice * 6 + slice / 8; }
 
-/* A thread's tokens of a slice, four to each chunk of 1024: in a row (VEC), or one of each 256.  They are
+/* A thread's tokens of a slice, four to each chunk of 1024: in a row (VEC), or one of each 32 of its
+ * warp's 128.  They are
  * masked and copied; those with a word, few as a rule, get their rules behind that, densely, from
  * the list, or (not LIST) right there.  What a row needs next is loaded while the row before it is under way: its arguments and
  * logits, then its path, biases and mask. */
 template <class T, bool VEC, int AHEAD, bool LIST>
-__global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant__ Args a) {
-  constexpr int STEP = VEC ? 1 : kThreads, CHUNK = 4 * kThreads; /* AHEAD chunks' logits are under way */
+__global__ void __launch_bounds__(kThreads, blocks_of(VEC)) apply_rules(const __grid_constant__ Args a) {
+  constexpr int STEP = VEC ? 1 : 32, CHUNK = 4 * kThreads; /* AHEAD chunks' logits are under way */
   extern __shared__ uint4 shared[];
   __shared__ unsigned long long s_best;
   __shared__ int s_length, s_history; /* of the list, and of its part that rows share */
@@ -185,7 +188,8 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
   __shared__ float s_bias[kThreads];
   const Words ws(shared, a.slice);
   const mk_rules_batch &b = a.b;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, mine = VEC ? 4 * tid : tid;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, mine = VEC ? 4 * tid : warp * 128 + lane;
+  const int mine_mask = VEC ? mine : warp * 128 + (lane & 3) * 32; /* the first token of this thread's word of a mask */
   const bool counts = b.ranges || b.path_offsets || b.bias_offsets;
   const RowLoader loader(b, warp == kWarps - 1 ? lane : 32);
   if (tid == 0) {
@@ -238,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
     float bias = 0.0f;
     uint32_t may[AHEAD];
     auto fetch_mask = [&](int k, const uint32_t *at, int left) {
-      may[k] = VEC && at && left > k * CHUNK ? __ldcg(at + k * (CHUNK / 32)) : 0xffffffffu;
+      may[k] = at && left > k * CHUNK ? __ldcg(at + k * (CHUNK / 32)) : 0xffffffffu;
     };
     const uint32_t *mask = nullptr; /* this thread's word of the row's next chunk */
     auto fetch_own = [&](const Row &r, bool is_sound, int slice) {
@@ -252,9 +256,9 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
         if (tid) bias_before = __ldcg(b.bias_tokens + r.bias0 + tid - 1);
       }
       const int s0 = slice * a.slice;
-      if (r.mask >= 0) mask = b.allowed + (size_t)r.mask * mask_words + (s0 + mine) / 32;
+      if (r.mask >= 0) mask = b.allowed + (size_t)r.mask * mask_words + (s0 + mine_mask) / 32;
 #pragma unroll
-      for (int k = 0; k < AHEAD; ++k) fetch_mask(k, mask, min(a.slice, a.vocab - s0) - mine);
+      for (int k = 0; k < AHEAD; ++k) fetch_mask(k, mask, min(a.slice, a.vocab - s0) - mine_mask);
     };
     Row r = s_row[0];
     bool is_sound = sound(b, r);
@@ -392,23 +396,22 @@ __global__ void __launch_bounds__(kThreads, 4) apply_rules(const __grid_constant
         for (int k = 0; k < AHEAD; ++k) {
           const float4 x = raw[k].get();
           uint32_t ok = may[k] >> (mine & 31), rest = 15; /* may follow; has no word */
+          if (!VEC) {
+            ok = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ok |= (__shfl_sync(0xffffffffu, may[k], j) >> lane & 1) << j;
+          }
           fetch(k);
-          if (!ends) fetch_mask(k, mask, left - AHEAD * CHUNK);
+          if (!ends) fetch_mask(k, mask, left + mine - mine_mask - AHEAD * CHUNK);
           if (left <= k * CHUNK) continue;
           if (VEC) {
             if (length) rest = ~marked[k * (CHUNK / 32)] >> (mine & 31);
           } else {
-            ok = 15;
+            uint32_t m[4] = {};
+            if (length) *(uint4 *)m = *(const uint4 *)(ws.marked + (c0 + k * CHUNK) / 32 + warp * 4);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int w = (c0 + k * CHUNK + j * STEP + mine) / 32;
-              if (left <= k * CHUNK + j * STEP) {
-                rest &= ~(1u << j);
-              } else {
-                if (masks && !(__ldcg(masks + w) >> (mine & 31) & 1)) ok &= ~(1u << j);
-                if (length && ws.marked[w] >> (mine & 31) & 1) rest &= ~(1u << j);
-              }
-            }
+            for (int j = 0; j < 4; ++j)
+              if (left <= k * CHUNK + j * STEP || (m[j] >> lane & 1)) rest &= ~(1u << j);
           }
           float y[4] = {x.x, x.y, x.z, x.w}, z[4];
           if (!LIST && counts) {
@@ -673,7 +676,7 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)a.slices * b->n_rows, m->n_sm * 4));
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>((int64_t)a.slices * b->n_rows, m->n_sm * blocks_of(vec)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = list ? words_bytes(a.slice) : (size_t)a.slice * 4;
   cfg.stream = m->stream;
