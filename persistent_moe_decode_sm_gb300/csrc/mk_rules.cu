@@ -665,11 +665,15 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   a.err = m->err;
   a.best = (unsigned long long *)(m->ws + 64);
   a.done = (int32_t *)(m->ws + 32);
-  /* slices: as large as leaves an SM two items (8 rows of 152064: 13.7 us, with one 18.3, with four
-   * 16.6; large slices cost a row less, 384 rows 118 us, with 4096 tokens a slice 158) */
+  /* slices: no larger than the vocabulary takes, and as large as leaves an SM two items (8 rows of
+   * 152064: 13.6 us, with one 18.3, with four 16.6; large slices cost a row less, 384 rows 118 us, with
+   * 4096 tokens a slice 158).  Lists where rows are many, but not in the smallest slices, where most
+   * tokens have a word (2048 rows of 1000 47 us, with a list 69). */
   a.slice = kSlice;
-  while (a.slice > kLeast && (V + a.slice - 1) / a.slice * b->n_rows < 2 * m->n_sm) a.slice /= 2;
-  const bool list = a.slice == kSlice;
+  while (a.slice > kLeast && a.slice / 2 >= V) a.slice /= 2;
+  auto items = [&] { return (V + a.slice - 1) / a.slice * b->n_rows; };
+  const bool list = a.slice >= 4 * kLeast && items() >= 2 * m->n_sm;
+  while (a.slice > kLeast && items() < 2 * m->n_sm) a.slice /= 2;
   a.slices = (int32_t)((V + a.slice - 1) / a.slice);
   const bool vec = V % 4 == 0 && row_stride % 4 == 0 && aligned(logits, 4 * (unsigned)size) && aligned(out, 16);
   cudaLaunchAttribute at[1];
