@@ -490,9 +490,10 @@ __global__ void __launch_bounds__(kThreads, blocks_of(VEC)) apply_rules(const __
         }
       }
       if (a.out_tokens) {
-#pragma unroll
-        for (int o = 16; o; o >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, o));
-        if (lane == 0 && key) atomicMax(&s_best, key);
+        /* the largest value, then the lowest id that has it (the complement of a key's second half) */
+        const uint32_t value = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32));
+        const uint32_t id = __reduce_max_sync(0xffffffffu, (uint32_t)(key >> 32) == value ? (uint32_t)key : 0);
+        if (lane == 0 && value) atomicMax(&s_best, (unsigned long long)value << 32 | id);
       }
       __syncthreads();
       if (a.out_tokens && tid == 0) {
