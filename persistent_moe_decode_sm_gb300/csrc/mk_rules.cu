@@ -90,7 +90,7 @@ __device__ __forceinline__ float load1(const __nv_bfloat16 *p) {
 struct Row {
   int begin, end, prompt, path0, path1, bias0, bias1, mask;
   float rep, pres, freq;
-  int pad;
+  int sound; /* whether they can be used */
 };
 constexpr int kRowWords = 11;
 struct RowLoader {
@@ -232,7 +232,12 @@ __global__ void __launch_bounds__(kThreads, blocks_of(VEC)) apply_rules(const __
       ahead += AHEAD * CHUNK;
       ahead_left -= AHEAD * CHUNK;
     };
-    if (warp == kWarps - 1 && lane < kRowWords) ((int *)&s_row[0])[lane] = loader(row);
+    auto put_row = [&](Row &to, int word) { /* by one warp */
+      if (lane < kRowWords) ((int *)&to)[lane] = word;
+      __syncwarp();
+      if (lane == 0) to.sound = sound(b, to);
+    };
+    if (warp == kWarps - 1) put_row(s_row[0], lane < kRowWords ? loader(row) : 0);
     begin(slice, row);
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k) fetch(k);
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(VEC)) apply_rules(const __
       for (int k = 0; k < AHEAD; ++k) fetch_mask(k, mask, min(a.slice, a.vocab - s0) - mine_mask);
     };
     Row r = s_row[0];
-    bool is_sound = sound(b, r);
+    bool is_sound = r.sound;
     fetch_own(r, is_sound, slice);
     int at_slice = -1, at_begin = 0, at_end = 0, at_prompt = 0; /* whose words are there */
 #pragma unroll 1
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(VEC)) apply_rules(const __
         left -= AHEAD * CHUNK;
       }
       unsigned long long key = at >= 0 ? best_key(top, v0 + at) : 0;
-      if (more && warp == kWarps - 1 && lane < kRowWords) ((int *)&s_row[(n + 1) & 1])[lane] = next_word;
+      if (more && warp == kWarps - 1) put_row(s_row[(n + 1) & 1], next_word);
       if (length) {
 #pragma unroll 1
         for (int k0 = 0; k0 < length; k0 += 4 * kThreads) {
@@ -521,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(VEC)) apply_rules(const __
       }
       if (more) {
         r = s_row[(n + 1) & 1];
-        is_sound = sound(b, r);
+        is_sound = r.sound;
         fetch_own(r, is_sound, next_slice);
       }
       __syncthreads();
