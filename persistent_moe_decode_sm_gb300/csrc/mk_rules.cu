@@ -8,9 +8,9 @@
  * The words of a history are counted once for all rows in a row that share it (the tokens of a
  * drafted tree); a row's path and biases are put in before its logits pass by, and taken out again.
  *
- * What bounds it: 384 bf16 rows of 152064 (350 MB) take 118 us, 3.0 TB/s, of which the copy with
- * masks and the greedy token is 74 (about 100 instructions for 128 tokens, half of them a row's
- * beginning and end) and the words and their rules the rest.  With rules in line, where a token's word
+ * What bounds it: 384 bf16 rows of 152064 (350 MB) take 107 us, 3.3 TB/s, of which the copy with
+ * masks and the greedy token is 74 (about 70 instructions for 128 tokens, and a row's beginning and
+ * end) and the words and their rules the rest.  With rules in line, where a token's word
  * is met, most warps run them for one lane: 140 us; but a list takes its time to make, so where rows
  * are few they are in line: 8 rows 13.7 us (15.7), one row of 32000 5.6 (8.0), both a chain of loads,
  * each for the next: arguments, histories, the rows' best.
@@ -455,17 +455,16 @@ __global__ void __launch_bounds__(kThreads, blocks_of(VEC)) apply_rules(const __
             }
           }
           const float m = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])); /* NaN only if all are */
-          if (m > top) {
-            top = m;
-            at = c0 + k * CHUNK + mine + (z[0] == m ? 0 : z[1] == m ? STEP : z[2] == m ? 2 * STEP : 3 * STEP);
-          }
+          const int here = c0 + k * CHUNK + (z[0] == m ? 0 : z[1] == m ? STEP : z[2] == m ? 2 * STEP : 3 * STEP);
+          at = m > top ? here : at;
+          top = fmaxf(top, m);
         }
         go_on();
         marked += AHEAD * (CHUNK / 32);
         to += AHEAD * CHUNK;
         left -= AHEAD * CHUNK;
       }
-      unsigned long long key = at >= 0 ? best_key(top, v0 + at) : 0;
+      unsigned long long key = at >= 0 ? best_key(top, v0 + mine + at) : 0;
       if (more && warp == kWarps - 1) put_row(s_row[(n + 1) & 1], next_word);
       if (length) {
 #pragma unroll 1
@@ -574,8 +573,10 @@ namespace {
 
 typedef void (*Kernel)(Args);
 template <class T, bool VEC>
-Kernel of_slice(int slice, bool list) { /* AHEAD divides a slice's chunks */
-  return list                    ? apply_rules<T, VEC, 4, true>
+Kernel of_slice(int slice, bool list) {
+  /* AHEAD divides a slice's chunks.  With a list, four chunks of fp32 are more registers than there are
+   * (256 rows of 152064: 108 us, so 98); four of bf16 are as many as two of those (384 rows 107, 114). */
+  return list                    ? apply_rules<T, VEC, VEC && sizeof(T) == 4 ? 2 : 4, true>
          : slice >= 4 * kLeast   ? apply_rules<T, VEC, 4, false>
          : slice == 2 * kLeast   ? apply_rules<T, VEC, 2, false>
                                  : apply_rules<T, VEC, 1, false>;
@@ -672,7 +673,7 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   a.best = (unsigned long long *)(m->ws + 64);
   a.done = (int32_t *)(m->ws + 32);
   /* slices: no larger than the vocabulary takes, and as large as leaves an SM two items (8 rows of
-   * 152064: 13.6 us, with one 18.3, with four 16.6; large slices cost a row less, 384 rows 118 us, with
+   * 152064: 13.6 us, with one 18.3, with four 16.6; large slices cost a row less: 384 rows 117 us, with
    * 4096 tokens a slice 158).  Lists where rows are many, but not in the smallest slices, where most
    * tokens have a word (2048 rows of 1000 47 us, with a list 69). */
   a.slice = kSlice;
