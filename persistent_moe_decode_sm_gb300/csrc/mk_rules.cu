@@ -9,10 +9,10 @@
  * drafted tree); a row's path and biases are put in before its logits pass by, and taken out again.
  *
  * What bounds it: 384 bf16 rows of 152064 (350 MB) take 107 us, 3.3 TB/s, of which the copy with
- * masks and the greedy token is 74 (about 70 instructions for 128 tokens, and a row's beginning and
- * end) and the words and their rules the rest.  With rules in line, where a token's word
+ * the greedy token is 69 (writes to DRAM, about 70 instructions for 128 tokens, a row's beginning and
+ * end) and masks, words and their rules the rest.  With rules in line, where a token's word
  * is met, most warps run them for one lane: 140 us; but a list takes its time to make, so where rows
- * are few they are in line: 8 rows 13.7 us (15.7), one row of 32000 5.6 (8.0), both a chain of loads,
+ * are few they are in line: 8 rows 13.4 us (15.7), one row of 32000 5.5 (8.0), both a chain of loads,
  * each for the next: arguments, histories, the rows' best.
  */
 #include <cuda_bf16.h>
