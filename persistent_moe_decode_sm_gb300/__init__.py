@@ -412,6 +412,7 @@ class Decoder:
         self.ctx = None
         self.ctx = mk_create(self.cdims, self.weights, stream)
         self.stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else (stream or 0)
+        self.device = getattr(tensors["embed"], "device", None)
         self.batch = 0
 
     def build_schedule(self, seq_lens, page_tables):
@@ -437,6 +438,11 @@ class Decoder:
             raise ValueError("the rules belong to another stream than the decoder")
         if rules is not None and out_logits is None:
             raise ValueError("rules need out_logits")
+        # the step writes rows of its own vocabulary, whatever the shape of out_logits
+        if rules is not None and rules[0].vocab != self.dims.vocab:
+            raise ValueError(f"the rules have a vocabulary of {rules[0].vocab}, the decoder of {self.dims.vocab}")
+        if rules is not None and rules[0].device != self.device:
+            raise ValueError(f"the rules are on {rules[0].device}, the decoder on {self.device}")
         if rules is not None:  # refused before the step, which cannot be taken back
             if rules[1].n_rows != self.batch:
                 raise ValueError(f"the rules are for {rules[1].n_rows} rows, the step has {self.batch}")

@@ -417,6 +417,47 @@ def test_the_binding_checks_batches():
             r.batch(3, **bad)
 
 
+def decoder(monkeypatch, vocab=100, batch=2):
+    """(a Decoder over host tensors whose step only counts, the counts)."""
+    import types
+
+    import torch
+
+    steps = []
+    d = mk.Decoder.__new__(mk.Decoder)
+    d.ctx, d.dims, d.batch, d.stream = None, types.SimpleNamespace(vocab=vocab), batch, 0
+    d.device = torch.device("cpu")
+    monkeypatch.setattr(mk, "mk_decode_step", lambda *a: steps.append(a))
+    return d, steps
+
+
+@pytest.mark.parametrize("other", [64, 99, 101, 4096])
+def test_a_step_refuses_rules_of_another_vocabulary(monkeypatch, other):
+    """Before the step, which writes rows of its own vocabulary over the tensor that the rules look at."""
+    import torch
+
+    d, steps = decoder(monkeypatch)
+    r = binding(other)
+    r._index, r.max_rows, r.stream = -1, 2, 0
+    with pytest.raises(ValueError, match="vocabulary"):
+        d.decode_step(torch.zeros(2, dtype=torch.int32), torch.zeros(2, other), torch.zeros(2, dtype=torch.int32),
+                      rules=(r, r.batch(2)))
+    assert not steps
+
+
+def test_a_step_refuses_rules_of_another_device(monkeypatch):
+    import torch
+
+    d, steps = decoder(monkeypatch)
+    r = binding()
+    r._index, r.max_rows, r.stream = -1, 2, 0
+    d.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="the decoder on cuda:1"):
+        d.decode_step(torch.zeros(2, dtype=torch.int32), torch.zeros(2, 100), torch.zeros(2, dtype=torch.int32),
+                      rules=(r, r.batch(2)))
+    assert not steps
+
+
 @gpu
 def test_wrong_calls_are_refused():
     c = Case(4096, 4, 15)
