@@ -24,7 +24,7 @@ extern "C" {
  * three of the bias come together). */
 typedef struct {
   int32_t n_rows;
-  int32_t n_tokens, n_path, n_bias, n_masks; /* entries of the arrays below */
+  int32_t n_tokens, n_path, n_bias, n_masks; /* entries of the arrays below; the first two at most 2^29 - 1 */
   const int32_t *tokens;       /* [n_tokens] the sequences' tokens */
   const int32_t *ranges;       /* [n_rows][2]: a row's history is tokens[begin .. end - 1]; the
                                 * rows of a tree share their sequence's */
@@ -64,6 +64,11 @@ void mk_rules_destroy(mk_rules *rules);
  * mk_rules_sync, once. */
 mk_status mk_rules_apply(mk_rules *rules, const mk_rules_batch *batch, const void *logits,
                          int32_t is_bf16, int64_t row_stride, float *out, int32_t *out_tokens);
+
+/* What mk_rules_apply returns for these arguments before it looks at the device; enqueues nothing.
+ * MK_ERR_BATCH for more than max_rows rows, MK_ERR_UNSUPPORTED for more tokens than above. */
+mk_status mk_rules_check(const mk_rules *rules, const mk_rules_batch *batch, const void *logits,
+                         int32_t is_bf16, int64_t row_stride, const float *out, const int32_t *out_tokens);
 
 /* Waits for the stream and returns the first device error since the last mk_rules_sync
  * (MK_OK if none); clears it.  MK_ERR_INVALID_ARG while the stream is being captured. */

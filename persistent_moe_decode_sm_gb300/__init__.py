@@ -163,7 +163,8 @@ EXPORTS = ["mk_create", "mk_build_schedule", "mk_decode_step", "mk_sync", "mk_de
            "mk_attn_sync",
            "mk_attn_set_wait_limit_ns", "mk_attn_debug_poison_wait",
            "mk_append_create", "mk_append_destroy", "mk_append_tokens", "mk_append_sync",
-           "mk_rules_create", "mk_rules_destroy", "mk_rules_apply", "mk_rules_sync"]
+           "mk_rules_create", "mk_rules_destroy", "mk_rules_check", "mk_rules_apply",
+           "mk_rules_sync"]
 _NO_STATUS = ("mk_destroy", "mk_status_string", "mk_kv_destroy", "mk_attn_destroy",
               "mk_append_destroy", "mk_rules_destroy")
 
@@ -227,6 +228,7 @@ def lib():
         L.mk_rules_destroy.argtypes = [vp]
         L.mk_rules_destroy.restype = None
         L.mk_rules_apply.argtypes = [vp, ctypes.POINTER(mk_rules_batch), vp, i32, i64, vp, vp]
+        L.mk_rules_check.argtypes = L.mk_rules_apply.argtypes
         L.mk_rules_sync.argtypes = [vp]
         for n in EXPORTS:
             if n not in _NO_STATUS:
@@ -446,7 +448,7 @@ class Decoder:
         if rules is not None:  # refused before the step, which cannot be taken back
             if rules[1].n_rows != self.batch:
                 raise ValueError(f"the rules are for {rules[1].n_rows} rows, the step has {self.batch}")
-            rules[0]._args(rules[1], out_logits, out_logits, out_next_tokens)
+            rules[0].check(rules[1], out_logits, out_logits, out_next_tokens)
         mk_decode_step(self.ctx, token_ids, out_logits, out_next_tokens)
         if rules is not None:
             rules[0].run(rules[1], out_logits, out=out_logits, tokens=out_next_tokens)

@@ -636,8 +636,8 @@ void mk_rules_destroy(mk_rules *m) {
   delete m;
 }
 
-mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logits, int32_t is_bf16,
-                         int64_t row_stride, float *out, int32_t *out_tokens) {
+mk_status mk_rules_check(const mk_rules *m, const mk_rules_batch *b, const void *logits, int32_t is_bf16,
+                         int64_t row_stride, const float *out, const int32_t *out_tokens) {
   if (!m || !b || b->n_rows < 0 || b->n_tokens < 0 || b->n_path < 0 || b->n_bias < 0 || b->n_masks < 0)
     return MK_ERR_INVALID_ARG;
   if (b->n_rows > m->max_rows) return MK_ERR_BATCH;
@@ -659,6 +659,15 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   const bool in_place = out == logits && !is_bf16 && row_stride == V;
   if (out && !in_place && rows_meet(logits, row_stride * size, V * size, out, V * 4, V * 4, b->n_rows))
     return MK_ERR_INVALID_ARG;
+  return MK_OK;
+}
+
+mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logits, int32_t is_bf16,
+                         int64_t row_stride, float *out, int32_t *out_tokens) {
+  const mk_status refused = mk_rules_check(m, b, logits, is_bf16, row_stride, out, out_tokens);
+  if (refused != MK_OK) return refused;
+  if (b->n_rows == 0) return MK_OK;
+  const int64_t size = is_bf16 ? 2 : 4, V = m->vocab;
   OnDevice on(m->dev);
   if (!on.ok) return MK_ERR_CUDA;
   Args a{};

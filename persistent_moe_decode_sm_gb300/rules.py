@@ -98,6 +98,11 @@ class TokenRules:
         _check(self._lib.mk_rules_apply(self.handle, ctypes.byref(batch),
                                         *self._args(batch, logits, out, tokens)), "mk_rules_apply")
 
+    def check(self, batch, logits, out=None, tokens=None):
+        """Raises what run() raises for these arguments; nothing is enqueued."""
+        _check(self._lib.mk_rules_check(self.handle, ctypes.byref(batch),
+                                        *self._args(batch, logits, out, tokens)), "mk_rules_check")
+
     def _args(self, batch, logits, out, tokens):
         """What mk_rules_apply takes behind the batch, checked."""
         n = batch.n_rows

@@ -281,3 +281,33 @@ def test_a_step_with_rules_behind_it(batch):
     other = mk.TokenRules(V, batch, stream=torch.cuda.Stream())
     with pytest.raises(ValueError, match="stream"):
         dec.decode_step(i32(tokens), logits, nxt, rules=(other, b))
+
+
+def test_a_step_is_refused_with_its_rules():
+    """What the library refuses on the host is refused before the step, which cannot be taken back."""
+    import torch
+
+    s = Shared(20)
+    s.cache.fork(i32([0, 0]), i32([1, 2]))
+    p = s.private([0, 1, 2])
+    dec = p.make()
+    dec.build_schedule(p.lens, p.tables)
+    V = DIMS.vocab
+    logits, nxt = torch.full((3, V), 5.0, device="cuda"), torch.full((3,), -9, dtype=torch.int32, device="cuda")
+    small, rules, closed = mk.TokenRules(V, 2), mk.TokenRules(V, 3), mk.TokenRules(V, 3)
+    closed.close()
+    long = rules.batch(3, tokens=i32([1, 2]), ranges=i32([[0, 2]] * 3))
+    long.n_tokens = 2 ** 29
+    drafted = rules.batch(3, path_offsets=i32([0] * 4), path_tokens=i32([1]))
+    drafted.n_path = 2 ** 31 - 1
+    lost = rules.batch(3, prompt_lens=i32([0] * 3), tokens=i32([1, 2]), ranges=i32([[0, 2]] * 3))
+    lost.ranges = None
+    for r, b, code in ((small, small.batch(3), mk.MK_ERR_BATCH), (rules, long, mk.MK_ERR_UNSUPPORTED),
+                       (rules, drafted, mk.MK_ERR_UNSUPPORTED), (rules, lost, mk.MK_ERR_INVALID_ARG),
+                       (closed, rules.batch(3), mk.MK_ERR_INVALID_ARG)):
+        with pytest.raises(mk.MkError) as e:
+            dec.decode_step(i32([3, 4, 5]), logits, nxt, rules=(r, b))
+        assert e.value.code == code
+    dec.sync()
+    assert dec.stats().steps == 0
+    assert (logits == 5.0).all() and (nxt == -9).all()

@@ -387,6 +387,10 @@ def test_create_and_null_handles():
     L.mk_rules_destroy(None)
 
 
+def test_check_of_null_handles():
+    assert mk.lib().mk_rules_check(None, None, None, 0, 0, None, None) == mk.MK_ERR_INVALID_ARG
+
+
 def binding(vocab=100):
     """A TokenRules over host tensors that makes no call into the library."""
     import torch
