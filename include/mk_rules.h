@@ -36,7 +36,8 @@ typedef struct {
   const int32_t *bias_tokens;  /* [n_bias], rising within a row */
   const float *bias;           /* [n_bias] */
   const uint32_t *allowed;     /* [n_masks][(vocab + 31) / 32]: bit t % 32 of word t / 32: token t may follow */
-  const int32_t *allowed_rows; /* [n_rows]: a row's mask, negative: all may follow; NULL: mask i of row i */
+  const int32_t *allowed_rows; /* [n_rows]: a row's mask, negative: all may follow (those of all rows where
+                                * n_masks is 0, allowed NULL or not); NULL: mask i of row i */
 } mk_rules_batch;
 
 typedef struct mk_rules mk_rules;

@@ -105,7 +105,7 @@ struct RowLoader {
       case 4: at = b.path_offsets ? b.path_offsets + 1 : nullptr; break;
       case 5: at = b.bias_offsets; break;
       case 6: at = b.bias_offsets ? b.bias_offsets + 1 : nullptr; break;
-      case 7: at = b.allowed ? b.allowed_rows : nullptr, otherwise = -1; break;
+      case 7: at = b.allowed_rows, otherwise = -1; break;
       case 8: at = (const int32_t *)b.repetition, otherwise = 0x3f800000; break;
       case 9: at = (const int32_t *)b.presence; break;
       case 10: at = (const int32_t *)b.frequency; break;
@@ -650,7 +650,7 @@ mk_status mk_rules_check(const mk_rules *m, const mk_rules_batch *b, const void 
     if (!aligned(p, 4)) return MK_ERR_INVALID_ARG;
   if ((b->ranges && b->n_tokens && !b->tokens) || (b->path_offsets && b->n_path && !b->path_tokens) ||
       (b->bias_offsets && b->n_bias && (!b->bias_tokens || !b->bias)) || (b->prompt_lens && !b->ranges) ||
-      (b->allowed_rows && !b->allowed) || (b->allowed && !b->allowed_rows && b->n_masks < b->n_rows))
+      (b->allowed_rows && b->n_masks && !b->allowed) || (b->allowed && !b->allowed_rows && b->n_masks < b->n_rows))
     return MK_ERR_INVALID_ARG;
   const int64_t size = is_bf16 ? 2 : 4, V = m->vocab;
   if (!logits || (!out && !out_tokens) || !aligned(logits, (unsigned)size) || row_stride < V ||
@@ -672,7 +672,7 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   if (!on.ok) return MK_ERR_CUDA;
   Args a{};
   a.b = *b;
-  if (!b->allowed) a.b.n_masks = 1; /* row masks are not looked at */
+  if (!b->allowed && !b->allowed_rows) a.b.n_masks = 1; /* row masks are not looked at */
   a.vocab = m->vocab;
   a.logits = logits;
   a.row_stride = row_stride;

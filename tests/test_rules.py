@@ -307,6 +307,18 @@ def test_empty_arrays_and_rows():
 
 
 @gpu
+@pytest.mark.parametrize("rows", [3, 340])
+def test_no_masks_and_rows_that_take_none(rows):
+    """No grammar is active: allowed has no rows, and none is asked for; one that is asked for is reported."""
+    c = Case(9000, rows, 48, bias=5)
+    c.which = np.full(rows, -1, np.int32)
+    none = np.zeros((0, (9000 + 31) // 32), np.int32)
+    c.check(allowed=none)
+    c.which[1] = 0
+    c.check(allowed=none, skip={1}, code=mk.MK_ERR_INVALID_ARG)
+
+
+@gpu
 def test_counts_of_one_token():
     """A history of one token over and over: 30000 atomics on one word."""
     c = Case(2000, 3, 11, history=30000)
