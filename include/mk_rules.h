@@ -66,6 +66,11 @@ void mk_rules_destroy(mk_rules *rules);
 mk_status mk_rules_apply(mk_rules *rules, const mk_rules_batch *batch, const void *logits,
                          int32_t is_bf16, int64_t row_stride, float *out, int32_t *out_tokens);
 
+/* mk_rules_apply behind mk_decode_step on the same stream, in place on its logits; out_tokens is the
+ * step's out_next_tokens, in which a row that is refused gets -1 instead of keeping the step's token
+ * (its logits stay the step's). */
+mk_status mk_rules_follow(mk_rules *rules, const mk_rules_batch *batch, float *logits, int32_t *out_tokens);
+
 /* What mk_rules_apply returns for these arguments before it looks at the device; enqueues nothing.
  * MK_ERR_BATCH for more than max_rows rows, MK_ERR_UNSUPPORTED for more tokens than above. */
 mk_status mk_rules_check(const mk_rules *rules, const mk_rules_batch *batch, const void *logits,

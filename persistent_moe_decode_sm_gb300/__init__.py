@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import subprocess
+import weakref
 from typing import List, Optional, Sequence
 
 import numpy as np
@@ -164,7 +165,7 @@ EXPORTS = ["mk_create", "mk_build_schedule", "mk_decode_step", "mk_sync", "mk_de
            "mk_attn_set_wait_limit_ns", "mk_attn_debug_poison_wait",
            "mk_append_create", "mk_append_destroy", "mk_append_tokens", "mk_append_sync",
            "mk_rules_create", "mk_rules_destroy", "mk_rules_check", "mk_rules_apply",
-           "mk_rules_sync"]
+           "mk_rules_follow", "mk_rules_sync"]
 _NO_STATUS = ("mk_destroy", "mk_status_string", "mk_kv_destroy", "mk_attn_destroy",
               "mk_append_destroy", "mk_rules_destroy")
 
@@ -229,6 +230,7 @@ def lib():
         L.mk_rules_destroy.restype = None
         L.mk_rules_apply.argtypes = [vp, ctypes.POINTER(mk_rules_batch), vp, i32, i64, vp, vp]
         L.mk_rules_check.argtypes = L.mk_rules_apply.argtypes
+        L.mk_rules_follow.argtypes = [vp, ctypes.POINTER(mk_rules_batch), vp, vp]
         L.mk_rules_sync.argtypes = [vp]
         for n in EXPORTS:
             if n not in _NO_STATUS:
@@ -416,6 +418,7 @@ class Decoder:
         self.stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else (stream or 0)
         self.device = getattr(tensors["embed"], "device", None)
         self.batch = 0
+        self._rules = weakref.WeakSet()  # those that stood behind a step
 
     def build_schedule(self, seq_lens, page_tables):
         self.batch = len(seq_lens)
@@ -435,7 +438,8 @@ class Decoder:
 
     def decode_step(self, token_ids, out_logits, out_next_tokens, rules=None):
         """rules: (TokenRules, its batch) that are put on out_logits (a torch tensor) behind the
-        step, on the same stream; out_next_tokens are then the greedy tokens under them."""
+        step, on the same stream; out_next_tokens are then the greedy tokens under them.  A row whose
+        rules are wrong on the device keeps the step's logits and gets the token -1, and sync() raises."""
         if rules is not None and rules[0].stream != self.stream:
             raise ValueError("the rules belong to another stream than the decoder")
         if rules is not None and out_logits is None:
@@ -451,10 +455,16 @@ class Decoder:
             rules[0].check(rules[1], out_logits, out_logits, out_next_tokens)
         mk_decode_step(self.ctx, token_ids, out_logits, out_next_tokens)
         if rules is not None:
-            rules[0].run(rules[1], out_logits, out=out_logits, tokens=out_next_tokens)
+            self._rules.add(rules[0])
+            rules[0].follow(rules[1], out_logits, out_next_tokens)
 
     def sync(self):
+        """Waits for the stream; raises the MkError of the first device error, of the steps and then of
+        the rules behind them."""
         mk_sync(self.ctx)
+        for rules in list(self._rules):
+            if rules.handle:
+                rules.sync()
 
     def routing(self):
         return mk_debug_routing(self.ctx, self.dims.n_layers, self.batch, self.dims.top_k)

@@ -41,6 +41,7 @@ constexpr uint32_t kPrompt = 1u << 31, kBias = 1u << 30, kCount = kBias - 1;
 struct Args {
   mk_rules_batch b;
   int32_t vocab, slice, slices;
+  int32_t behind_step; /* out_tokens holds the step's own tokens, which a wrong row must not keep */
   const void *logits;
   int64_t row_stride;
   float *out;
@@ -552,7 +553,10 @@ __global__ void __launch_bounds__(kThreads, blocks_of(VEC)) apply_rules(const __
     for (int k = 0; k < 8; ++k) {
       const int i = i0 + k * kThreads;
       if (i < b.n_rows) a.best[i] = 0;
-      if (key[k] != kWrong) a.out_tokens[i] = key[k] ? (int32_t)~(uint32_t)key[k] : -1;
+      if (key[k] != kWrong)
+        a.out_tokens[i] = key[k] ? (int32_t)~(uint32_t)key[k] : -1;
+      else if (a.behind_step && i < b.n_rows)
+        a.out_tokens[i] = -1;
     }
   }
   if (tid == 0) *a.done = 0;
@@ -662,8 +666,8 @@ mk_status mk_rules_check(const mk_rules *m, const mk_rules_batch *b, const void 
   return MK_OK;
 }
 
-mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logits, int32_t is_bf16,
-                         int64_t row_stride, float *out, int32_t *out_tokens) {
+static mk_status apply(mk_rules *m, const mk_rules_batch *b, const void *logits, int32_t is_bf16,
+                       int64_t row_stride, float *out, int32_t *out_tokens, bool behind_step) {
   const mk_status refused = mk_rules_check(m, b, logits, is_bf16, row_stride, out, out_tokens);
   if (refused != MK_OK) return refused;
   if (b->n_rows == 0) return MK_OK;
@@ -678,6 +682,7 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   a.row_stride = row_stride;
   a.out = out;
   a.out_tokens = out_tokens;
+  a.behind_step = behind_step;
   a.err = m->err;
   a.best = (unsigned long long *)(m->ws + 64);
   a.done = (int32_t *)(m->ws + 32);
@@ -703,6 +708,16 @@ mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logit
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel_of(is_bf16 != 0, vec, a.slice, list), a) == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}
+
+mk_status mk_rules_apply(mk_rules *m, const mk_rules_batch *b, const void *logits, int32_t is_bf16,
+                         int64_t row_stride, float *out, int32_t *out_tokens) {
+  return apply(m, b, logits, is_bf16, row_stride, out, out_tokens, false);
+}
+
+mk_status mk_rules_follow(mk_rules *m, const mk_rules_batch *b, float *logits, int32_t *out_tokens) {
+  if (!m || (b && b->n_rows > 0 && !out_tokens)) return MK_ERR_INVALID_ARG;
+  return apply(m, b, logits, 0, m->vocab, logits, out_tokens, true);
 }
 
 mk_status mk_rules_sync(mk_rules *m) {

@@ -98,6 +98,12 @@ class TokenRules:
         _check(self._lib.mk_rules_apply(self.handle, ctypes.byref(batch),
                                         *self._args(batch, logits, out, tokens)), "mk_rules_apply")
 
+    def follow(self, batch, logits, tokens):
+        """run() in place behind a decode step, whose own greedy tokens `tokens` holds: a row that is
+        refused on the device gets -1 there and does not keep the step's."""
+        at, _, _, _, to = self._args(batch, logits, logits, tokens)
+        _check(self._lib.mk_rules_follow(self.handle, ctypes.byref(batch), at, to), "mk_rules_follow")
+
     def check(self, batch, logits, out=None, tokens=None):
         """Raises what run() raises for these arguments; nothing is enqueued."""
         _check(self._lib.mk_rules_check(self.handle, ctypes.byref(batch),

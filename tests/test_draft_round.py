@@ -311,3 +311,68 @@ def test_a_step_is_refused_with_its_rules():
     dec.sync()
     assert dec.stats().steps == 0
     assert (logits == 5.0).all() and (nxt == -9).all()
+
+
+@pytest.mark.parametrize("wrong", ["repetition", "mask", "bias"])
+def test_a_row_whose_rules_are_wrong_has_no_token(wrong):
+    """Not the step's own, which the rules never saw; the decoder's sync() raises, once; the step behind it is
+    right again."""
+    import torch
+
+    s = Shared(20)
+    s.cache.fork(i32([0, 0]), i32([1, 2]))
+    seqs, tokens = [0, 1, 2], np.array([3, 4, 5], np.int32)
+    p = s.private(seqs)
+    plain, first = s.step(seqs, tokens)
+    V = DIMS.vocab
+    rules = mk.TokenRules(V, 5)
+    repetition = torch.full((3,), 2.0, device="cuda")
+    allowed = torch.zeros(1, (V + 31) // 32, dtype=torch.int32, device="cuda")
+    allowed[0, 3] = -1                                           # 96 to 127
+    which, ids = i32([-1, 0, 0]), i32([7, 9, 11, 100, 101, 102])
+    b = rules.batch(3, repetition=repetition, allowed=allowed, allowed_rows=which, bias_offsets=i32([0, 2, 4, 6]),
+                    bias_tokens=ids, bias=torch.zeros(6, device="cuda"))
+    logits, nxt = torch.zeros(3, V, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    dec = p.make()
+    dec.build_schedule(p.lens, p.tables)
+    if wrong == "repetition":
+        repetition[1] = 0.0
+    elif wrong == "mask":
+        which[1] = 1
+    else:
+        ids[2] = 100
+    dec.decode_step(i32(tokens), logits, nxt, rules=(rules, b))
+    with pytest.raises(mk.MkError) as e:
+        dec.sync()
+    assert e.value.code == mk.MK_ERR_INVALID_ARG
+    dec.sync()
+    rules.sync()
+    masked = plain.copy()
+    masked[:, :96], masked[:, 128:] = -np.inf, -np.inf
+    got = logits.cpu().numpy()
+    assert nxt.tolist() == [int(first[0]), -1, int(masked[2].argmax())]
+    assert np.array_equal(got[:2], plain[:2]) and np.array_equal(got[2], masked[2])
+    repetition[1], which[1], ids[2] = 2.0, 0, 11
+    dec.build_schedule(p.lens, p.tables)
+    dec.decode_step(i32(tokens), logits, nxt, rules=(rules, b))
+    dec.sync()
+    assert nxt.tolist() == [int(first[0])] + [int(x) for x in masked[1:].argmax(1)]
+
+
+def test_rules_that_are_gone_do_not_matter_to_sync():
+    import torch
+
+    s = Shared(20)
+    p = s.private([0])
+    dec = p.make()
+    dec.build_schedule(p.lens, p.tables)
+    logits, nxt = torch.zeros(1, DIMS.vocab, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for close in (True, False):
+        rules = mk.TokenRules(DIMS.vocab, 1)
+        dec.decode_step(i32([3]), logits, nxt, rules=(rules, rules.batch(1)))
+        if close:
+            rules.close()
+        else:
+            del rules
+        dec.sync()
+    assert int(nxt) == int(logits.argmax())

@@ -399,8 +399,9 @@ def test_create_and_null_handles():
     L.mk_rules_destroy(None)
 
 
-def test_check_of_null_handles():
+def test_check_and_follow_of_null_handles():
     assert mk.lib().mk_rules_check(None, None, None, 0, 0, None, None) == mk.MK_ERR_INVALID_ARG
+    assert mk.lib().mk_rules_follow(None, None, None, None) == mk.MK_ERR_INVALID_ARG
 
 
 def binding(vocab=100):
