@@ -61,7 +61,7 @@ def _batch(device, page_tables, seq_lens, q_offsets, group_starts, prefix_lens, 
         n_tokens = n
     b = mk_attn_batch(n, n_tokens, groups, page_tables.shape[1], page_tables.data_ptr(), seq_lens.data_ptr(),
                       _addr(q_offsets), _addr(group_starts), _addr(prefix_lens))
-    b.keep = (page_tables, seq_lens, q_offsets, group_starts, prefix_lens)
+    b.keep, b.device = (page_tables, seq_lens, q_offsets, group_starts, prefix_lens), device
     return b
 
 
@@ -259,6 +259,8 @@ class PrefixAttention:
         [words], see tree_rows): which of its sequence's query tokens each one sees, a bit for
         each; None: those before it and itself."""
         rows = (batch.n_tokens, self.heads, self.head_dim)
+        if batch.device != self.device:
+            raise ValueError(f"the batch is on {batch.device}, not on {self.device}")
         if (q.shape != rows or q.dtype is not self._bf16 or q.get_device() != self._index
                 or q.stride(2) != 1 or (self.heads > 1 and q.stride(1) != self.head_dim)):
             raise ValueError(f"q has to be bfloat16 {rows} with contiguous heads on {self.device}")
@@ -440,6 +442,8 @@ class KvAppend:
         as parts of a fused projection.  positions (int32 [n_tokens]): what the heads turn to,
         None: the tokens' places.  q_norm, k_norm: gains of the norm, None: no norm."""
         n = batch.n_tokens
+        if batch.device != self.device:
+            raise ValueError(f"the batch is on {batch.device}, not on {self.device}")
         if (q is None) != (q_out is None):
             raise ValueError("q and q_out come together")
         kv = (n, self.kv_heads, self.head_dim)

@@ -39,7 +39,8 @@ class TokenRules:
               path_tokens=None, repetition=None, presence=None, frequency=None, bias_offsets=None,
               bias_tokens=None, bias=None, allowed=None, allowed_rows=None):
         """What holds for the rows of a call, to be kept as long as its tensors stay in place
-        (their contents may change between calls).
+        (their contents may change between calls), by these rules or others with the same
+        vocabulary and device.
 
         tokens int32, ranges int32 [n_rows][2] (begin and end of a row's history in tokens; rows
         may share one), prompt_lens int32 [n_rows] (of it, not generated); path_offsets int32
@@ -88,7 +89,7 @@ class TokenRules:
                   frequency, bias_offsets, bias_tokens, bias, allowed, allowed_rows)
         b = mk_rules_batch(n_rows, count(tokens), count(path_tokens), count(bias_tokens),
                            count(allowed), *[_addr(t) for t in arrays])
-        b.keep = arrays
+        b.keep, b.vocab, b.device = arrays, self.vocab, self.device
         return b
 
     def run(self, batch, logits, out=None, tokens=None):
@@ -112,6 +113,9 @@ class TokenRules:
     def _args(self, batch, logits, out, tokens):
         """What mk_rules_apply takes behind the batch, checked."""
         n = batch.n_rows
+        # the library knows a mask's length by the vocabulary alone
+        if batch.vocab != self.vocab or batch.device != self.device:
+            raise ValueError("the batch was made by rules with another vocabulary or on another device")
         stride, half = logits.stride(), logits.dtype is self._bf16
         if (logits.shape != (n, self.vocab) or not (half or logits.dtype is self._f32)
                 or logits.get_device() != self._index or (self.vocab > 1 and stride[1] != 1)):

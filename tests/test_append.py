@@ -407,6 +407,20 @@ def test_binding_checks_without_a_gpu():
         mk.KvAppend(4, 2, 64, 16, [])
 
 
+@pytest.mark.parametrize("kind", ["KvAppend", "PrefixAttention"])
+def test_batches_of_another_device_are_refused(kind):
+    import torch
+
+    a = getattr(mk, kind).__new__(getattr(mk, kind))
+    a.handle, a.device, a.heads, a.kv_heads, a.head_dim, a._index = None, torch.device("cpu"), 1, 1, 32, -1
+    a._bf16, a._int32, a.max_tokens = torch.bfloat16, torch.int32, 2
+    b = a.batch(torch.zeros(2, 3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32))
+    a.device = torch.device("cuda", 1)
+    x = torch.zeros(2, 1, 32, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="the batch is on cpu, not on cuda:1"):
+        a.run(0, b, x, x)
+
+
 @gpu
 def test_the_binding_refuses_wrong_tensors():
     c = Case([(40, 9), (21, 21)])

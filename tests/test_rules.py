@@ -434,6 +434,23 @@ def test_the_binding_checks_batches():
             r.batch(3, **bad)
 
 
+@pytest.mark.parametrize("vocab, device", [(64, "cpu"), (4096, "cpu"), (100, "cuda:1")])
+def test_batches_of_other_rules_are_refused(vocab, device):
+    """A mask of 100 tokens has 4 words; under 4096 tokens 128 would be read."""
+    import torch
+
+    a, b = binding(), binding(vocab)
+    for r in (a, b):
+        r._index, r.max_rows, r._lib = -1, 2, mk.lib()
+    b.device = torch.device(device)
+    batch = a.batch(2, allowed=torch.zeros(2, 4, dtype=torch.int32))
+    logits, tokens = torch.zeros(2, vocab), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: b.run(batch, logits, tokens=tokens), lambda: b.check(batch, logits, tokens=tokens),
+                 lambda: b.follow(batch, logits, tokens)):
+        with pytest.raises(ValueError, match="made by rules"):
+            call()
+
+
 def decoder(monkeypatch, vocab=100, batch=2):
     """(a Decoder over host tensors whose step only counts, the counts)."""
     import types
