@@ -233,7 +233,9 @@ typedef struct {
                                               * NULL: rope_base^(-2i / rotary_dim) */
   float rope_base;                           /* above 0 where it is used */
   float magnitude;                           /* of cos and sin, above 0; 0: 1 */
-  float norm_eps;                            /* 0 or above */
+  float norm_eps;                            /* 0 or above; where it is 2^-100 or more, heads that are
+                                              * normed have a mean square below 2^121 (elements below
+                                              * 2^60 do) */
 } mk_append_desc;
 
 typedef struct mk_append mk_append;

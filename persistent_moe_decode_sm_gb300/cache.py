@@ -380,7 +380,8 @@ class KvAppend:
     layers: (k_cache, v_cache) of each layer as for PrefixAttention.  rotary_dim: the head's first
     dims that turn (None: all).  interleaved: pairs are neighbours, else halves.  frequencies:
     radians a position of each pair (see rope_frequencies), None: of rope_base.  magnitude: of
-    the cosines and sines."""
+    the cosines and sines.  norm_eps: 0 or above; under 2^-100 heads of any size are normed, else
+    those whose elements are below 2^60."""
 
     def __init__(self, n_q_heads: int, n_kv_heads: int, head_dim: int, page_size: int, layers,
                  rotary_dim: int = None, interleaved: bool = False, rope_base: float = 10000.0,

@@ -249,6 +249,38 @@ def test_norm_of_small_and_large_heads(scale, eps):
 
 
 @gpu
+@pytest.mark.parametrize("eps", [0.0, 1e-44, 1e-35, 1e-6, 1e20])
+@pytest.mark.parametrize("heads", [(4, 2, 64), (5, 3, 32), (2, 1, 128)])
+def test_norm_over_the_whole_range(heads, eps):
+    """Heads whose squares leave 32 bits at either end, each beside others that do not, and heads with both
+    large and small values.  The scales by powers of two are exact, so the tolerance is the same; results
+    below 2^-126 are rounded to steps of 2^-133."""
+    c = Case([(40, 30)], heads, norm="qk", eps=eps, seed=8)
+    t, rng = c.t, np.random.default_rng(8)
+    sizes = [-132, -125, -100, -67, -60, -51, -49, 0, 49, 51, 57]
+    if eps < 2.0 ** -100:
+        sizes += [63, 64, 100, 124]
+    size = 2.0 ** rng.choice(sizes, c.qkv.shape[:2])
+    spread = 2.0 ** rng.choice([0, 0, -20, -45], c.qkv.shape)
+    x = c.qkv.double() * t.from_numpy(size)[:, :, None] * t.from_numpy(np.where(rng.random(c.qkv.shape[:2] + (1,)) < 0.5, 1, spread))
+    c.qkv = x.clamp(-3e38, 3e38).to(t.bfloat16)
+    if eps == 0.0:  # no head of zeros: its norm is 0 / 0
+        c.qkv[..., 0] = t.where((c.qkv == 0).all(-1), t.full((), 2.0 ** -133, dtype=t.bfloat16), c.qkv[..., 0])
+    close = c.close
+    c.close = lambda got, want, size: close(got, want, size + 2.0 ** -134 * 2.0 ** 19)
+    c.check()
+
+
+@gpu
+@pytest.mark.parametrize("scale", [1e-20, 1e-30, 1e-38, 1e30])
+def test_norm_without_eps_of_equal_sizes(scale):
+    """A head of one size is its signs times the gain, at any size: of tiny heads K too."""
+    c = Case([(40, 6)], norm="qk", eps=0.0)
+    c.qkv = c.qkv.float().sign().mul(scale).to(c.t.bfloat16)
+    c.check()
+
+
+@gpu
 def test_infinities_and_nan_stay_in_their_head():
     c = Case([(40, 4)], (4, 2, 64), rotary=32)
     c.qkv[0, 1, 3], c.qkv[2, 0, 50], c.qkv[3, 7, 5] = float("nan"), float("inf"), float("nan")
