@@ -56,6 +56,8 @@ struct Args {
   float scale_log2; /* scale * log2(e) */
   const uint32_t *tree; /* [n_tokens][tree_words] bits of the sequence's tokens that a token sees, or NULL */
   int32_t tree_words, max_query; /* max_query: tokens of a sequence */
+  const __nv_bfloat16 *q, *k_pool, *v_pool; /* for redo_rows: the tiles have tensor maps */
+  int64_t q_stride;
   int32_t TB;       /* query tokens of a row tile: 128 / G */
   uint32_t inv_g;   /* ceil(2^16 / G): r * inv_g >> 16 is r / G for r < 128 */
   unsigned long long inv_p; /* ceil(2^38 / P): k * inv_p >> 38 is k / P for k < 2^30 */
@@ -70,7 +72,8 @@ struct Args {
                       * none; y: the first piece's worker; z: the token's first row in worker 0's
                       * place; w: rows from a worker's place to the next */
   float *part;       /* [2 * n_tokens * Hq + 4 * SMs * 128][D] weighted sums */
-  float2 *part_ml;   /* the same rows: maximum (in powers of two), sum */
+  float2 *part_ml;   /* the same rows: maximum (in powers of two), sum; of a tree's rows that need
+                      * no join too, there with the sum only where the result is not finite, else -1 */
 };
 
 __device__ __forceinline__ void report(const Args &a, int code) {
@@ -1079,6 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ch = ln % RL, mine = min(32, crows - w0); /* rows of this warp */
         float *to = a.part + (c.t0 ? extra : c.own * dense + row0) * D + ch * 4;
         const float f = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l; /* NaN stays NaN */
+        float odd = 0.0f; /* NaN if a column is not finite */
 #pragma unroll 1
         for (int i0 = 0; i0 < D; i0 += W) {
           float o[W];
@@ -1088,6 +1092,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_ld32(at_o + i0, o);
           else
             tmem_ld16(at_o + i0, o);
+          if (TREE && whole) {
+#pragma unroll
+            for (int k = 0; k < W; ++k) odd = fmaf(o[k], 0.0f, odd);
+          }
 #pragma unroll
           for (int k = 0; k < W / 4; ++k)
             *(float4 *)(qd + k / CR * C::BLOCK + ln * C::ROWB + ((k % CR) ^ (ln & (CR - 1))) * 16) =
@@ -1111,6 +1119,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (valid && whole) {
           if (a.lse)
             a.lse[orow] = l == 0.0f ? -INFINITY : (m * c2 + log2f(l)) * 0.69314718055994531f;
+          if (TREE)
+            a.part_ml[dense + orow] = make_float2(m == -INFINITY ? m : m * c2, odd == odd || l != l ? -1.0f : l);
         } else if (valid) {
           a.part_ml[c.t0 ? extra + r : c.own * dense + orow] =
               make_float2(l != l ? 0.0f : m == -INFINITY ? m : m * c2, l); /* NaN goes by l */
@@ -1147,6 +1157,99 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 /* ---- the join ----------------------------------------------------------------- */
 
+/* Rows of a tree's results that are not finite, once more: the products with V take weights of 0 for the
+ * keys that a row does not see, and 0 times what lies there may be NaN.  By the block that has heads h0 to
+ * h1 of a token: columns where a hidden value is not finite are summed again over what the token sees, for
+ * the heads whose sum ml.y is not -1, against the maximum and sum of the row, which V does not reach.
+ * Other columns are what the definition gives.  Rare, and slow, since it reads a row's keys again: a value
+ * that is not finite in each of 8 trees of 40 tokens over 8000 keys makes the call take 3.6 ms (78 us), of 2
+ * over 106000 keys 22.5 ms (190 us).  Where all is finite, knowing so costs 16 trees behind two prompts
+ * 0.8 us of 82. */
+template <int D>
+__device__ __noinline__ void redo_rows(const Args &a, int tok, int kvh, int h0, int h1, const float2 *ml) {
+  constexpr int N = D / 32, C = D / 8; /* columns a lane, 16-byte pieces of a row */
+  __shared__ uint4 s_q[8][C], s_k[32][C + 1], s_v[32][C];
+  __shared__ bool s_seen[32], s_again[D];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int b = tok;
+  if (a.off) { /* the last sequence that begins at or before it */
+    int hi = a.n_seqs - 1;
+    for (b = 0; b < hi;) {
+      const int m = (b + hi + 1) >> 1;
+      if (__ldcg(a.off + m) <= tok)
+        b = m;
+      else
+        hi = m - 1;
+    }
+  }
+  const int first = a.off ? __ldcg(a.off + b) : b, end = a.off ? __ldcg(a.off + b + 1) : b + 1;
+  const int len = __ldcg(a.lens + b), base = len - (end - first), limit = len - (end - tok) + 1;
+  auto sees = [&](int key) -> bool {
+    if (key < base || key >= limit) return key < limit;
+    const int u = key - base;
+    return __ldcg(a.tree + (size_t)tok * a.tree_words + (u >> 5)) >> (u & 31) & 1;
+  };
+  auto row_of = [&](int key) -> long long { /* in the pools, -1 for a page that is out of range */
+    const int page = __ldcg(a.tables + (size_t)b * a.max_pages + key / a.P);
+    if ((unsigned)page >= (unsigned)a.num_pages) return -1;
+    return (((long long)page * a.Hkv + kvh) * a.P + key % a.P) * D;
+  };
+  bool again = false;
+  if (tid < D) {
+    for (int key = max(base, 0); key < len; ++key) {
+      const long long at = sees(key) ? -1 : row_of(key);
+      if (at >= 0) again |= (__ldcg((const unsigned short *)a.v_pool + at + tid) & 0x7f80) == 0x7f80;
+    }
+    s_again[tid] = again;
+  }
+  if (!__syncthreads_or(again)) return;
+  for (int hg0 = h0; hg0 < h1; hg0 += 8) {
+    const int hg = hg0 + warp, hq = kvh * a.G + hg;
+    const bool mine = hg < h1 && ml[hg - h0].y >= 0.0f;
+    if (!__syncthreads_or(mine)) continue;
+    const float M = mine ? ml[hg - h0].x : -INFINITY;
+    if (mine && lane < C) s_q[warp][lane] = __ldcg((const uint4 *)(a.q + tok * a.q_stride + hq * D) + lane);
+    float o[N] = {};
+    for (int key0 = 0; key0 < limit; key0 += 32) {
+      __syncthreads();
+      for (int i = tid; i < 32 * C; i += 256) {
+        const int j = i / C, c = i % C, key = key0 + j;
+        const long long at = key < limit && sees(key) ? row_of(key) : -1;
+        s_k[j][c] = at < 0 ? make_uint4(0, 0, 0, 0) : __ldcg((const uint4 *)(a.k_pool + at) + c);
+        s_v[j][c] = at < 0 ? make_uint4(0, 0, 0, 0) : __ldcg((const uint4 *)(a.v_pool + at) + c);
+        if (c == 0) s_seen[j] = at >= 0;
+      }
+      __syncthreads();
+      if (M == -INFINITY) continue;
+      float x = 0.0f;
+#pragma unroll 4
+      for (int c = 0; c < C; ++c) {
+        const uint4 q = s_q[warp][c], k = s_k[lane][c];
+        const uint32_t qs[4] = {q.x, q.y, q.z, q.w}, ks[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x = fmaf(__uint_as_float(qs[i] << 16), __uint_as_float(ks[i] << 16), x);
+          x = fmaf(__uint_as_float(qs[i] & 0xffff0000u), __uint_as_float(ks[i] & 0xffff0000u), x);
+        }
+      }
+      const float p = s_seen[lane] ? exp2_approx(fmaf(x, a.scale_log2, -M)) : 0.0f;
+#pragma unroll 4
+      for (int j = 0; j < 32; ++j) {
+        const float w = __shfl_sync(0xffffffffu, p, j);
+        const unsigned short *v = (const unsigned short *)s_v[j] + lane * N;
+#pragma unroll
+        for (int k = 0; k < N; ++k) o[k] = fmaf(w, __uint_as_float((uint32_t)v[k] << 16), o[k]);
+      }
+    }
+    if (!mine) continue;
+    const float l = ml[hg - h0].y, inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __nv_bfloat16 *dst = a.out + ((size_t)tok * a.Hq + hq) * D + lane * N;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (s_again[lane * N + k]) dst[k] = __float2bfloat16_rn(o[k] * inv);
+  }
+}
+
 /* M = max m_i, out = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i over a row's pieces.  A
  * block has a token and kv head, or some heads of its group (`blocks` blocks, a cluster,
  * share it) where there are too few for all SMs; its warps take the heads, several a head
@@ -1155,9 +1258,11 @@ __global__ void __launch_bounds__(kThreads, 1)
  * 32 pieces' maxima and four pieces' sums are in flight together (with eight, and 80
  * registers, fewer blocks fit an SM: 64 samples of one prompt 42 us, so 38); where blocks are
  * MANY, more of them an SM instead. */
-template <int D, bool MANY>
+template <int D, bool MANY, bool TREE>
 __global__ void __launch_bounds__(256, MANY ? 7 : 4) attn_merge(const __grid_constant__ Args a, int n_cta, int blocks) {
   __shared__ float sums[8][D];
+  __shared__ float2 odd_ml[TREE ? 64 : 1]; /* of heads whose results are not finite: for redo_rows */
+  bool any_odd = false;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int unit = blockIdx.x / blocks, rank = blockIdx.x - unit * blocks, units = a.n_tokens * a.Hkv;
   const int tok = unit / a.Hkv, kvh = unit - tok * a.Hkv;
@@ -1171,9 +1276,20 @@ __global__ void __launch_bounds__(256, MANY ? 7 : 4) attn_merge(const __grid_con
   if (blocks > 1)
     asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
   if (rank == 0 && threadIdx.x < 2) a.where[threadIdx.x * units + unit] = make_int4(0, 0, 0, 0);
-  if (wo.x == 1) return; /* written by attn_tiles */
-  const int n_shared = ws.x ? ws.x - 1 : 0, n = n_shared + (wo.x ? wo.x - 1 : 0);
   const int heads = (a.G + blocks - 1) / blocks, h0 = rank * heads, h1 = min(a.G, h0 + heads);
+  if (wo.x == 1) { /* written by attn_tiles */
+    if (TREE) {
+      const int hg = h0 + threadIdx.x;
+      bool odd = false;
+      if (hg < h1) {
+        odd_ml[threadIdx.x] = a.part_ml[(size_t)(a.n_tokens + tok) * a.Hq + kvh * a.G + hg];
+        odd = odd_ml[threadIdx.x].y >= 0.0f;
+      }
+      if (__syncthreads_or(odd)) redo_rows<D>(a, tok, kvh, h0, h1, odd_ml);
+    }
+    return;
+  }
+  const int n_shared = ws.x ? ws.x - 1 : 0, n = n_shared + (wo.x ? wo.x - 1 : 0);
   int split = 8; /* warps a head */
   while (split > 1 && 8 / split < heads) split >>= 1;
   const int part = warp % split, at_once = 8 / split;
@@ -1247,7 +1363,16 @@ __global__ void __launch_bounds__(256, MANY ? 7 : 4) attn_merge(const __grid_con
     }
     if (a.lse && lane == 0)
       a.lse[orow] = l == 0.0f ? -INFINITY : (M + log2f(l)) * 0.69314718055994531f;
+    if (TREE) {
+      float odd = 0.0f; /* NaN if a column is not finite; where the sum is NaN, so is the row */
+#pragma unroll
+      for (int k = 0; k < N; ++k) odd = fmaf(o[k], 0.0f, odd);
+      const bool again = __any_sync(0xffffffffu, odd != odd) && l == l;
+      if (lane == 0) odd_ml[hg - h0] = make_float2(M, again ? l : -1.0f);
+      any_odd |= again;
+    }
   }
+  if (TREE && __syncthreads_or(any_odd)) redo_rows<D>(a, tok, kvh, h0, h1, odd_ml);
 }
 
 /* Makes `dev` current for a scope. */
@@ -1275,7 +1400,8 @@ bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
 
 struct mk_attn {
   mk_attn_desc d{};
-  std::vector<CUtensorMap> maps; /* K and V of each layer */
+  std::vector<CUtensorMap> maps;    /* K and V of each layer */
+  std::vector<const void *> pools; /* the same */
   float scale_log2 = 0.0f;
   int box_rows = 0;
   cudaStream_t stream = nullptr;
@@ -1323,9 +1449,9 @@ cudaError_t launch(const mk_attn *at, int layer, const CUtensorMap &qmap, const 
   cfg.gridDim = dim3((unsigned)a.n_tokens * a.Hkv * blocks);
   cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return a.n_tokens * a.Hkv >= 16 * at->n_sm
-             ? cudaLaunchKernelEx(&cfg, attn_merge<D, true>, a, at->n_sm, blocks)
-             : cudaLaunchKernelEx(&cfg, attn_merge<D, false>, a, at->n_sm, blocks);
+  const bool many = a.n_tokens * a.Hkv >= 16 * at->n_sm;
+  return a.tree ? cudaLaunchKernelEx(&cfg, many ? attn_merge<D, true, true> : attn_merge<D, false, true>, a, at->n_sm, blocks)
+                : cudaLaunchKernelEx(&cfg, many ? attn_merge<D, true, false> : attn_merge<D, false, false>, a, at->n_sm, blocks);
 }
 
 }  // namespace
@@ -1372,6 +1498,10 @@ mk_status mk_attn_create(const mk_attn_desc *d, void *stream, mk_attn **out) {
   mk_status st = MK_OK;
   try {
     at->maps.resize(2 * (size_t)d->n_layers);
+    for (int l = 0; l < d->n_layers; ++l) {
+      at->pools.push_back(d->k_caches[l]);
+      at->pools.push_back(d->v_caches[l]);
+    }
     for (int l = 0; l < d->n_layers && st == MK_OK; ++l) {
       st = mk_encode_rows_map(d, d->k_caches[l], at->box_rows, &at->maps[2 * l]);
       if (st == MK_OK) st = mk_encode_rows_map(d, d->v_caches[l], at->box_rows, &at->maps[2 * l + 1]);
@@ -1478,6 +1608,10 @@ static mk_status attend(mk_attn *at, int32_t layer, const mk_attn_batch *b, cons
   a.tree = tree;
   a.tree_words = tree_words;
   a.max_query = tree ? 32 * tree_words : INT32_MAX;
+  a.q = (const __nv_bfloat16 *)q;
+  a.q_stride = q_token_stride;
+  a.k_pool = (const __nv_bfloat16 *)at->pools[2 * layer];
+  a.v_pool = (const __nv_bfloat16 *)at->pools[2 * layer + 1];
   a.TB = kTile / a.G;
   a.inv_g = (65536 + a.G - 1) / a.G;
   a.inv_p = ((1ull << 38) + a.P - 1) / a.P;

@@ -174,6 +174,64 @@ def test_what_lies_behind_a_length_does_not_matter():
     c.check(want=want)
 
 
+def hiding(rng, T):
+    """Any bits, and tokens that none sees."""
+    m = np.tril(rng.random((T, T)) < 0.7)
+    m[:, rng.random(T) < 0.3] = 0
+    return m
+
+
+SPOILT = [([(0, [(90, 40), (33, 33), (300, 129), (20, 1)])], heads) for heads in HEADS] + [
+    ([(304, [(90, 40), (33, 33), (200, 129), (1, 1)]), (0, [(700, 5)])], (32, 4, 128)),   # behind shared pages
+    ([(0, [(9000, 50)]), (2000, [(50, 20), (40, 20)])], (16, 2, 64)),                     # cut over the SMs
+    ([(0, [(400, 150), (700, 170)])], (8, 8, 32)),                                        # many blocks of the join
+    ([(0, [(12, 12), (150, 150), (4, 9), (0, 3), (16, 16)])], (4, 2, 64))]                # no context, no place
+
+
+@gpu
+@pytest.mark.parametrize("groups, heads", SPOILT)
+def test_what_lies_at_hidden_tokens_does_not_matter(groups, heads):
+    """K and V of tokens that no row sees are infinite or NaN, in some columns or all."""
+    c = Tree(groups, heads, bits=hiding, words=6, seed=5)
+    want, rng, n = c.exact(), np.random.default_rng(6), 0
+    for b, (L, T) in enumerate(zip(c.lens, c.T)):
+        for u in range(T):
+            place = L - T + u
+            if place < 0 or c.seen[b][:, u].any():
+                continue
+            page, slot, n = c.rows[b][place // 16], place % 16, n + 1
+            c.k[page, :, slot] = float(rng.choice([np.nan, np.inf]))
+            columns = rng.random(c.D) < rng.choice([0.05, 0.5, 1.0])
+            c.v[page, :, slot, c.t.from_numpy(columns)] = float(rng.choice([np.nan, np.inf, -np.inf]))
+    assert n > 0
+    c.check(want=want)
+    first, again = c.run(), c.run()
+    assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
+@gpu
+@pytest.mark.parametrize("groups, heads", SPOILT[1:5] + SPOILT[6:9])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_spoilt_token_stays_in_its_branch(groups, heads, bad):
+    """A column of V of one drafted token in three: rows that see it have no number there, all else is as before."""
+    c = Tree(groups, heads, seed=7)
+    want, (out, lse) = c.exact(), c.run()
+    spoilt, column = np.zeros(out.shape[0], bool), c.D // 3
+    for b, (L, T) in enumerate(zip(c.lens, c.T)):
+        for u in range(1, T, 3):
+            place = L - T + u
+            c.v[c.rows[b][place // 16], :, place % 16, column] = bad
+            spoilt[c.off[b]:c.off[b + 1]] |= c.seen[b][:, u].astype(bool)
+    assert spoilt.any() and not spoilt.all()
+    got, got_lse = c.run()
+    assert np.array_equal(got_lse, lse)
+    rest = np.arange(c.D) != column
+    assert np.array_equal(got[..., rest], out[..., rest])
+    assert not np.isfinite(got[spoilt][..., column]).any()
+    got[spoilt, :, column] = out[spoilt, :, column]
+    c.check(got=(got, got_lse), want=want)
+
+
 @gpu
 def test_rising_scores_among_the_tokens():
     """The last keys, which the tree hides from most rows, have the largest scores."""
