@@ -193,9 +193,9 @@ mk_status mk_prefix_attention(mk_attn *attn, int32_t layer, const mk_attn_batch 
  * behind the context in the cache) token t sees those at places u <= t whose bit is set in
  * its row, bit u % 32 of word u / 32 (itself among them only if its bit is set), and every
  * key before them.  K and V of drafted tokens need not be finite: what lies at those that a token
- * does not see has no part in its result (where V is not finite there, a call takes milliseconds).  tree: DEVICE [n_tokens][tree_words], 4-byte aligned, not over out or lse;
- * T is at most 32 * tree_words (longer: nothing is written, MK_ERR_INVALID_ARG from
- * mk_attn_sync).  Parents come before their children, so a row is its parent's row and its own
+ * does not see has no part in its result (where V is not finite there, a call takes milliseconds).
+ * tree: DEVICE [n_tokens][tree_words], 4-byte aligned, not over out or lse; T is at most
+ * 32 * tree_words (longer: nothing is written, MK_ERR_INVALID_ARG from mk_attn_sync).  Parents come before their children, so a row is its parent's row and its own
  * bit.  A token that sees no key at all gets zeros and lse -inf. */
 mk_status mk_tree_attention(mk_attn *attn, int32_t layer, const mk_attn_batch *batch,
                             const uint32_t *tree, int32_t tree_words, const void *q,

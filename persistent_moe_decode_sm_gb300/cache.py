@@ -416,7 +416,7 @@ class KvAppend:
 
     def batch(self, page_tables, seq_lens, q_offsets=None, n_tokens: int = None):
         """The batch of a call, as PrefixAttention.batch makes it (whose batches run() takes
-        too).  n_tokens: rows of q, k and v; needed with q_offsets."""
+        too), of at most 1024 sequences.  n_tokens: rows of q, k and v; needed with q_offsets."""
         if q_offsets is not None and n_tokens is None:
             raise ValueError("n_tokens is needed with q_offsets")
         return _batch(self.device, page_tables, seq_lens, q_offsets, None, None, n_tokens)

@@ -31,7 +31,8 @@ constexpr int kBlocks = 3;     /* of an SM */
 /* Which of a head's dims a lane holds, as four pairs (a, b): PAIR_HALVES 4 dims and the 4 half the
  * rotary part further on (rotary_dim a multiple of 8), PAIR_NEIGHBOURS 8 dims in a row, PAIR_ANY any
  * halves, to which 8 dims in a row are exchanged through shared memory (25400 tokens with 100 of 128
- * dims turned and norms: 130 us, loaded and stored one by one 319).  No angle is turned twice. */
+ * dims turned and norms: 130 us, loaded and stored one by one 319).  A lane turns an angle once for all
+ * heads of its part of a token. */
 enum { PAIR_HALVES = 0, PAIR_NEIGHBOURS = 1, PAIR_ANY = 2 };
 
 struct Args {

@@ -11,9 +11,9 @@
  * What bounds it: 384 bf16 rows of 152064 (350 MB) take 107 us, 3.3 TB/s, of which the copy with
  * the greedy token is 69 (writes to DRAM, about 70 instructions for 128 tokens, a row's beginning and
  * end) and masks, words and their rules the rest.  With rules in line, where a token's word
- * is met, most warps run them for one lane: 140 us; but a list takes its time to make, so where rows
- * are few they are in line: 8 rows 13.4 us (15.7), one row of 32000 5.5 (8.0), both a chain of loads,
- * each for the next: arguments, histories, the rows' best.
+ * is met, most warps run them for one lane: 132 us; but a list takes its time to make, so where rows
+ * are few they are in line: 8 rows 13.4 us (with a list 15.7), one row of 32000 5.5 (8.0), both a chain of
+ * loads, each for the next: arguments, histories, the rows' best.
  */
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -687,9 +687,10 @@ static mk_status apply(mk_rules *m, const mk_rules_batch *b, const void *logits,
   a.best = (unsigned long long *)(m->ws + 64);
   a.done = (int32_t *)(m->ws + 32);
   /* slices: no larger than the vocabulary takes, and as large as leaves an SM two items (8 rows of
-   * 152064: 13.6 us, with one 18.3, with four 16.6; large slices cost a row less: 384 rows 117 us, with
-   * 4096 tokens a slice 158).  Lists where rows are many, but not in the smallest slices, where most
-   * tokens have a word (2048 rows of 1000 47 us, with a list 69). */
+   * 152064: 13.4 us, with one 16.2, with four 15.6; large slices cost a row less: 384 rows 107 us, with
+   * 4096 tokens a slice 144).  Lists where rows are many, but not in the smallest slices, where most
+   * tokens have a word (2048 rows of 1000: a list cost the kernel half as much again when it was one of
+   * 47 us, 69; now 35). */
   a.slice = kSlice;
   while (a.slice > kLeast && a.slice / 2 >= V) a.slice /= 2;
   auto items = [&] { return (V + a.slice - 1) / a.slice * b->n_rows; };
